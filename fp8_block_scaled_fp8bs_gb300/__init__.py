@@ -16,17 +16,26 @@ Raw entry points (same names and arguments as the C functions; pointers are ints
     fp8bs_gemm_grouped(a, a_s, b, b_s, c, row_offsets, groups, N, K, scale_fmt, stream)
     fp8bs_device_error(clear=True, stream=0) -> int
     fp8bs_probe_wait_timeout(timeout_ns, stream)
+    fp8bs_qk_norm_rope(args, stream), fp8bs_paged_attention(args, stream),
+    fp8bs_moe_route / _experts / _layer: argument structures QkNormRopeArgs, PagedAttentionArgs,
+        MoeRouting with the C structures' fields
 Tensor conveniences (PyTorch CUDA tensors; outputs allocated with torch):
     act_quant(x, scale_fmt="fp32") -> (y, s)      ("DeepSeek-V3 Administrator & Developer
     weight_dequant(w, s) -> y                        Guide", §8.5.1, §8.5.2, §8.5.3)
     fp8_gemm(a, a_s, b, b_s, scale_fmt="fp32") -> c
     fp8_gemm_grouped(a, a_s, b, b_s, row_offsets, scale_fmt="fp32") -> c
+    qk_norm_rope(q, k, cos, sin, positions, ...) -> q (and k, or the keys and values in a PagedCache)
+    paged_attention(q, cache, page_table, q_start, kv_len, ...) -> out (and lse)
+    moe_route(x, router_w, ...) -> (weights, ids)      ("DeepSeek-V3 Administrator & Developer
+    moe_experts(x, weights, ids, w13, s13, w2, s2) -> y    Guide", §6.4)
+    moe_layer(x, router_w, w13, s13, w2, s2, ...) -> y
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+from typing import Any, NamedTuple
 
 BLOCK = 128
 SCALE_FP32 = 0
@@ -34,23 +43,54 @@ SCALE_UE8M0 = 1
 STATUS = {0: "ok", 1: "invalid argument", 2: "pointer not aligned",
           3: "unsupported device (needs sm_103)", 4: "CUDA error"}
 DEVERR_SCALE_NOT_POW2 = 0x10
+DEVERR_INDEX = 0x20
 DEVERR_PROBE = 0x100
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8bs.so")
 GEMM_WEIGHTS_CONSTANT = 0x1
 GEMM_QUANT_IN_KERNEL = 0x2
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+MOE_MAX_TOKENS = 64
 KERNEL_SWAPPED, KERNEL_PROMOTED, KERNEL_BLOCK_SCALED, KERNEL_BLOCK_SCALED_PAIR = 0, 1, 2, 3
 EXPORTS = ("fp8bs_act_quant", "fp8bs_weight_dequant", "fp8bs_gemm", "fp8bs_gemm_ex",
            "fp8bs_gemm_ws", "fp8bs_gemm_workspace_size", "fp8bs_gemm_plan", "fp8bs_gemm_config",
            "fp8bs_gemm_noalloc",
            "fp8bs_act_quant_gemm", "fp8bs_linear_bf16",
            "fp8bs_gemm_grouped",
+           "fp8bs_qk_norm_rope", "fp8bs_paged_attention", "fp8bs_paged_attention_workspace_size",
+           "fp8bs_moe_route", "fp8bs_moe_experts", "fp8bs_moe_layer", "fp8bs_moe_workspace_size",
            "fp8bs_status_string", "fp8bs_device_error", "fp8bs_probe_wait_timeout",
            "fp8bs_probe_occupy")
 
 _lock = threading.Lock()
 _lib = None
+
+
+def _structure(name, doc, **fields):
+    return type(name, (ctypes.Structure,), {"_fields_": list(fields.items()), "__doc__": doc,
+                                            "__slots__": ()})
+
+
+_vp, _i64 = ctypes.c_void_p, ctypes.c_int64
+KvCache = _structure(
+    "KvCache", "fp8bs_kv_cache", k=_vp, v=_vp, pages=_i64, page_size=_i64, heads=_i64, dk=_i64,
+    dv=_i64, k_page_stride=_i64, k_slot_stride=_i64, k_head_stride=_i64, v_page_stride=_i64,
+    v_slot_stride=_i64, v_head_stride=_i64)
+QkNormRopeArgs = _structure(
+    "QkNormRopeArgs", "fp8bs_qk_norm_rope_args", q=_vp, k=_vp, v=_vp, q_token_stride=_i64,
+    q_head_stride=_i64, k_token_stride=_i64, k_head_stride=_i64, v_token_stride=_i64,
+    v_head_stride=_i64, q_weight=_vp, k_weight=_vp, cos=_vp, sin=_vp, positions=_vp, slots=_vp,
+    q_out=_vp, cache=KvCache, T=_i64, q_heads=_i64, max_positions=_i64, rot_start=_i64,
+    rot_dim=_i64, interleaved=ctypes.c_int, eps=ctypes.c_float)
+PagedAttentionArgs = _structure(
+    "PagedAttentionArgs", "fp8bs_paged_attention_args", q=_vp, q_token_stride=_i64,
+    q_head_stride=_i64, cache=KvCache, page_table=_vp, table_stride=_i64, q_start=_vp, kv_len=_vp,
+    out=_vp, lse=_vp, B=_i64, T=_i64, q_heads=_i64, max_q_len=_i64, max_kv_len=_i64, window=_i64,
+    causal=ctypes.c_int, scale=ctypes.c_float, workspace=_vp, workspace_bytes=ctypes.c_size_t)
+MoeRouting = _structure(
+    "MoeRouting", "fp8bs_moe_routing", router_w=_vp, bias=_vp, top_k=_i64, groups=_i64,
+    topk_groups=_i64, score=ctypes.c_int, normalise=ctypes.c_int, route_scale=ctypes.c_float)
 
 
 class Fp8bsError(RuntimeError):
@@ -89,6 +129,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                            vp]
         lib.fp8bs_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(ctypes.c_int64),
                                            i64, i64, i64, i32, vp]
+        lib.fp8bs_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeArgs), vp]
+        lib.fp8bs_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), vp]
+        lib.fp8bs_paged_attention_workspace_size.argtypes = [ctypes.POINTER(PagedAttentionArgs),
+                                                             ctypes.POINTER(ctypes.c_size_t)]
+        lib.fp8bs_moe_workspace_size.argtypes = [i64] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.fp8bs_moe_route.argtypes = [vp, ctypes.POINTER(MoeRouting), vp, vp, i64, i64, i64, vp]
+        lib.fp8bs_moe_experts.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, ctypes.c_size_t, vp]
+        lib.fp8bs_moe_layer.argtypes = [vp, ctypes.POINTER(MoeRouting)] + [vp] * 5 + [i64] * 4 + \
+            [i32, vp, ctypes.c_size_t, vp]
         lib.fp8bs_status_string.argtypes = [i32]
         lib.fp8bs_status_string.restype = ctypes.c_char_p
         lib.fp8bs_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), i32, vp]
@@ -177,6 +226,47 @@ def fp8bs_gemm_grouped(a, a_s, b, b_s, c, row_offsets, groups, N, K, scale_fmt=S
     offs = (ctypes.c_int64 * (int(groups) + 1))(*[int(x) for x in row_offsets])
     _check("fp8bs_gemm_grouped", load().fp8bs_gemm_grouped(a, a_s, b, b_s, c, offs, groups, N, K,
                                                            scale_fmt, stream))
+
+
+def fp8bs_qk_norm_rope(args: QkNormRopeArgs, stream=0) -> None:
+    _check("fp8bs_qk_norm_rope", load().fp8bs_qk_norm_rope(ctypes.byref(args), stream))
+
+
+def fp8bs_paged_attention(args: PagedAttentionArgs, stream=0) -> None:
+    _check("fp8bs_paged_attention", load().fp8bs_paged_attention(ctypes.byref(args), stream))
+
+
+def fp8bs_paged_attention_workspace_size(args: PagedAttentionArgs) -> int:
+    out = ctypes.c_size_t(0)
+    _check("fp8bs_paged_attention_workspace_size",
+           load().fp8bs_paged_attention_workspace_size(ctypes.byref(args), ctypes.byref(out)))
+    return out.value
+
+
+def fp8bs_moe_workspace_size(T, D, I, experts, top_k) -> int:
+    out = ctypes.c_size_t(0)
+    _check("fp8bs_moe_workspace_size",
+           load().fp8bs_moe_workspace_size(T, D, I, experts, top_k, ctypes.byref(out)))
+    return out.value
+
+
+def fp8bs_moe_route(x, routing: MoeRouting, weights, ids, T, D, experts, stream=0) -> None:
+    _check("fp8bs_moe_route", load().fp8bs_moe_route(x, ctypes.byref(routing), weights, ids, T, D,
+                                                     experts, stream))
+
+
+def fp8bs_moe_experts(x, weights, ids, w13, s13, w2, s2, y, T, D, I, experts, top_k,
+                      scale_fmt=SCALE_FP32, workspace=0, workspace_bytes=0, stream=0) -> None:
+    _check("fp8bs_moe_experts", load().fp8bs_moe_experts(
+        x, weights, ids, w13, s13, w2, s2, y, T, D, I, experts, top_k, scale_fmt, workspace,
+        workspace_bytes, stream))
+
+
+def fp8bs_moe_layer(x, routing: MoeRouting, w13, s13, w2, s2, y, T, D, I, experts,
+                    scale_fmt=SCALE_FP32, workspace=0, workspace_bytes=0, stream=0) -> None:
+    _check("fp8bs_moe_layer", load().fp8bs_moe_layer(
+        x, ctypes.byref(routing), w13, s13, w2, s2, y, T, D, I, experts, scale_fmt, workspace,
+        workspace_bytes, stream))
 
 
 def fp8bs_device_error(clear: bool = True, stream=0) -> int:
@@ -381,3 +471,237 @@ def fp8_gemm_grouped(a, a_s, b, b_s, row_offsets, scale_fmt="fp32", out=None):
     fp8bs_gemm_grouped(a.data_ptr(), a_s.data_ptr(), b.data_ptr(), b_s.data_ptr(), c.data_ptr(),
                        offs, G, N, K, _fmt(scale_fmt), _stream())
     return c
+
+
+# ------------------------------------------------------------- around the products of a decoder layer
+
+class PagedCache(NamedTuple):
+    """Keys [pages, page_size, heads, dk] and values [pages, page_size, heads, dv], bf16 CUDA tensors
+    (views of another order too: rows contiguous, the other strides multiples of 8)."""
+    k: Any
+    v: Any
+
+
+def _rows(t, ndim, name):
+    """A bf16 CUDA tensor whose last axis is contiguous and whose rows start on 16-byte boundaries."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {ndim}-D tensor with contiguous rows")
+    return t
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, like the other tensors")
+
+
+def _kv_cache(cache):
+    k, v = _rows(cache.k, 4, "cache.k"), _rows(cache.v, 4, "cache.v")
+    if k.shape[:3] != v.shape[:3]:
+        raise ValueError("cache.k and cache.v must have the same pages, page size and heads")
+    _same_device(k.device, **{"cache.v": v})
+    pages, page_size, heads, dk = k.shape
+    return KvCache(k.data_ptr(), v.data_ptr(), pages, page_size, heads, dk, v.shape[3],
+                   *k.stride()[:3], *v.stride()[:3])
+
+
+def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, rot_start=0,
+                 interleaved=False, cache=None, v=None, slots=None, out=None):
+    """RMS norm per head (where a weight is given) and rotation of q bf16 [T, Hq, D] and k bf16
+    [T, Hk, D] by positions int32 [T]; cos, sin fp32 [max_positions, R/2] rotate the channels
+    rot_start .. rot_start+R-1. With a PagedCache, the keys and v bf16 [T, Hk, Dv] go to its slots
+    int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k)."""
+    import torch
+    _rows(q, 3, "q")
+    _rows(k, 3, "k")
+    T, hq, d = q.shape
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and channels")
+    _require(cos, torch.float32, 2, "cos")
+    _require(sin, torch.float32, 2, "sin")
+    if cos.shape != sin.shape:
+        raise ValueError("cos and sin must have the same shape")
+    _require(positions, torch.int32, 1, "positions")
+    if positions.shape[0] != T:
+        raise ValueError("positions must have one entry per token")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _require(w, torch.bfloat16, 1, name)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must have {d} entries")
+    _same_device(q.device, k=k, v=v, cos=cos, sin=sin, positions=positions, q_weight=q_weight,
+                 k_weight=k_weight, slots=slots)
+    k_out = None
+    if cache is None:
+        if v is not None or slots is not None:
+            raise ValueError("v and slots need a cache")
+        k_out = torch.empty((T, k.shape[1], d), dtype=torch.bfloat16, device=q.device)
+        kv = KvCache(k_out.data_ptr(), None, min(T, 1), max(T, 1), k.shape[1], d, d, 0, *k_out.stride()[:2],
+                     0, 0, 0)
+    else:
+        if v is None or slots is None:
+            raise ValueError("a cache needs v and slots")
+        kv = _kv_cache(cache)
+        _same_device(q.device, cache=cache.k)
+        _rows(v, 3, "v")
+        if (kv.heads, kv.dk) != tuple(k.shape[1:]) or tuple(v.shape) != (T, kv.heads, kv.dv):
+            raise ValueError("k and v do not match the cache's heads and channels")
+        _require(slots, torch.int64, 1, "slots")
+        if slots.shape[0] != T:
+            raise ValueError("slots must have one entry per token")
+    q_out = _output(out, (T, hq, d), q.device)
+    fp8bs_qk_norm_rope(QkNormRopeArgs(
+        q.data_ptr(), k.data_ptr(), v.data_ptr() if v is not None else None, *q.stride()[:2],
+        *k.stride()[:2], *(v.stride()[:2] if v is not None else (0, 0)),
+        q_weight.data_ptr() if q_weight is not None else None,
+        k_weight.data_ptr() if k_weight is not None else None, cos.data_ptr(), sin.data_ptr(),
+        positions.data_ptr(), slots.data_ptr() if slots is not None else None, q_out.data_ptr(), kv,
+        T, hq, cos.shape[0], rot_start, 2 * cos.shape[1], int(interleaved), eps), _stream())
+    return q_out if cache is not None else (q_out, k_out)
+
+
+_scratch = {}
+
+
+def _scratch_bytes(device, nbytes):
+    """Device memory of at least nbytes for one call on the current stream: one buffer per device and
+    stream, kept and grown (calls on one stream follow one another, so they can share it)."""
+    import torch
+    if nbytes == 0:
+        return None
+    key = (device.index, _stream())
+    buf = _scratch.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _scratch[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return buf
+
+
+def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=True, window=0,
+                    max_q_len=None, max_kv_len=None, out=None, return_lse=False):
+    """Attention of the new tokens q bf16 [T, Hq, Dk] of B sequences (sequence b: rows q_start[b] ..
+    q_start[b+1]-1) over a PagedCache that holds their kv_len[b] keys, their own included, in the
+    pages page_table[b] (int32 [B, n]) -> out bf16 [T, Hq, Dv] (and lse fp32 [T, Hq]). q_start int32
+    [B+1] and kv_len int32 [B] are on the GPU; max_q_len and max_kv_len bound them for the host
+    (default: T, and what the table can hold; tighter is faster). window > 0: each query sees that
+    many keys at most, its own the last."""
+    import torch
+    _rows(q, 3, "q")
+    kv = _kv_cache(cache)
+    T, hq, dk = q.shape
+    if dk != kv.dk or hq % kv.heads:
+        raise ValueError("q does not match the cache's channels, or its heads are no multiple")
+    _require(page_table, torch.int32, 2, "page_table")
+    _require(q_start, torch.int32, 1, "q_start")
+    _require(kv_len, torch.int32, 1, "kv_len")
+    B, n = page_table.shape
+    if kv_len.shape[0] != B or q_start.shape[0] != B + 1:
+        raise ValueError("page_table, q_start and kv_len must agree on the number of sequences")
+    _same_device(q.device, cache=cache.k, page_table=page_table, q_start=q_start, kv_len=kv_len)
+    o = _output(out, (T, hq, kv.dv), q.device)
+    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    args = PagedAttentionArgs(
+        q.data_ptr(), *q.stride()[:2], kv, page_table.data_ptr(), n, q_start.data_ptr(),
+        kv_len.data_ptr(), o.data_ptr(), lse.data_ptr() if return_lse else None, B, T, hq,
+        T if max_q_len is None else max_q_len,
+        n * kv.page_size if max_kv_len is None else max_kv_len, window, int(causal),
+        dk ** -0.5 if scale is None else scale, None, 0)
+    ws = _scratch_bytes(q.device, fp8bs_paged_attention_workspace_size(args))
+    if ws is not None:
+        args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
+    fp8bs_paged_attention(args, _stream())
+    return (o, lse) if return_lse else o
+
+
+def _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale):
+    import torch
+    _require(x, torch.bfloat16, 2, "x")
+    _require(router_w, torch.bfloat16, 2, "router_w")
+    if router_w.shape[1] != x.shape[1]:
+        raise ValueError("router_w must have x's channels")
+    if bias is not None:
+        _require(bias, torch.float32, 1, "bias")
+        if bias.shape[0] != router_w.shape[0]:
+            raise ValueError("bias must have one entry per expert")
+    _same_device(x.device, router_w=router_w, bias=bias)
+    if score not in ("sigmoid", "softmax"):
+        raise ValueError(f"unknown score {score!r}")
+    if normalise is None:
+        normalise = score == "sigmoid"
+    return MoeRouting(router_w.data_ptr(), bias.data_ptr() if bias is not None else None, top_k,
+                      groups, topk_groups, SCORE_SIGMOID if score == "sigmoid" else SCORE_SOFTMAX,
+                      int(normalise), route_scale)
+
+
+def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_groups=1, normalise=None,
+              route_scale=1.0):
+    """Expert choice for x bf16 [T, D] with router_w bf16 [E, D] -> (weights fp32 [T, top_k], ids
+    int32 [T, top_k], best first). bias fp32 [E] shifts the choice only; groups/topk_groups limit it
+    to the best groups of experts; normalise (default: for sigmoid scores) makes a token's weights
+    sum to route_scale."""
+    import torch
+    routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
+    T, D = x.shape
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+    fp8bs_moe_route(x.data_ptr(), routing, weights.data_ptr(), ids.data_ptr(), T, D,
+                    router_w.shape[0], _stream())
+    return weights, ids
+
+
+def _expert_shapes(x, w13, s13, w2, s2):
+    import torch
+    _require(x, torch.bfloat16, 2, "x")
+    _require(w13, torch.float8_e4m3fn, 3, "w13")
+    _require(w2, torch.float8_e4m3fn, 3, "w2")
+    _require(s13, torch.float32, 3, "s13")
+    _require(s2, torch.float32, 3, "s2")
+    T, D = x.shape
+    E, _, inter = w2.shape
+    if tuple(w13.shape) != (E, 2 * inter, D) or w2.shape[1] != D or \
+            tuple(s13.shape) != (E, 2 * inter // BLOCK, D // BLOCK) or \
+            tuple(s2.shape) != (E, D // BLOCK, inter // BLOCK):
+        raise ValueError("expert weight or scale shapes do not match")
+    _same_device(x.device, w13=w13, s13=s13, w2=w2, s2=s2)
+    return T, D, inter, E
+
+
+def moe_experts(x, weights, ids, w13, s13, w2, s2, scale_fmt="fp32", out=None):
+    """The experts of a mixture-of-experts layer for x bf16 [T <= 64, D]: w13 e4m3 [E, 2I, D] (gate
+    rows, then up rows), w2 e4m3 [E, D, I], scales per 128 x 128 block; ids int32 [T, top_k] (-1: none)
+    and weights fp32 [T, top_k] as moe_route gives them -> y bf16 [T, D]."""
+    import torch
+    T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
+    _require(weights, torch.float32, 2, "weights")
+    _require(ids, torch.int32, 2, "ids")
+    if weights.shape != ids.shape or ids.shape[0] != T:
+        raise ValueError("weights and ids must be [T, top_k]")
+    _same_device(x.device, weights=weights, ids=ids)
+    y = _output(out, (T, D), x.device)
+    k = ids.shape[1]
+    ws = _scratch_bytes(x.device, fp8bs_moe_workspace_size(T, D, inter, E, k))
+    fp8bs_moe_experts(x.data_ptr(), weights.data_ptr(), ids.data_ptr(), w13.data_ptr(),
+                      s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr(), T, D, inter, E, k,
+                      _fmt(scale_fmt), ws.data_ptr() if ws is not None else None,
+                      ws.numel() if ws is not None else 0, _stream())
+    return y
+
+
+def moe_layer(x, router_w, w13, s13, w2, s2, top_k, bias=None, score="sigmoid", groups=1,
+              topk_groups=1, normalise=None, route_scale=1.0, scale_fmt="fp32", out=None):
+    """A whole mixture-of-experts layer for x bf16 [T <= 64, D]: moe_route, then moe_experts."""
+    routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
+    T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
+    if router_w.shape[0] != E:
+        raise ValueError("router_w must have one row per expert")
+    y = _output(out, (T, D), x.device)
+    ws = _scratch_bytes(x.device, fp8bs_moe_workspace_size(T, D, inter, E, top_k))
+    fp8bs_moe_layer(x.data_ptr(), routing, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
+                    s2.data_ptr(), y.data_ptr(), T, D, inter, E, _fmt(scale_fmt),
+                    ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+                    _stream())
+    return y

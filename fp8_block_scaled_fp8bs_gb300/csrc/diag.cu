@@ -44,15 +44,19 @@ cudaError_t launch_probe_wait(uint64_t timeout_ns, cudaStream_t stream) {
 }
 
 cudaError_t read_device_error(unsigned int* out, bool clear, cudaStream_t stream) {
-    unsigned int words[5] = {0, 0, 0, 0, 0};
+    unsigned int words[8] = {};
     cudaError_t e = read_tu_error(&words[0], clear, stream);
     if (e == cudaSuccess) e = read_error_tn(&words[1], clear, stream);
     if (e == cudaSuccess) e = read_error_bs(&words[2], clear, stream);
     if (e == cudaSuccess) e = read_error_swapab(&words[3], clear, stream);
     if (e == cudaSuccess) e = read_error_linear(&words[4], clear, stream);
+    if (e == cudaSuccess) e = read_error_norm_rope(&words[5], clear, stream);
+    if (e == cudaSuccess) e = read_error_attention(&words[6], clear, stream);
+    if (e == cudaSuccess) e = read_error_moe(&words[7], clear, stream);
     if (e == cudaSuccess && clear) e = reset_static_workspace_counters(stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    *out = words[0] | words[1] | words[2] | words[3] | words[4];
+    *out = 0;
+    for (unsigned int w : words) *out |= w;
     return e;
 }
 

@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/fp8bs.h"
+
 namespace fp8bs {
 
 // Launch with programmatic stream serialisation (see grid_dependency_wait in ptx.cuh): the
@@ -181,6 +183,45 @@ cudaError_t launch_linear_bf16_swap(const CUtensorMap& tmW, const CUtensorMap& t
                                     const float* w_s, void* y, int M, int N, int K, int MT,
                                     int weights_constant, cudaStream_t stream);
 
+// Query/key norm, rotation and cache write (fp8bs_qk_norm_rope); T >= 1.
+cudaError_t launch_qk_norm_rope(const fp8bs_qk_norm_rope_args& a, cudaStream_t stream);
+
+// Attention over a paged cache (fp8bs_paged_attention). attention_plan cuts the work from the
+// sizes in `a` alone; attention_workspace gives the bytes that the plan needs.
+struct AttentionPlan {
+    int pieces;        // pieces of the key axis (1: no join)
+    int piece_len;     // keys per piece, a multiple of the key tile
+};
+AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms);
+size_t attention_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan);
+cudaError_t launch_paged_attention(const fp8bs_paged_attention_args& a, const AttentionPlan& plan,
+                                   cudaStream_t stream);
+
+// Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
+constexpr int kMoeMaxTokens = 64;
+struct MoeWorkspace {
+    size_t x8, xs, h8, hs, h32, weights, ids, total;
+};
+MoeWorkspace moe_workspace(int64_t T, int64_t D, int64_t I, int64_t E, int64_t top_k);
+// The router (routing non-null: weights, ids written) and the quantisation of x (x8 non-null: its
+// codes [T, D], and scales xs [D/128][kMoeMaxTokens], token fastest), together or alone.
+cudaError_t launch_moe_prepare(const void* x, const fp8bs_moe_routing* routing, float* weights,
+                               int32_t* ids, void* x8, float* xs, int64_t T, int64_t D, int64_t E,
+                               bool ue8m0, cudaStream_t stream);
+struct MoeArgs {
+    const float* weights;
+    const int32_t* ids;
+    const void* w13;
+    const float* s13;
+    const void* w2;
+    const float* s2;
+    void* y;
+    uint8_t* ws;
+    int T, D, I, E, top_k;
+    bool ue8m0;
+};
+cudaError_t launch_moe_experts(const MoeArgs& a, const MoeWorkspace& w, cudaStream_t stream);
+
 // Diagnostic kernel: one wait on a barrier nothing signals (see fp8bs_probe_wait_timeout).
 cudaError_t launch_probe_wait(uint64_t timeout_ns, cudaStream_t stream);
 
@@ -195,5 +236,8 @@ cudaError_t read_error_tn(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_bs(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_swapab(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_linear(unsigned int* out, bool clear, cudaStream_t stream);
+cudaError_t read_error_norm_rope(unsigned int* out, bool clear, cudaStream_t stream);
+cudaError_t read_error_attention(unsigned int* out, bool clear, cudaStream_t stream);
+cudaError_t read_error_moe(unsigned int* out, bool clear, cudaStream_t stream);
 
 }  // namespace fp8bs

@@ -1,0 +1,258 @@
+// moe_prepare.cu -- the router of a mixture-of-experts layer and the quantisation of its input, one
+// kernel ("DeepSeek-V3 Administrator & Developer Guide", §6.4 MoE expert routing and §8.5.1
+// act_quant_kernel).
+//
+// A cluster of 8 CTAs serves PREP_TOKENS tokens: CTA r takes every 8th part of the channels, quantises
+// them and computes its part of all logits, so that the router's weights (2 bytes x experts x D, from
+// L2 after their first reader) are spread over 8 SMs even for a single token. The partial logits meet
+// in CTA 0 through distributed shared memory, are added in rank order (the same bits every time) and
+// one warp per token makes the choice. Bound by latency: a single token's 32 x 7168 router is
+// 0.46 MB.
+#include "gemm_common.cuh"
+#include "quant_math.cuh"
+
+namespace fp8bs {
+
+namespace {
+
+constexpr int PREP_CLUSTER = 8;
+constexpr int PREP_TOKENS = 4;
+constexpr int PREP_THREADS = 256;
+constexpr int PREP_EXPERTS = 4;     // experts a warp computes at once
+constexpr int kMaxExperts = 512;
+
+struct PrepArgs {
+    const uint4* x;
+    const uint4* router_w;    // null: no routing
+    const float* bias;
+    float* weights;
+    int32_t* ids;
+    uint4* x8;                // null: no quantisation
+    float* xs;
+    int64_t T;
+    int D, E, top_k, groups, topk_groups, score, normalise, ue8m0;
+    float route_scale;
+};
+
+// Larger key = better choice: the value's order, then the lower index. Never 0.
+__device__ __forceinline__ uint64_t choice_key(float v, int e) {
+    const uint32_t b = __float_as_uint(v);
+    const uint32_t ord = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    return (static_cast<uint64_t>(ord) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e));
+}
+
+// The choice for one token by one warp: logits in sc[0..E) (shared memory), replaced by scores.
+__device__ __forceinline__ void choose(const PrepArgs& a, float* sc, float* ch, int64_t t, int lane) {
+    const int E = a.E;
+    if (a.score == FP8BS_SCORE_SIGMOID) {
+        for (int e = lane; e < E; e += 32) sc[e] = 1.0f / (1.0f + expf(-sc[e]));
+    } else {
+        float m = -INFINITY;
+        for (int e = lane; e < E; e += 32) m = fmaxf(m, sc[e]);
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+        float sum = 0.0f;
+        for (int e = lane; e < E; e += 32) {
+            sc[e] = expf(sc[e] - m);
+            sum += sc[e];
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        for (int e = lane; e < E; e += 32) sc[e] /= sum;
+    }
+    for (int e = lane; e < E; e += 32) ch[e] = a.bias ? sc[e] + a.bias[e] : sc[e];
+    __syncwarp();
+    if (a.groups > 1) {
+        const int per = E / a.groups;
+        float rank = -INFINITY;
+        if (lane < a.groups) {
+            float m1 = -INFINITY, m2 = -INFINITY;
+            for (int i = 0; i < per; ++i) {
+                const float v = ch[lane * per + i];
+                if (v > m1) {
+                    m2 = m1;
+                    m1 = v;
+                } else if (v > m2) {
+                    m2 = v;
+                }
+            }
+            rank = a.bias && per > 1 ? m1 + m2 : m1;
+        }
+        const uint64_t key = choice_key(rank, lane);
+        int better = 0;
+        for (int g = 0; g < a.groups; ++g)
+            better += __shfl_sync(0xffffffffu, key, g) > key ? 1 : 0;
+        const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && better < a.topk_groups);
+        __syncwarp();
+        for (int e = lane; e < E; e += 32)
+            if (!((keep >> (e / per)) & 1u)) ch[e] = -INFINITY;
+        __syncwarp();
+    }
+    // top_k rounds of a warp-wide maximum; lane l holds experts l, l + 32, ...
+    unsigned taken = 0;
+    float total = 0.0f;
+    int mine = 0;               // lane j keeps the j-th choice
+    for (int j = 0; j < a.top_k; ++j) {
+        uint64_t best = 0;
+        for (int i = 0, e = lane; e < E; ++i, e += 32)
+            if (!((taken >> i) & 1u)) {
+                const uint64_t key = choice_key(ch[e], e);
+                best = key > best ? key : best;
+            }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) {
+            const uint64_t o = __shfl_xor_sync(0xffffffffu, best, i);
+            best = o > best ? o : best;
+        }
+        const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+        if ((e & 31) == lane) taken |= 1u << (e >> 5);
+        total += sc[e];
+        if (lane == j) mine = e;
+    }
+    if (lane < a.top_k) {
+        a.ids[t * a.top_k + lane] = mine;
+        const float w = a.normalise ? sc[mine] / total : sc[mine];
+        a.weights[t * a.top_k + lane] = w * a.route_scale;
+    }
+}
+
+__global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArgs a) {
+    extern __shared__ __align__(16) uint8_t prep_smem[];
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x / PREP_CLUSTER) * PREP_TOKENS;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(PREP_TOKENS), a.T - t0));
+    const int nb = a.D / BK;
+    const int b0 = rank * nb / PREP_CLUSTER;
+    const int nbr = (rank + 1) * nb / PREP_CLUSTER - b0;      // this CTA's blocks of 128 channels
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    // [tokens][blocks of this CTA, most of any][16 pieces of 16 bytes]
+    const int nb_max = (nb + PREP_CLUSTER - 1) / PREP_CLUSTER;
+    uint4* sx = reinterpret_cast<uint4*>(prep_smem);
+    const int pitch = nb_max * (BK / 8);
+    float* part = reinterpret_cast<float*>(sx + PREP_TOKENS * pitch);  // CTA 0: [rank][tokens][E]
+    float* choice = part + PREP_CLUSTER * PREP_TOKENS * a.E;             // CTA 0: [tokens][E]
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // x into shared memory and its codes and scales out: 8 lanes per block of 128.
+    const int tasks = PREP_TOKENS * nbr;
+    for (int base = warp * 4; base < tasks; base += PREP_THREADS / 8) {
+        const int task = base + (lane >> 3);
+        const int tok = nbr ? task / nbr : 0;
+        const int blk = task - tok * nbr;
+        const int chunk = lane & 7;
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+        const bool live = task < tasks && tok < nt;
+        if (live) {
+            const uint4* src = a.x + ((t0 + tok) * a.D + (b0 + blk) * BK) / 8 + 2 * chunk;
+            v0 = __ldg(src);
+            v1 = __ldg(src + 1);
+        }
+        if (task < tasks) {
+            sx[tok * pitch + blk * (BK / 8) + 2 * chunk] = v0;
+            sx[tok * pitch + blk * (BK / 8) + 2 * chunk + 1] = v1;
+        }
+        if (a.x8) {
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            uint32_t out[4];
+            const float sc = a.ue8m0 ? quant_block16<true>(w, out) : quant_block16<false>(w, out);
+            if (live) {
+                a.x8[((t0 + tok) * a.D + (b0 + blk) * BK) / 16 + chunk] =
+                    make_uint4(out[0], out[1], out[2], out[3]);
+                if (chunk == 0) a.xs[(b0 + blk) * kMoeMaxTokens + t0 + tok] = sc;
+            }
+        }
+    }
+    if (!a.router_w) return;       // uniform over the grid
+    cluster_sync();                // x staged; every CTA of the cluster is running
+    // Partial logits: a warp takes PREP_EXPERTS experts at a time, its lanes the channels.
+    const uint32_t part0 = mapa_shared(smem_addr(part), 0);
+    const int pieces = nbr * (BK / 8);
+    for (int e0 = warp * PREP_EXPERTS; e0 < a.E; e0 += PREP_THREADS / 32 * PREP_EXPERTS) {
+        float acc[PREP_EXPERTS][PREP_TOKENS] = {};
+        const uint4* wrow[PREP_EXPERTS];
+#pragma unroll
+        for (int i = 0; i < PREP_EXPERTS; ++i)
+            wrow[i] = a.router_w +
+                      (static_cast<int64_t>(min(e0 + i, a.E - 1)) * a.D + b0 * BK) / 8;
+#pragma unroll 2
+        for (int c = lane; c < pieces; c += 32) {
+            uint4 wv[PREP_EXPERTS];
+#pragma unroll
+            for (int i = 0; i < PREP_EXPERTS; ++i) wv[i] = __ldg(wrow[i] + c);
+#pragma unroll
+            for (int k = 0; k < PREP_TOKENS; ++k) {
+                const uint4 xv = sx[k * pitch + c];
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                for (int i = 0; i < PREP_EXPERTS; ++i) {
+                    const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i][k] = fmaf(bf16_lo(xw[j]), bf16_lo(ww[j]), acc[i][k]);
+                        acc[i][k] = fmaf(bf16_hi(xw[j]), bf16_hi(ww[j]), acc[i][k]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PREP_EXPERTS; ++i)
+#pragma unroll
+            for (int k = 0; k < PREP_TOKENS; ++k) {
+                float v = acc[i][k];
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+                if (lane == 0 && e0 + i < a.E)
+                    st_shared_cluster_f32(
+                        part0 + static_cast<uint32_t>(((rank * PREP_TOKENS + k) * a.E + e0 + i) * 4),
+                        v);
+            }
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    for (int i = threadIdx.x; i < PREP_TOKENS * a.E; i += PREP_THREADS) {
+        float v = part[i];
+        for (int r = 1; r < PREP_CLUSTER; ++r) v += part[r * PREP_TOKENS * a.E + i];
+        part[i] = v;               // slot of rank 0: logits [tokens][E]
+    }
+    __syncthreads();
+    if (warp < nt) choose(a, part + warp * a.E, choice + warp * a.E, t0 + warp, lane);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_prepare(const void* x, const fp8bs_moe_routing* routing, float* weights,
+                               int32_t* ids, void* x8, float* xs, int64_t T, int64_t D, int64_t E,
+                               bool ue8m0, cudaStream_t stream) {
+    PrepArgs a = {};
+    a.x = static_cast<const uint4*>(x);
+    a.x8 = static_cast<uint4*>(x8);
+    a.xs = xs;
+    a.T = T;
+    a.D = static_cast<int>(D);
+    a.E = static_cast<int>(E);
+    a.ue8m0 = ue8m0 ? 1 : 0;
+    if (routing) {
+        a.router_w = static_cast<const uint4*>(routing->router_w);
+        a.bias = routing->bias;
+        a.weights = weights;
+        a.ids = ids;
+        a.top_k = static_cast<int>(routing->top_k);
+        a.groups = static_cast<int>(routing->groups);
+        a.topk_groups = static_cast<int>(routing->topk_groups);
+        a.score = routing->score;
+        a.normalise = routing->normalise;
+        a.route_scale = routing->route_scale;
+    }
+    const int64_t nb_max = (D / BK + PREP_CLUSTER - 1) / PREP_CLUSTER;
+    int64_t smem = PREP_TOKENS * nb_max * BK * 2;
+    if (routing) smem += (PREP_CLUSTER + 1) * PREP_TOKENS * E * 4;
+    cudaError_t e = set_smem(moe_prepare_kernel, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t clusters = (T + PREP_TOKENS - 1) / PREP_TOKENS;
+    return launch_pdl_cluster(moe_prepare_kernel, dim3(static_cast<unsigned>(clusters * PREP_CLUSTER)),
+                              PREP_THREADS, smem, stream, PREP_CLUSTER, false, a);
+}
+
+}  // namespace fp8bs

@@ -323,6 +323,181 @@ FP8BS_API int fp8bs_gemm_grouped(const void* a, const float* a_s, const void* b,
                                  void* c, const int64_t* row_offsets, int64_t groups, int64_t N,
                                  int64_t K, int scale_fmt, void* stream);
 
+/* --------------------------------------------------------------------------------------------
+ * What stands between the FP8 products of a decoder layer when it serves tokens: norms and
+ * rotation of the queries and keys, attention over a paged cache, and a mixture-of-experts
+ * layer for a few tokens. Strides below are in elements.
+ */
+
+/*
+ * A paged key/value cache in bf16: slot o of page p holds the keys of one token, `heads` rows of
+ * `dk` channels, at k + p*k_page_stride + o*k_slot_stride + h*k_head_stride, and its values, rows
+ * of `dv` channels, likewise. Rows are contiguous; the strides are multiples of 8 (so that every
+ * row starts on a 16-byte boundary) and otherwise free: page-slot-head and page-head-slot orders
+ * both work.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t pages, page_size, heads, dk, dv;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+} fp8bs_kv_cache;
+
+/*
+ * fp8bs_qk_norm_rope -- per head: RMS norm of queries and keys, rotation by position, and the
+ * keys and values written into a cache, in one pass over the projections' output.
+ *
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        (skipped where the weight is NULL)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)       for the pairs of channels of
+ *                                                  [rot_start, rot_start + rot_dim)
+ *
+ * in binary32, rounded to bf16 once. Pair i is channels (2i, 2i+1) of that range if `interleaved`,
+ * else (i, i + rot_dim/2); its cosine and sine are cos[p][i], sin[p][i] at p = positions[t].
+ *
+ *   q [T, q_heads, dk], k [T, cache.heads, dk], v [T, cache.heads, dv]: bf16, rows contiguous and
+ *       16-byte aligned, token and head strides multiples of 8. v may be NULL: no values are
+ *       written (cache.v is not looked at).
+ *   q_weight, k_weight: bf16 [dk] or NULL.    cos, sin: fp32 [max_positions, rot_dim/2].
+ *   positions: int32 [T].  A position outside [0, max_positions) sets FP8BS_DEVERR_INDEX; that
+ *       token's q_out is zero and its slot is not written.
+ *   slots: int64 [T], the slot (page * page_size + offset) of each token, or NULL: token t goes to
+ *       slot t. A negative slot is a padding token (its q_out is written, its keys and values are
+ *       not); one past the cache sets FP8BS_DEVERR_INDEX and is not written. No slot may occur
+ *       twice.
+ *   q_out: bf16 [T, q_heads, dk] contiguous, 16-byte aligned.
+ *   dk, dv: multiples of 16, 16 .. 256 (dv is taken as dk without v). rot_start: a multiple of 8;
+ *   rot_dim: a multiple of 16, 0 for no rotation; rot_start + rot_dim <= dk.
+ */
+typedef struct {
+    const void *q, *k, *v;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+        v_head_stride;
+    const void *q_weight, *k_weight;
+    const float *cos, *sin;
+    const int32_t* positions;
+    const int64_t* slots;
+    void* q_out;
+    fp8bs_kv_cache cache;
+    int64_t T, q_heads, max_positions, rot_start, rot_dim;
+    int interleaved;
+    float eps;
+} fp8bs_qk_norm_rope_args;
+
+FP8BS_API int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stream);
+
+/*
+ * fp8bs_paged_attention -- attention of new tokens over a paged cache that already holds their own
+ * keys and values. Sequence b has the query tokens q_start[b] .. q_start[b+1]-1 (n of them, 0 or
+ * more; single tokens and long chunks may be mixed) and kv_len[b] = L keys, key j in slot
+ * j % page_size of page page_table[b*table_stride + j / page_size]. Its i-th query attends the keys
+ *
+ *   j <= L - n + i           (causal; all j < L otherwise)
+ *   j >  L - n + i - window  (window > 0)
+ *
+ *   o = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j)
+ *
+ * with query head h reading key head h / (q_heads / cache.heads). Scores, softmax sums and o are
+ * held in binary32, the probabilities rounded to bf16 for their product with v, o to bf16 at the
+ * end. A query with no key gets o = 0, lse = -inf. Keys at and past L and pages past them are
+ * never used, whatever they hold (their table entries are not read); values of keys below L have
+ * to be finite. A page id outside the cache sets FP8BS_DEVERR_INDEX and reads as zeros.
+ *
+ *   q [T, q_heads, dk] bf16, rows contiguous and 16-byte aligned, strides multiples of 8.
+ *   out bf16 [T, q_heads, dv] contiguous, 16-byte aligned. lse fp32 [T, q_heads] or NULL.
+ *   page_table int32 [B, table_stride]; q_start int32 [B+1], q_start[0] = 0, q_start[B] = T;
+ *   kv_len int32 [B].   (dk, dv): (64, 64), (128, 128) or (192, 128).
+ *   max_q_len, max_kv_len: bounds on n and L that the caller knows on the host; they steer how
+ *       the work is cut (max_kv_len at most 2^31 - 1024). A sequence past them sets
+ *       FP8BS_DEVERR_INDEX and leaves its rows of out undefined.
+ *   workspace: fp8bs_paged_attention_workspace_size(args) bytes, 16-byte aligned (0 bytes: NULL).
+ *       Its contents need not be kept between calls; calls that may overlap need their own.
+ *
+ * The key axis is cut into pieces of equal length when the rows alone would not fill the GPU; the
+ * pieces' results are joined in key order. The cut depends only on the sizes in `args`, so equal
+ * calls give equal bits.
+ */
+typedef struct {
+    const void* q;
+    int64_t q_token_stride, q_head_stride;
+    fp8bs_kv_cache cache;
+    const int32_t* page_table;
+    int64_t table_stride;
+    const int32_t *q_start, *kv_len;
+    void* out;
+    float* lse;
+    int64_t B, T, q_heads, max_q_len, max_kv_len, window;
+    int causal;
+    float scale;
+    void* workspace;
+    size_t workspace_bytes;
+} fp8bs_paged_attention_args;
+
+FP8BS_API int fp8bs_paged_attention_workspace_size(const fp8bs_paged_attention_args* args,
+                                                   size_t* bytes);
+FP8BS_API int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, void* stream);
+
+/*
+ * Expert choice of a mixture-of-experts layer ("DeepSeek-V3 Administrator & Developer Guide", §6.4
+ * MoE expert routing): logits = x . router_w^T in binary32, score = sigmoid(logits) or
+ * softmax(logits); for the choice (not the weight) bias is added to the scores. With groups > 1 the
+ * experts stand in `groups` equal runs; only the topk_groups runs with the highest rank stay (rank:
+ * the sum of the run's two highest biased scores, or without a bias its highest score). The top_k
+ * highest are chosen, in falling order. Ties go to the lowest index. weight = score, divided by the
+ * sum of the token's chosen scores if `normalise`, times route_scale.
+ */
+typedef enum { FP8BS_SCORE_SIGMOID = 0, FP8BS_SCORE_SOFTMAX = 1 } fp8bs_score;
+
+typedef struct {
+    const void* router_w;  /* bf16 [experts, D], 16-byte aligned */
+    const float* bias;     /* fp32 [experts] or NULL */
+    int64_t top_k, groups, topk_groups;
+    int score;             /* fp8bs_score */
+    int normalise;
+    float route_scale;
+} fp8bs_moe_routing;
+
+/*
+ * fp8bs_moe_route -- the choice alone. x bf16 [T, D], 16-byte aligned; weights fp32 [T, top_k], ids
+ * int32 [T, top_k]. D a multiple of 128 up to 16384, experts 1 .. 512, top_k 1 .. 32, groups
+ * 1 .. 32 dividing experts, top_k <= topk_groups * (experts / groups), any T.
+ */
+FP8BS_API int fp8bs_moe_route(const void* x, const fp8bs_moe_routing* routing, float* weights,
+                              int32_t* ids, int64_t T, int64_t D, int64_t experts, void* stream);
+
+/*
+ * fp8bs_moe_experts -- the experts of a mixture-of-experts layer for a few tokens (T <= 64):
+ *
+ *   y[t] = sum_j weights[t,j] * W2_e . q(silu(Wg_e . q(x[t])) * (Wu_e . q(x[t]))),  e = ids[t,j]
+ *
+ * where q is act_quant (scale_fmt) and every product is fp8_gemm's: e4m3 codes, one scale per 1 x 128
+ * block of activations and 128 x 128 block of weights, accumulated in binary32. Nothing between the
+ * codes of x and y is rounded to bf16: the gate, the sum over experts and the weights stay in
+ * binary32, y is rounded once. An id of -1 chooses nothing; another id outside [0, experts) sets
+ * FP8BS_DEVERR_INDEX and chooses nothing. A token without experts gets y = 0.
+ *
+ *   x bf16 [T, D]; ids int32 [T, top_k]; weights fp32 [T, top_k]; y bf16 [T, D].
+ *   w13 e4m3 [experts, 2 I, D]: the I gate rows, then the I up rows; s13 fp32 [experts, 2I/128, D/128].
+ *   w2  e4m3 [experts, D, I]; s2 fp32 [experts, D/128, I/128].
+ *   x, y, w13, w2, workspace 16-byte aligned, the rest 4-byte. T 0 .. 64, top_k 1 .. 32, experts
+ *   1 .. 512; D, I multiples of 128, 128 .. 16384.
+ *   workspace: fp8bs_moe_workspace_size bytes; contents need not be kept between calls.
+ */
+FP8BS_API int fp8bs_moe_workspace_size(int64_t T, int64_t D, int64_t I, int64_t experts,
+                                       int64_t top_k, size_t* bytes);
+FP8BS_API int fp8bs_moe_experts(const void* x, const float* weights, const int32_t* ids,
+                                const void* w13, const float* s13, const void* w2, const float* s2,
+                                void* y, int64_t T, int64_t D, int64_t I, int64_t experts,
+                                int64_t top_k, int scale_fmt, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* fp8bs_moe_layer -- fp8bs_moe_route, then fp8bs_moe_experts on its choice, as one call: the router's
+ * kernel also quantises x, and two kernels compute the experts. */
+FP8BS_API int fp8bs_moe_layer(const void* x, const fp8bs_moe_routing* routing, const void* w13,
+                              const float* s13, const void* w2, const float* s2, void* y, int64_t T,
+                              int64_t D, int64_t I, int64_t experts, int scale_fmt, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Human-readable name of an fp8bs_status value (a static string; never NULL). */
 FP8BS_API const char* fp8bs_status_string(int status);
 
@@ -342,6 +517,7 @@ FP8BS_API int fp8bs_device_error(unsigned int* out, int clear, void* stream);
 #define FP8BS_DEVERR_EPILOGUE_WAIT 0x4u  /* promotion/epilogue waited too long for TMEM */
 #define FP8BS_DEVERR_DRAIN_WAIT 0x8u     /* in-flight copies did not drain after an abort */
 #define FP8BS_DEVERR_SCALE_NOT_POW2 0x10u /* FP8BS_SCALE_UE8M0 GEMM met a scale that is not 2^e */
+#define FP8BS_DEVERR_INDEX 0x20u         /* a position, slot, page, expert or length out of range */
 #define FP8BS_DEVERR_PROBE 0x100u        /* set by fp8bs_probe_wait_timeout */
 
 /*
