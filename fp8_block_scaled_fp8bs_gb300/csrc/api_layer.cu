@@ -25,6 +25,13 @@ int check_cache(const fp8bs_kv_cache& c, bool values) {
     if (values &&
         (!stride_ok(c.v_page_stride) || !stride_ok(c.v_slot_stride) || !stride_ok(c.v_head_stride)))
         return FP8BS_ERR_INVALID_ARG;
+    // rows must not lie on one another
+    if ((c.pages > 1 && c.k_page_stride < 8) || (c.page_size > 1 && c.k_slot_stride < 8) ||
+        (c.heads > 1 && c.k_head_stride < 8))
+        return FP8BS_ERR_INVALID_ARG;
+    if (values && ((c.pages > 1 && c.v_page_stride < 8) || (c.page_size > 1 && c.v_slot_stride < 8) ||
+                   (c.heads > 1 && c.v_head_stride < 8)))
+        return FP8BS_ERR_INVALID_ARG;
     if (c.pages > 0 && (!c.k || (values && !c.v))) return FP8BS_ERR_INVALID_ARG;
     if (!aligned16(c.k) || (values && !aligned16(c.v))) return FP8BS_ERR_MISALIGNED;
     return FP8BS_OK;
@@ -66,6 +73,27 @@ extern "C" int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* str
 
 namespace {
 
+// A cache's keys or values as {channels, heads, slots, pages}, boxes of {64 channels, 1, slots, 1},
+// 128-byte swizzle. Out-of-range pages read as zero.
+bool make_cache_map(CUtensorMap* map, const void* base, const fp8bs_kv_cache& c, int64_t d,
+                    int64_t head_stride, int64_t slot_stride, int64_t page_stride, int box_slots) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    // (the stride of an axis of length one is never used, but has to be a valid one)
+    auto bytes = [&](int64_t stride, int64_t n) {
+        return static_cast<cuuint64_t>(n > 1 ? stride * 2 : d * 2);
+    };
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.heads),
+                                static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[3] = {bytes(head_stride, c.heads), bytes(slot_stride, c.page_size),
+                                   bytes(page_stride, c.pages)};
+    const cuuint32_t box[4] = {64u, 1u, static_cast<cuuint32_t>(box_slots), 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Everything but the pointers of a paged_attention call.
 int check_attention_sizes(const fp8bs_paged_attention_args& a) {
     const int64_t dk = a.cache.dk, dv = a.cache.dv;
@@ -74,7 +102,7 @@ int check_attention_sizes(const fp8bs_paged_attention_args& a) {
     if (a.B < 0 || a.B >= (1 << 20) || a.T < 0 || a.T >= kMaxDim || a.q_heads < 1 ||
         a.q_heads >= (1 << 16) || a.cache.heads < 1 || a.q_heads % a.cache.heads || a.window < 0 ||
         a.max_q_len < 0 || a.max_q_len > a.T || a.max_kv_len < 0 || a.max_kv_len >= kMaxDim - 1024 ||
-        a.table_stride < 0 || a.T * a.q_heads >= kMaxDim * 64)
+        a.table_stride < 0 || a.T * (a.q_heads / a.cache.heads) >= kMaxDim)
         return FP8BS_ERR_INVALID_ARG;
     if (a.T > 0 && (a.B < 1 || a.max_q_len < 1)) return FP8BS_ERR_INVALID_ARG;
     if (a.cache.page_size < 1 ||
@@ -104,7 +132,7 @@ extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, voi
     if (rc != FP8BS_OK) return rc;
     if (!stride_ok(a.q_token_stride) || !stride_ok(a.q_head_stride)) return FP8BS_ERR_INVALID_ARG;
     rc = check_cache(a.cache, true);
-    if (rc == FP8BS_ERR_INVALID_ARG) return rc;
+    if (rc == FP8BS_ERR_INVALID_ARG || a.cache.pages < 1) return FP8BS_ERR_INVALID_ARG;
     if (a.T == 0) return FP8BS_OK;
     if (!a.q || !a.q_start || !a.kv_len || !a.out || (a.max_kv_len > 0 && !a.page_table))
         return FP8BS_ERR_INVALID_ARG;
@@ -118,7 +146,14 @@ extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, voi
     const fp8bs::AttentionPlan plan = fp8bs::attention_plan(a, sms);
     const size_t need = fp8bs::attention_workspace(a, plan);
     if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return FP8BS_ERR_INVALID_ARG;
-    return status_of(fp8bs::launch_paged_attention(a, plan, static_cast<cudaStream_t>(stream)));
+    const int box_log2 = fp8bs::attention_box_log2(a.cache.page_size);
+    CUtensorMap tmK, tmV;
+    const fp8bs_kv_cache& c = a.cache;
+    if (!make_cache_map(&tmK, c.k, c, c.dk, c.k_head_stride, c.k_slot_stride, c.k_page_stride, 1 << box_log2) ||
+        !make_cache_map(&tmV, c.v, c, c.dv, c.v_head_stride, c.v_slot_stride, c.v_page_stride, 1 << box_log2))
+        return FP8BS_ERR_CUDA;
+    return status_of(fp8bs::launch_paged_attention(tmK, tmV, a, box_log2, plan,
+                                                   static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

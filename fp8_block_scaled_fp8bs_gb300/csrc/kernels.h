@@ -194,8 +194,12 @@ struct AttentionPlan {
 };
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms);
 size_t attention_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan);
-cudaError_t launch_paged_attention(const fp8bs_paged_attention_args& a, const AttentionPlan& plan,
-                                   cudaStream_t stream);
+// tmK, tmV: the cache as {channels, heads, slots, pages} with boxes {64, 1, 2^box_log2, 1} and
+// 128-byte swizzle.
+int attention_box_log2(int64_t page_size);
+cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                   const fp8bs_paged_attention_args& a, int box_log2,
+                                   const AttentionPlan& plan, cudaStream_t stream);
 
 // Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
 constexpr int kMoeMaxTokens = 64;
