@@ -574,9 +574,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[buf]);
             }
-            // (one query tile: its last two products may both be in flight, one phase each)
-            if (ok && NQ == 1 && nt > 1 && !warp_wait(&o_done[q], nt & 1)) ok = false;
-            if (ok && !warp_wait(&o_done[q], (nt - 1) & 1)) ok = false;
+            // every product of this query tile is done (o_done's parity would not tell: with two S
+            // buffers the last two products may complete before this warp looks)
+            if (ok && !warp_wait(&drain[q], 0)) ok = false;
             if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
             tc_fence_after();
             if (ok && !idle) {
