@@ -188,7 +188,7 @@ int check_experts(const void* x, const void* w13, const float* s13, const void* 
 
 int run_experts(const fp8bs::MoeWorkspace& ws, const float* weights, const int32_t* ids, const void* w13,
                 const float* s13, const void* w2, const float* s2, void* y, int64_t T, int64_t D,
-                int64_t I, int64_t E, int64_t top_k, int scale_fmt, void* workspace, void* stream) {
+                int64_t I, int64_t E, int64_t top_k, int scale_fmt, void* workspace, int sms, void* stream) {
     fp8bs::MoeArgs a = {};
     a.weights = weights;
     a.ids = ids;
@@ -204,7 +204,12 @@ int run_experts(const fp8bs::MoeWorkspace& ws, const float* weights, const int32
     a.E = static_cast<int>(E);
     a.top_k = static_cast<int>(top_k);
     a.ue8m0 = scale_fmt == FP8BS_SCALE_UE8M0;
-    return status_of(fp8bs::launch_moe_experts(a, ws, static_cast<cudaStream_t>(stream)));
+    fp8bs::MoeMaps m;
+    const int mt = fp8bs::moe_token_rows(T);
+    if (!make_map(&m.w13, w13, E * 2 * I, D, 128) || !make_map(&m.w2, w2, E * D, I, 128) ||
+        !make_map(&m.x8, a.ws + ws.x8, T, D, mt) || !make_map(&m.h8, a.ws + ws.h8, ws.active * T, I, mt))
+        return FP8BS_ERR_CUDA;
+    return status_of(fp8bs::launch_moe_experts(m, a, ws, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -254,7 +259,7 @@ extern "C" int fp8bs_moe_experts(const void* x, const float* weights, const int3
         scale_fmt == FP8BS_SCALE_UE8M0, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return status_of(e);
     return run_experts(ws, weights, ids, w13, s13, w2, s2, y, T, D, I, experts, top_k, scale_fmt, workspace,
-                       stream);
+                       sms, stream);
 }
 
 extern "C" int fp8bs_moe_layer(const void* x, const fp8bs_moe_routing* routing, const void* w13,
@@ -280,5 +285,5 @@ extern "C" int fp8bs_moe_layer(const void* x, const fp8bs_moe_routing* routing, 
         scale_fmt == FP8BS_SCALE_UE8M0, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return status_of(e);
     return run_experts(ws, weights, ids, w13, s13, w2, s2, y, T, D, I, experts, routing->top_k, scale_fmt,
-                       workspace, stream);
+                       workspace, sms, stream);
 }

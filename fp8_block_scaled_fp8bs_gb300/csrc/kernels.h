@@ -204,7 +204,8 @@ cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tm
 // Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
 constexpr int kMoeMaxTokens = 64;
 struct MoeWorkspace {
-    size_t x8, xs, h8, hs, h32, weights, ids, total;
+    size_t x8, xs, h8, hs, weights, ids, total;
+    int64_t active;   // most experts that can have tokens
 };
 MoeWorkspace moe_workspace(int64_t T, int64_t D, int64_t I, int64_t E, int64_t top_k);
 // The router (routing non-null: weights, ids written) and the quantisation of x (x8 non-null: its
@@ -224,7 +225,15 @@ struct MoeArgs {
     int T, D, I, E, top_k;
     bool ue8m0;
 };
-cudaError_t launch_moe_experts(const MoeArgs& a, const MoeWorkspace& w, cudaStream_t stream);
+// Rows of the token side of the MMAs (the boxes of x8 and h8).
+int moe_token_rows(int64_t T);
+// w13 [E*2I, D], w2 [E*D, I]: boxes {128, 128}; x8 [T, D], h8 [active*T, I]: boxes
+// {128, moe_token_rows(T)}.
+struct MoeMaps {
+    CUtensorMap w13, w2, x8, h8;
+};
+cudaError_t launch_moe_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspace& w, int num_sms,
+                               cudaStream_t stream);
 
 // Diagnostic kernel: one wait on a barrier nothing signals (see fp8bs_probe_wait_timeout).
 cudaError_t launch_probe_wait(uint64_t timeout_ns, cudaStream_t stream);

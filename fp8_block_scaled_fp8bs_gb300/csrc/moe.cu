@@ -1,9 +1,19 @@
-// moe.cu -- the experts of a mixture-of-experts layer for a few tokens (fp8bs_moe_experts):
-// gate and up products, silu(gate) * up, its quantisation, the down product and the weighted sum over
-// experts ("DeepSeek-V3 Administrator & Developer Guide", §6.4 MoE expert routing, §8.5.3
-// fp8_gemm_kernel for the products).
+// moe.cu -- the experts of a mixture-of-experts layer for a few tokens (fp8bs_moe_experts), two
+// kernels ("DeepSeek-V3 Administrator & Developer Guide", §6.4 MoE expert routing; the products as in
+// §8.5.3 fp8_gemm_kernel):
+//   moe_up_kernel    h = silu(Wg x) * (Wu x) of every active expert, quantised per 128 channels
+//   moe_down_kernel  y[t] = sum over active experts of weight[t, e] * W2 h, in binary32, bf16 once
 //
-// First form: one warp per row of the weights, on the CUDA cores.
+// Bound by the weights' bytes: 3 D I per active expert, read once, while the tokens (64 at most) are few.
+// So 128 rows of weights take the MMA's M side and all T tokens its N side, for every active expert:
+// the products of tokens that did not choose the expert cost the tensor core what nothing else needs
+// (128 x MT x 128 per 16 KB of weights), and the activations need no gather. The partial of each K block
+// is scaled and added to binary32 registers by the promotion warps, as in gemm_swapab.cu.
+//
+// The choices meet the products in the factors: the up kernel writes zero codes and a zero factor for a
+// token that did not choose the expert, and otherwise the factor (block scale of h) * (weight of the
+// expert), so that the down kernel's accumulators run over all experts without a break: one sum per output,
+// in expert and channel order, the same bits every time.
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
@@ -11,96 +21,577 @@ namespace fp8bs {
 
 namespace {
 
-__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float* f) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const __nv_fp8x2_storage_t p = static_cast<__nv_fp8x2_storage_t>((w >> (16 * h)) & 0xFFFFu);
-        const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(p, __NV_E4M3)));
-        f[2 * h] = v.x;
-        f[2 * h + 1] = v.y;
-    }
-}
+constexpr int MOE_PROMOTE_WARP0 = 2;                  // warps 2..5 promote (TMEM lanes warp % 4)
+constexpr int MOE_ISSUER2 = 6;
+constexpr int MOE_THREADS = 7 * 32;
+constexpr int MOE_NBUF = 4;                           // TMEM buffers (K blocks in flight)
+constexpr int kMaxExperts = 512;
 
-// Dot product over nkb K blocks: lane l takes 4 codes of each block. xs: stride between blocks' scales.
-__device__ __forceinline__ float dot_blocks(const uint8_t* w, const float* ws, const uint8_t* x,
-                                            const float* xs, int xs_stride, int nkb, int lane) {
-    float sum = 0.0f;
-    for (int kb = 0; kb < nkb; ++kb) {
-        float a[4], b[4];
-        unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(w + kb * BK + 4 * lane), a);
-        unpack_e4m3x4(*reinterpret_cast<const uint32_t*>(x + kb * BK + 4 * lane), b);
-        const float p = a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
-        sum = fmaf(p, ws[kb] * xs[kb * xs_stride], sum);
-    }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    return sum;
-}
+// Which experts have tokens, and which tokens: built by every CTA from the ids.
+struct Routing {
+    unsigned long long mask[kMaxExperts];             // bit t: token t chose the expert
+    uint16_t active[kMaxExperts];                     // the experts with tokens, in order
+    int n;
+};
 
-// h[slot][i], slot = t * top_k + j; grid (I / 8, E)
-__global__ void moe_up_kernel(const MoeArgs a, const uint8_t* x8, const float* xs, float* h) {
-    grid_dependency_wait();
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int e = blockIdx.y;
-    const int nkb = a.D / BK;
-    const uint8_t* w13 = static_cast<const uint8_t*>(a.w13) + static_cast<int64_t>(e) * 2 * a.I * a.D;
-    const float* s13 = a.s13 + static_cast<int64_t>(e) * (2 * a.I / BK) * nkb;
-    for (int s = 0; s < a.T * a.top_k; ++s) {
-        const int id = a.ids[s];
-        if ((id < -1 || id >= a.E) && lane == 0) record_error(FP8BS_DEVERR_INDEX);
-        if (id != e) continue;
-        const int t = s / a.top_k;
-        const float g = dot_blocks(w13 + static_cast<int64_t>(i) * a.D, s13 + (i / BK) * nkb,
-                                   x8 + static_cast<int64_t>(t) * a.D, xs + t, kMoeMaxTokens, nkb, lane);
-        const float u = dot_blocks(w13 + static_cast<int64_t>(a.I + i) * a.D,
-                                   s13 + ((a.I + i) / BK) * nkb, x8 + static_cast<int64_t>(t) * a.D,
-                                   xs + t, kMoeMaxTokens, nkb, lane);
-        if (lane == 0) h[static_cast<int64_t>(s) * a.I + i] = g / (1.0f + expf(-g)) * u;
-    }
-}
-
-// one warp per (slot, block of 128)
-__global__ void moe_quant_kernel(const MoeArgs a, const float* h, uint8_t* h8, float* hs) {
-    grid_dependency_wait();
-    const int s = blockIdx.y;
-    const int b = blockIdx.x;
-    const int lane = threadIdx.x;
-    if (a.ids[s] < 0 || a.ids[s] >= a.E) return;
-    const float4 v = *reinterpret_cast<const float4*>(h + static_cast<int64_t>(s) * a.I + b * BK + 4 * lane);
-    float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    float sc = __fdiv_rn(fmaxf(m, 1e-4f), 448.0f);
-    if (a.ue8m0) {
-        uint32_t bits = __float_as_uint(sc);
-        if (bits & 0x007FFFFFu) bits = (bits & 0xFF800000u) + 0x00800000u;
-        sc = __uint_as_float(bits);
-    }
-    const uint32_t lo = pack_e4m3x2(__fdiv_rn(v.x, sc), __fdiv_rn(v.y, sc));
-    const uint32_t hi = pack_e4m3x2(__fdiv_rn(v.z, sc), __fdiv_rn(v.w, sc));
-    *reinterpret_cast<uint32_t*>(h8 + static_cast<int64_t>(s) * a.I + b * BK + 4 * lane) = lo | (hi << 16);
-    if (lane == 0) hs[s * (a.I / BK) + b] = sc;
-}
-
-__global__ void moe_down_kernel(const MoeArgs a, const uint8_t* h8, const float* hs) {
-    grid_dependency_wait();
-    const int d = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.y;
-    const int nkb = a.I / BK;
-    float y = 0.0f;
-    for (int j = 0; j < a.top_k; ++j) {
-        const int s = t * a.top_k + j;
+// All threads of the CTA; ends with a block barrier.
+__device__ __forceinline__ void build_routing(Routing& r, const MoeArgs& a, bool report) {
+    for (int e = threadIdx.x; e < a.E; e += MOE_THREADS) r.mask[e] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < a.T * a.top_k; s += MOE_THREADS) {
         const int e = a.ids[s];
-        if (e < 0 || e >= a.E) continue;
-        const float v = dot_blocks(
-            static_cast<const uint8_t*>(a.w2) + (static_cast<int64_t>(e) * a.D + d) * a.I,
-            a.s2 + (static_cast<int64_t>(e) * (a.D / BK) + d / BK) * nkb,
-            h8 + static_cast<int64_t>(s) * a.I, hs + s * nkb, 1, nkb, lane);
-        y = fmaf(a.weights[s], v, y);
+        if (e >= 0 && e < a.E)
+            atomicOr(&r.mask[e], 1ull << (s / a.top_k));
+        else if (e != -1 && report)
+            record_error(FP8BS_DEVERR_INDEX);
     }
-    if (lane == 0) static_cast<__nv_bfloat16*>(a.y)[static_cast<int64_t>(t) * a.D + d] = __float2bfloat16_rn(y);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int n = 0;
+        for (int base = 0; base < a.E; base += 32) {
+            const bool on = base + lane < a.E && r.mask[base + lane] != 0;
+            const unsigned b = __ballot_sync(0xffffffffu, on);
+            if (on) r.active[n + __popc(b & ((1u << lane) - 1))] = static_cast<uint16_t>(base + lane);
+            n += __popc(b);
+        }
+        if (lane == 0) r.n = n;
+    }
+    __syncthreads();
+}
+
+// Barriers of a CTA.
+struct MoeBars {
+    uint64_t *full, *empty, *tfull, *tempty, *drain;
+};
+
+__device__ __forceinline__ MoeBars carve_bars(uint8_t* p, int stages) {
+    MoeBars b;
+    b.full = reinterpret_cast<uint64_t*>(p);
+    b.empty = b.full + stages;
+    b.tfull = b.empty + stages;
+    b.tempty = b.tfull + MOE_NBUF;
+    b.drain = b.tempty + MOE_NBUF;
+    return b;
+}
+
+constexpr int moe_bar_bytes(int stages) { return (2 * stages + 2 * MOE_NBUF + 1) * 8; }
+
+// Scales of the weights along a CTA's sequence of K blocks: lane l of a warp holds those of blocks
+// 32 c + l of chunk c, the next chunk's already on their way.
+template <typename Load>
+struct ScaleStream {
+    float cur, next;
+    __device__ __forceinline__ ScaleStream(int lane, const Load& load) : next(load(lane)) { cur = 0.0f; }
+    __device__ __forceinline__ float at(int n, int lane, const Load& load) {
+        if ((n & 31) == 0) {
+            cur = next;
+            next = load(n + 32 + lane);
+        }
+        return __shfl_sync(0xffffffffu, cur, n & 31);
+    }
+};
+
+// Barrier 1 of the four promotion warps, and whether any of their threads failed: all of them learn of it
+// together, so that none is left waiting.
+__device__ __forceinline__ bool promotion_any(bool failed) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(failed ? 1 : 0)
+        : "memory");
+    return r != 0;
+}
+
+// v[i] * x[i] * s added to acc, two at a time.
+template <int MT>
+__device__ __forceinline__ void promote(float* acc, const float* v, const float* xs, float s) {
+#pragma unroll
+    for (int i = 0; i < MT; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(xs + i);
+        const float2 f0 = __fmul2_rn(make_float2(f.x, f.y), make_float2(s, s));
+        const float2 f1 = __fmul2_rn(make_float2(f.z, f.w), make_float2(s, s));
+        fma2_into(acc + i, v[i], v[i + 1], f0.x, f0.y);
+        fma2_into(acc + i + 2, v[i + 2], v[i + 3], f1.x, f1.y);
+    }
+}
+
+template <int MT>
+struct UpCfg {
+    static constexpr int X_TILE = MT * BK;
+    static constexpr int STAGE = 2 * A_TILE + X_TILE;
+    static constexpr uint32_t TMEM_COLS = tmem_cols_for(MOE_NBUF * 2 * MT);
+    static int fixed(int nkb) { return 1024 + nkb * MT * 4 + 4 * MT * 4 + moe_bar_bytes(kMaxStages); }
+};
+
+template <int MT>
+__global__ void __launch_bounds__(MOE_THREADS, 1)
+    moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                  const MoeArgs a, const float* xs, uint8_t* h8, float* hs, const int stages) {
+    using Cfg = UpCfg<MT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Routing rt;
+    __shared__ uint32_t s_tmem;
+    uint8_t* smem = align_1024(smem_raw);
+    const int nkb = a.D / BK;
+    uint8_t* sW = smem;                                      // [stages][gate, up][128 x 128]
+    uint8_t* sX = sW + stages * 2 * A_TILE;                  // [stages][MT x 128]
+    float* sXs = reinterpret_cast<float*>(sX + stages * Cfg::X_TILE);   // [nkb][MT] scales of x
+    float* sMax = sXs + nkb * MT;                            // [4][MT]
+    const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sMax + 4 * MT), stages);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 2);
+        }
+        for (int i = 0; i < MOE_NBUF; ++i) {
+            mbar_init(&bar.tfull[i], 2);
+            mbar_init(&bar.tempty[i], 4);
+        }
+        mbar_init(bar.drain, 2);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) tmem_alloc(&s_tmem, Cfg::TMEM_COLS);
+    tc_fence_before();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int i = threadIdx.x; i < nkb * MT; i += MOE_THREADS) {
+        const int t = i % MT;
+        sXs[i] = t < a.T ? xs[(i / MT) * kMoeMaxTokens + t] : 0.0f;
+    }
+    build_routing(rt, a, blockIdx.x == 0);
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int iblocks = a.I / BK;
+    const int items = rt.n * iblocks;
+    // this CTA's items: blockIdx.x, + gridDim.x, ...; K blocks counted on through them
+    const int mine = blockIdx.x < items ? (items - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    const int total = mine * nkb;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last();
+            const uint64_t stream = l2_policy_evict_first();
+            int n = 0;
+            bool ok = true;
+            for (int m = 0; ok && m < mine; ++m) {
+                const int item = blockIdx.x + m * gridDim.x;
+                const int act = item / iblocks;
+                const int row = rt.active[act] * 2 * a.I + (item - act * iblocks) * BM;
+                for (int kb = 0; kb < nkb; ++kb, ++n) {
+                    const int st = n % stages;
+                    if (!mbar_wait(&bar.empty[st], ((n / stages) & 1) ^ 1)) {
+                        record_error(FP8BS_DEVERR_PRODUCER_WAIT);
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE);
+                    uint8_t* w = sW + st * 2 * A_TILE;
+                    tma_load_2d_hint(w, &tmW, &bar.full[st], kb * BK, row, stream);
+                    tma_load_2d_hint(w + A_TILE, &tmW, &bar.full[st], kb * BK, row + a.I, stream);
+                    tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmX, &bar.full[st], kb * BK, 0, keep);
+                }
+            }
+            if (!ok)
+                for (int i = max(0, n - stages); i < n; ++i)
+                    if (!mbar_wait(&bar.full[i % stages], (i / stages) & 1, kDrainLimitNs))
+                        record_error(FP8BS_DEVERR_DRAIN_WAIT);
+        }
+    } else if (warp == 1 || warp == MOE_ISSUER2) {
+        if (lane == 0) {
+            const int half = warp == 1 ? 0 : 1;              // gate or up tile
+            constexpr uint32_t idesc = idesc_e4m3_f32(BM, MT);
+            for (int n = 0; n < total; ++n) {
+                const int st = n % stages;
+                const int buf = n % MOE_NBUF;
+                if (!mbar_wait(&bar.tempty[buf], ((n / MOE_NBUF) & 1) ^ 1) ||
+                    !mbar_wait(&bar.full[st], (n / stages) & 1)) {
+                    record_error(FP8BS_DEVERR_MMA_WAIT);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t w = smem_addr(sW + (2 * st + half) * A_TILE);
+                const uint32_t x = smem_addr(sX + st * Cfg::X_TILE);
+                const uint32_t d = tmem + static_cast<uint32_t>((2 * buf + half) * MT);
+#pragma unroll
+                for (int j = 0; j < BK / MMA_K; ++j)
+                    mma_f8(d, smem_desc_k_sw128(w + j * MMA_K), smem_desc_k_sw128(x + j * MMA_K), idesc,
+                           j > 0 ? 1u : 0u);
+                mma_commit(&bar.empty[st]);
+                mma_commit(&bar.tfull[buf]);
+            }
+            mma_commit(bar.drain);
+            if (!mbar_wait(bar.drain, 0, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;                   // row of the tile = channel of the block
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        auto scale_of = [&](int n, int half) {
+            if (n >= total) return 0.0f;
+            const int m = n / nkb;
+            const int item = blockIdx.x + m * gridDim.x;
+            const int act = item / iblocks;
+            const int64_t block = static_cast<int64_t>(rt.active[act]) * 2 * iblocks + half * iblocks +
+                                  (item - act * iblocks);
+            return __ldg(a.s13 + block * nkb + (n - m * nkb));
+        };
+        auto gate_scale = [&](int n) { return scale_of(n, 0); };
+        auto up_scale = [&](int n) { return scale_of(n, 1); };
+        ScaleStream<decltype(gate_scale)> gs(lane, gate_scale);
+        ScaleStream<decltype(up_scale)> us(lane, up_scale);
+        bool ok = true;
+        int n = 0;
+        for (int m = 0; ok && m < mine; ++m) {
+            float g[MT], u[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) g[i] = u[i] = 0.0f;
+            for (int kb = 0; kb < nkb; ++kb, ++n) {
+                const float sg = gs.at(n, lane, gate_scale);
+                const float su = us.at(n, lane, up_scale);
+                const int buf = n % MOE_NBUF;
+                if (!warp_wait(&bar.tfull[buf], (n / MOE_NBUF) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t0 = tmem + lanes + static_cast<uint32_t>(2 * buf * MT);
+                const float* xk = sXs + kb * MT;
+                if constexpr (MT == 16) {
+                    float v[16], w[16];
+                    tmem_ld_16cols(t0, v);
+                    tmem_ld_16cols(t0 + 16, w);
+                    tmem_wait_ld_16(v);
+                    tmem_wait_ld_16(w);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.tempty[buf]);
+                    promote<16>(g, v, xk, sg);
+                    promote<16>(u, w, xk, su);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < MT / 32; ++c) {
+                        float v[32], w[32];
+                        tmem_ld_32cols(t0 + 32 * c, v);
+                        tmem_ld_32cols(t0 + MT + 32 * c, w);
+                        tmem_wait_ld_32(v);
+                        tmem_wait_ld_32(w);
+                        if (c + 1 == MT / 32) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.tempty[buf]);
+                        }
+                        promote<32>(g + 32 * c, v, xk + 32 * c, sg);
+                        promote<32>(u + 32 * c, w, xk + 32 * c, su);
+                    }
+                }
+            }
+            // h of this block of 128 channels: block maxima across the four warps, codes, factors
+            const int item = blockIdx.x + m * gridDim.x;
+            const int act = item / iblocks;
+            const int ib = item - act * iblocks;
+            const int e = rt.active[act];
+            const unsigned long long mask = rt.mask[e];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                if (ok && ((mask >> t) & 1)) {
+                    g[t] = g[t] / (1.0f + expf(-g[t])) * u[t];
+                    const float mag = fmaxf(fabsf(g[t]), 0.0f);          // (NaN counts as nothing)
+                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
+                    if (lane == 0) sMax[quarter * MT + t] = __uint_as_float(top);
+                }
+            if (promotion_any(!ok)) {
+                ok = false;
+                break;
+            }
+            uint8_t* out = h8 + static_cast<int64_t>(act) * a.T * a.I + ib * BK + r;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                if (t < a.T) {
+                    uint8_t code = 0;
+                    if ((mask >> t) & 1) {
+                        const float top = fmaxf(fmaxf(sMax[t], sMax[MT + t]),
+                                                fmaxf(sMax[2 * MT + t], sMax[3 * MT + t]));
+                        const float sc = block_scale(top, a.ue8m0);
+                        code = static_cast<uint8_t>(pack_e4m3x2(__fdiv_rn(g[t], sc), 0.0f));
+                    }
+                    out[static_cast<int64_t>(t) * a.I] = code;
+                }
+            if (r < MT) {
+                float f = 0.0f;
+                if (r < a.T && ((mask >> r) & 1)) {
+                    float w = 0.0f;
+                    for (int j = 0; j < a.top_k; ++j)
+                        if (a.ids[r * a.top_k + j] == e) w += a.weights[r * a.top_k + j];
+                    f = w * block_scale(fmaxf(fmaxf(sMax[r], sMax[MT + r]),
+                                              fmaxf(sMax[2 * MT + r], sMax[3 * MT + r])), a.ue8m0);
+                }
+                hs[(static_cast<int64_t>(act) * iblocks + ib) * kMoeMaxTokens + r] = f;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");       // sMax is free again
+        }
+        if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, Cfg::TMEM_COLS);
+}
+
+template <int MT>
+struct DownCfg {
+    static constexpr int X_TILE = MT * BK;
+    static constexpr int F_BYTES = MT * 4;                   // factors of the tokens
+    static constexpr int STAGE = A_TILE + X_TILE;
+    static constexpr uint32_t TMEM_COLS = tmem_cols_for(MOE_NBUF * MT);
+    static constexpr int MAX_STAGES = 11;
+    static constexpr int FIXED = 1024 + moe_bar_bytes(MAX_STAGES);
+    static constexpr int fit = (kSmemLimit - 10240 - FIXED) / (STAGE + F_BYTES);   // (Routing is static)
+    static constexpr int STAGES = fit < MAX_STAGES ? fit : MAX_STAGES;
+    static constexpr int SMEM = FIXED + STAGES * (STAGE + F_BYTES);
+};
+
+// One cluster per 128 output channels; its C CTAs share the (expert, K block) units evenly and add their
+// sums in rank order.
+template <int MT>
+__global__ void __launch_bounds__(MOE_THREADS, 1)
+    moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
+                    const MoeArgs a, const float* hs, const int C) {
+    using Cfg = DownCfg<MT>;
+    constexpr int S = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Routing rt;
+    __shared__ uint32_t s_tmem;
+    uint8_t* smem = align_1024(smem_raw);
+    uint8_t* sW = smem;                                      // [S][128 x 128]
+    uint8_t* sX = sW + S * A_TILE;                           // [S][MT x 128]
+    float* sF = reinterpret_cast<float*>(sX + S * Cfg::X_TILE);   // [S][MT]
+    const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sF + S * MT), S);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int slab = blockIdx.x / C;
+    const int rank = blockIdx.x - slab * C;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1 + 4);
+        }
+        for (int i = 0; i < MOE_NBUF; ++i) {
+            mbar_init(&bar.tfull[i], 1);
+            mbar_init(&bar.tempty[i], 4);
+        }
+        mbar_init(bar.drain, 2);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmH);
+    }
+    if (warp == 1) tmem_alloc(&s_tmem, Cfg::TMEM_COLS);
+    tc_fence_before();
+    // The ids and weights were complete before the up kernel let this one start (it does so after its own
+    // wait), so the experts are known and the weights' ring fills while the up kernel is still running.
+    build_routing(rt, a, false);
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int nkb = a.I / BK;
+    const int units = rt.n * nkb;
+    const int u0 = static_cast<int>(static_cast<int64_t>(rank) * units / C);
+    const int total = static_cast<int>(static_cast<int64_t>(rank + 1) * units / C) - u0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last();
+            const uint64_t stream = l2_policy_evict_first();
+            auto load_w = [&](int n) {
+                const int st = n % S;
+                const int act = (u0 + n) / nkb;
+                const int kb = u0 + n - act * nkb;
+                mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE + Cfg::F_BYTES);
+                tma_load_2d_hint(sW + st * A_TILE, &tmW, &bar.full[st], kb * BK,
+                                 rt.active[act] * a.D + slab * BM, stream);
+            };
+            auto load_h = [&](int n) {
+                const int st = n % S;
+                const int act = (u0 + n) / nkb;
+                const int kb = u0 + n - act * nkb;
+                tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmH, &bar.full[st], kb * BK, act * a.T, keep);
+                bulk_load(sF + st * MT, hs + (static_cast<int64_t>(act) * nkb + kb) * kMoeMaxTokens,
+                          Cfg::F_BYTES, &bar.full[st]);
+            };
+            const int ahead = min(S, total);
+            for (int n = 0; n < ahead; ++n) load_w(n);
+            grid_dependency_wait();
+            grid_launch_dependents();
+            for (int n = 0; n < ahead; ++n) load_h(n);
+            int n = ahead;
+            for (; n < total; ++n) {
+                if (!mbar_wait(&bar.empty[n % S], ((n / S) & 1) ^ 1)) {
+                    record_error(FP8BS_DEVERR_PRODUCER_WAIT);
+                    for (int i = max(0, n - S); i < n; ++i)
+                        if (!mbar_wait(&bar.full[i % S], (i / S) & 1, kDrainLimitNs))
+                            record_error(FP8BS_DEVERR_DRAIN_WAIT);
+                    break;
+                }
+                load_w(n);
+                load_h(n);
+            }
+        }
+    } else if (warp == 1 || warp == MOE_ISSUER2) {
+        grid_dependency_wait();
+        if (lane == 0) {
+            const int me = warp == 1 ? 0 : 1;                // every other K block
+            constexpr uint32_t idesc = idesc_e4m3_f32(BM, MT);
+            for (int n = me; n < total; n += 2) {
+                const int st = n % S;
+                const int buf = n % MOE_NBUF;
+                if (!mbar_wait(&bar.tempty[buf], ((n / MOE_NBUF) & 1) ^ 1) ||
+                    !mbar_wait(&bar.full[st], (n / S) & 1)) {
+                    record_error(FP8BS_DEVERR_MMA_WAIT);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t w = smem_addr(sW + st * A_TILE);
+                const uint32_t x = smem_addr(sX + st * Cfg::X_TILE);
+                const uint32_t d = tmem + static_cast<uint32_t>(buf * MT);
+#pragma unroll
+                for (int j = 0; j < BK / MMA_K; ++j)
+                    mma_f8(d, smem_desc_k_sw128(w + j * MMA_K), smem_desc_k_sw128(x + j * MMA_K), idesc,
+                           j > 0 ? 1u : 0u);
+                mma_commit(&bar.empty[st]);
+                mma_commit(&bar.tfull[buf]);
+            }
+            mma_commit(bar.drain);
+            if (!mbar_wait(bar.drain, 0, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+        }
+    } else {
+        grid_dependency_wait();
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;                   // output channel of the slab
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        auto scale_of = [&](int n) {
+            if (n >= total) return 0.0f;
+            const int act = (u0 + n) / nkb;
+            const int kb = u0 + n - act * nkb;
+            return __ldg(a.s2 + (static_cast<int64_t>(rt.active[act]) * (a.D / BK) + slab) * nkb + kb);
+        };
+        ScaleStream<decltype(scale_of)> ss(lane, scale_of);
+        float acc[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = 0.0f;
+        bool ok = true;
+        for (int n = 0; n < total; ++n) {
+            const float s = ss.at(n, lane, scale_of);
+            const int buf = n % MOE_NBUF;
+            const int st = n % S;
+            // (the products are done, so the stage has landed; its barrier orders the factors' copy)
+            if (!warp_wait(&bar.tfull[buf], (n / MOE_NBUF) & 1) ||
+                !warp_wait(&bar.full[st], (n / S) & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t t0 = tmem + lanes + static_cast<uint32_t>(buf * MT);
+            const float* f = sF + st * MT;
+            if constexpr (MT == 16) {
+                float v[16];
+                tmem_ld_16cols(t0, v);
+                tmem_wait_ld_16(v);
+                tc_fence_before();
+                promote<16>(acc, v, f, s);
+            } else {
+#pragma unroll
+                for (int c = 0; c < MT / 32; ++c) {
+                    float v[32];
+                    tmem_ld_32cols(t0 + 32 * c, v);
+                    tmem_wait_ld_32(v);
+                    if (c + 1 == MT / 32) tc_fence_before();
+                    promote<32>(acc + 32 * c, v, f + 32 * c, s);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar.tempty[buf]);
+                mbar_arrive(&bar.empty[st]);
+            }
+        }
+        if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + slab * BM + r;
+        if (C == 1) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                if (t < a.T) y[static_cast<int64_t>(t) * a.D] = __float2bfloat16_rn(acc[t]);
+        } else {
+            // CTA q of the cluster adds up tokens q * per .. of every rank's sums: [rank][token][channel]
+            const int per = MT / C;
+            const uint32_t recv = smem_addr(smem);
+            cluster_sync();                                  // every CTA is done with its stages
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int q = t / per;
+                st_shared_cluster_f32(
+                    mapa_shared(recv + static_cast<uint32_t>(((rank * per + t - q * per) * BM + r) * 4),
+                                static_cast<uint32_t>(q)),
+                    acc[t]);
+            }
+            cluster_sync();
+            const float* got = reinterpret_cast<const float*>(smem);
+            for (int i = 0; i < per; ++i) {
+                const int t = rank * per + i;
+                if (t >= a.T) break;
+                float v = got[i * BM + r];
+                for (int q = 1; q < C; ++q) v += got[(q * per + i) * BM + r];
+                y[static_cast<int64_t>(t) * a.D] = __float2bfloat16_rn(v);
+            }
+        }
+    }
+    if (C > 1 && !(warp >= MOE_PROMOTE_WARP0 && warp < MOE_PROMOTE_WARP0 + 4)) {
+        cluster_sync();
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, Cfg::TMEM_COLS);
+}
+
+template <int MT>
+cudaError_t launch_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspace& w, int num_sms,
+                           cudaStream_t stream) {
+    const int nkb = a.D / BK;
+    const int fixed = UpCfg<MT>::fixed(nkb) + 10240;         // Routing and a margin are static
+    int stages = (kSmemLimit - fixed) / UpCfg<MT>::STAGE;
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages < 2) return cudaErrorInvalidValue;
+    const int smem = UpCfg<MT>::fixed(nkb) + stages * UpCfg<MT>::STAGE;
+    cudaError_t e = set_smem(moe_up_kernel<MT>, smem);
+    if (e == cudaSuccess) e = set_smem(moe_down_kernel<MT>, DownCfg<MT>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int most_active = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
+    const int64_t items = static_cast<int64_t>(most_active) * (a.I / BK);
+    const int grid = static_cast<int>(items < num_sms ? items : num_sms);
+    const float* xs = reinterpret_cast<const float*>(a.ws + w.xs);
+    float* hs = reinterpret_cast<float*>(a.ws + w.hs);
+    e = launch_pdl(moe_up_kernel<MT>, grid, MOE_THREADS, smem, stream, m.w13, m.x8, a, xs, a.ws + w.h8, hs,
+                   stages);
+    if (e != cudaSuccess) return e;
+    // The most CTAs per slab that still leave every cluster of the grid its own SMs.
+    const int slabs = a.D / BM;
+    int C = 1;
+    while (C < kMaxSplit && slabs * C * 2 <= num_sms && most_active * (a.I / BK) >= 2 * C) C *= 2;
+    while (C > 1 && max_active_clusters(reinterpret_cast<const void*>(moe_down_kernel<MT>), MOE_THREADS,
+                                        DownCfg<MT>::SMEM, C) < slabs)
+        C /= 2;
+    return launch_pdl_cluster(moe_down_kernel<MT>, dim3(slabs * C), MOE_THREADS, DownCfg<MT>::SMEM, stream, C,
+                              false, m.w2, m.h8, a, hs, C);
 }
 
 }  // namespace
@@ -114,29 +605,26 @@ MoeWorkspace moe_workspace(int64_t T, int64_t D, int64_t I, int64_t E, int64_t t
     };
     MoeWorkspace w = {};
     const int64_t slots = T * top_k;
+    w.active = E < slots ? E : slots;
     w.x8 = take(T * D);
     w.xs = take(D / BK * kMoeMaxTokens * 4);
-    w.h8 = take(slots * I);
-    w.hs = take(slots * (I / BK) * 4);
-    w.h32 = take(slots * I * 4);
+    w.h8 = take(w.active * T * I);
+    w.hs = take(w.active * (I / BK) * kMoeMaxTokens * 4);
     w.weights = take(slots * 4);
     w.ids = take(slots * 4);
     w.total = at;
-    (void)E;
     return w;
 }
 
-cudaError_t launch_moe_experts(const MoeArgs& a, const MoeWorkspace& w, cudaStream_t stream) {
-    uint8_t* h8 = a.ws + w.h8;
-    float* hs = reinterpret_cast<float*>(a.ws + w.hs);
-    float* h32 = reinterpret_cast<float*>(a.ws + w.h32);
-    cudaError_t e = launch_pdl(moe_up_kernel, dim3(a.I / 8, a.E), 256, 0, stream, a, a.ws + w.x8,
-                               reinterpret_cast<const float*>(a.ws + w.xs), h32);
-    if (e == cudaSuccess)
-        e = launch_pdl(moe_quant_kernel, dim3(a.I / BK, a.T * a.top_k), 32, 0, stream, a, h32, h8, hs);
-    if (e == cudaSuccess)
-        e = launch_pdl(moe_down_kernel, dim3(a.D / 8, a.T), 256, 0, stream, a, h8, hs);
-    return e;
+int moe_token_rows(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
+cudaError_t launch_moe_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspace& w, int num_sms,
+                               cudaStream_t stream) {
+    switch (moe_token_rows(a.T)) {
+        case 16: return launch_experts<16>(m, a, w, num_sms, stream);
+        case 32: return launch_experts<32>(m, a, w, num_sms, stream);
+        default: return launch_experts<64>(m, a, w, num_sms, stream);
+    }
 }
 
 cudaError_t read_error_moe(unsigned int* out, bool clear, cudaStream_t stream) {

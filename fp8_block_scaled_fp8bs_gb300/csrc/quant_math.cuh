@@ -36,6 +36,18 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
         __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
 
+// The scale of a block with this amax: max(amax, 1e-4) / 448 with one IEEE division, rounded up to a
+// power of two for ue8m0.
+__device__ __forceinline__ float block_scale(float amax, bool ue8m0) {
+    float sc = __fdiv_rn(fmaxf(amax, 1e-4f), 448.0f);
+    if (ue8m0) {
+        uint32_t bits = __float_as_uint(sc);
+        if (bits & 0x007FFFFFu) bits = (bits & 0xFF800000u) + 0x00800000u;
+        sc = __uint_as_float(bits);
+    }
+    return sc;
+}
+
 // Sixteen bf16 values (packed two per word) of one 128-element block, held by one of eight
 // consecutive lanes that own the block: the block's amax is reduced with shuffles (every lane
 // of the warp must call this), and the lane's 16 e4m3 codes (packed four per word) and the
