@@ -34,6 +34,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Any, NamedTuple
 
@@ -129,14 +130,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                            vp]
         lib.fp8bs_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(ctypes.c_int64),
                                            i64, i64, i64, i32, vp]
-        lib.fp8bs_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeArgs), vp]
-        lib.fp8bs_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), vp]
-        lib.fp8bs_paged_attention_workspace_size.argtypes = [ctypes.POINTER(PagedAttentionArgs),
-                                                             ctypes.POINTER(ctypes.c_size_t)]
+        # (argument structures: byref of one, or its bytes)
+        lib.fp8bs_qk_norm_rope.argtypes = [vp, vp]
+        lib.fp8bs_paged_attention.argtypes = [vp, vp]
+        lib.fp8bs_paged_attention_workspace_size.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
         lib.fp8bs_moe_workspace_size.argtypes = [i64] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
-        lib.fp8bs_moe_route.argtypes = [vp, ctypes.POINTER(MoeRouting), vp, vp, i64, i64, i64, vp]
+        lib.fp8bs_moe_route.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
         lib.fp8bs_moe_experts.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, ctypes.c_size_t, vp]
-        lib.fp8bs_moe_layer.argtypes = [vp, ctypes.POINTER(MoeRouting)] + [vp] * 5 + [i64] * 4 + \
+        lib.fp8bs_moe_layer.argtypes = [vp] * 7 + [i64] * 4 + \
             [i32, vp, ctypes.c_size_t, vp]
         lib.fp8bs_status_string.argtypes = [i32]
         lib.fp8bs_status_string.restype = ctypes.c_char_p
@@ -474,6 +475,11 @@ def fp8_gemm_grouped(a, a_s, b, b_s, row_offsets, scale_fmt="fp32", out=None):
 
 
 # ------------------------------------------------------------- around the products of a decoder layer
+#
+# These calls take microseconds on the GPU, so their host side is kept short: one pass over the tensors'
+# attributes decides whether everything is as it should be (_fine), and only if it is not do the checks that
+# say what is wrong run; the C structures are packed in one go (the ctypes structures above, field by field,
+# cost several microseconds a call).
 
 class PagedCache(NamedTuple):
     """Keys [pages, page_size, heads, dk] and values [pages, page_size, heads, dv], bf16 CUDA tensors
@@ -482,8 +488,44 @@ class PagedCache(NamedTuple):
     v: Any
 
 
+_KV_FORMAT = "PP11q"
+_pack_norm_rope = struct.Struct("@PPP6qPPPPPPP" + _KV_FORMAT + "5qif").pack
+_pack_attention = struct.Struct("@Pqq" + _KV_FORMAT + "PqPPPP6qifPN").pack
+_pack_routing = struct.Struct("@PP3qiif4x").pack
+_KV_SIZE, _NORM_ROPE_SIZE, _ATTENTION_SIZE, _ROUTING_SIZE = (
+    struct.calcsize("@" + f) for f in (_KV_FORMAT, "PPP6qPPPPPPP" + _KV_FORMAT + "5qif",
+                                       "Pqq" + _KV_FORMAT + "PqPPPP6qifPN", "PP3qiif4x"))
+assert (_KV_SIZE, _NORM_ROPE_SIZE, _ATTENTION_SIZE, _ROUTING_SIZE) == tuple(
+    ctypes.sizeof(c) for c in (KvCache, QkNormRopeArgs, PagedAttentionArgs, MoeRouting))
+
+
+def _fine(dev, rows, dense):
+    """Whether every (tensor, ndim) of rows is bf16 with contiguous rows, and every (tensor, dtype, ndim) of
+    dense contiguous (None: absent), all on the CUDA device `dev`."""
+    import torch
+    bf16 = torch.bfloat16
+    try:
+        for t, ndim in rows:
+            if t.dtype is not bf16 or t.get_device() != dev or t.dim() != ndim or t.stride(-1) != 1:
+                return False
+        for t, dtype, ndim in dense:
+            if t is not None and (t.dtype is not dtype or t.get_device() != dev or t.dim() != ndim or
+                                  not t.is_contiguous()):
+                return False
+    except (AttributeError, IndexError):
+        return False
+    return dev >= 0
+
+
+def _device_index(t):
+    try:
+        return t.get_device()
+    except AttributeError:
+        return -1
+
+
 def _rows(t, ndim, name):
-    """A bf16 CUDA tensor whose last axis is contiguous and whose rows start on 16-byte boundaries."""
+    """A bf16 CUDA tensor whose last axis is contiguous."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -494,20 +536,53 @@ def _rows(t, ndim, name):
     return t
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
+def _explain(device, rows, dense):
+    """The checks of _fine, one by one, with what is wrong. rows: {name: (tensor, ndim)}, dense: {name:
+    (tensor, dtype, ndim)}."""
+    for name, (t, ndim) in rows.items():
+        _rows(t, ndim, name)
+    for name, (t, dtype, ndim) in dense.items():
+        if t is not None:
+            _require(t, dtype, ndim, name)
+    for name, (t, *_) in (*rows.items(), *dense.items()):
         if t is not None and t.device != device:
             raise ValueError(f"{name} must be on {device}, like the other tensors")
 
 
-def _kv_cache(cache):
-    k, v = _rows(cache.k, 4, "cache.k"), _rows(cache.v, 4, "cache.v")
-    if k.shape[:3] != v.shape[:3]:
+_stream_of = None
+
+
+def _raw_stream(dev):
+    """The current stream of device `dev` (by torch's own shortcut where it has one: a Stream object
+    takes microseconds to make)."""
+    global _stream_of
+    if _stream_of is None:
+        import torch
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _stream_of(dev)
+
+
+def _cache_fields(cache):
+    """The fields of a fp8bs_kv_cache, and (pages, page size, heads, dk, dv)."""
+    k, v = cache
+    shape, vshape = k.shape, v.shape
+    if shape[:3] != vshape[:3]:
         raise ValueError("cache.k and cache.v must have the same pages, page size and heads")
-    _same_device(k.device, **{"cache.v": v})
-    pages, page_size, heads, dk = k.shape
-    return KvCache(k.data_ptr(), v.data_ptr(), pages, page_size, heads, dk, v.shape[3],
-                   *k.stride()[:3], *v.stride()[:3])
+    sizes = (shape[0], shape[1], shape[2], shape[3], vshape[3])
+    return (k.data_ptr(), v.data_ptr(), *sizes, *k.stride()[:3], *v.stride()[:3]), sizes
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _new_output(out, shape, like):
+    """The bf16 output of `shape`: new on the device of `like`, or the caller's `out`, checked."""
+    if out is None:
+        import torch
+        return like.new_empty(shape, dtype=torch.bfloat16)
+    return _output(out, shape, like.device)
 
 
 def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, rot_start=0,
@@ -517,67 +592,69 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     rot_start .. rot_start+R-1. With a PagedCache, the keys and v bf16 [T, Hk, Dv] go to its slots
     int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k)."""
     import torch
-    _rows(q, 3, "q")
-    _rows(k, 3, "k")
+    rows = [(q, 3), (k, 3)]
+    if cache is not None:
+        rows += [(v, 3), (cache[0], 4), (cache[1], 4)]
+    elif v is not None or slots is not None:
+        raise ValueError("v and slots need a cache")
+    dev = _device_index(q)
+    if not _fine(dev, rows, ((cos, torch.float32, 2), (sin, torch.float32, 2),
+                             (positions, torch.int32, 1), (q_weight, torch.bfloat16, 1),
+                             (k_weight, torch.bfloat16, 1), (slots, torch.int64, 1))):
+        _rows(q, 3, "q")
+        if cache is not None and (v is None or slots is None):
+            raise ValueError("a cache needs v and slots")
+        _explain(q.device, dict(zip(("q", "k", "v", "cache.k", "cache.v"), rows)),
+                 {"cos": (cos, torch.float32, 2), "sin": (sin, torch.float32, 2),
+                  "positions": (positions, torch.int32, 1), "q_weight": (q_weight, torch.bfloat16, 1),
+                  "k_weight": (k_weight, torch.bfloat16, 1), "slots": (slots, torch.int64, 1)})
     T, hq, d = q.shape
-    if k.shape[0] != T or k.shape[2] != d:
+    tk, hk, dk = k.shape
+    max_pos, half = cos.shape
+    if tk != T or dk != d:
         raise ValueError("q and k must have the same tokens and channels")
-    _require(cos, torch.float32, 2, "cos")
-    _require(sin, torch.float32, 2, "sin")
-    if cos.shape != sin.shape:
+    if sin.shape != cos.shape:
         raise ValueError("cos and sin must have the same shape")
-    _require(positions, torch.int32, 1, "positions")
     if positions.shape[0] != T:
         raise ValueError("positions must have one entry per token")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _require(w, torch.bfloat16, 1, name)
-            if w.shape[0] != d:
-                raise ValueError(f"{name} must have {d} entries")
-    _same_device(q.device, k=k, v=v, cos=cos, sin=sin, positions=positions, q_weight=q_weight,
-                 k_weight=k_weight, slots=slots)
-    k_out = None
+    if (q_weight is not None and q_weight.shape[0] != d) or \
+            (k_weight is not None and k_weight.shape[0] != d):
+        raise ValueError(f"q_weight and k_weight must have {d} entries")
     if cache is None:
-        if v is not None or slots is not None:
-            raise ValueError("v and slots need a cache")
-        k_out = torch.empty((T, k.shape[1], d), dtype=torch.bfloat16, device=q.device)
-        kv = KvCache(k_out.data_ptr(), None, min(T, 1), max(T, 1), k.shape[1], d, d, 0, *k_out.stride()[:2],
-                     0, 0, 0)
+        k_out = k.new_empty((T, hk, d))
+        fields = (k_out.data_ptr(), 0, min(T, 1), max(T, 1), hk, d, d, 0, hk * d, d, 0, 0, 0)
+        v_strides = (0, 0)
     else:
-        if v is None or slots is None:
+        if slots is None:
             raise ValueError("a cache needs v and slots")
-        kv = _kv_cache(cache)
-        _same_device(q.device, cache=cache.k)
-        _rows(v, 3, "v")
-        if (kv.heads, kv.dk) != tuple(k.shape[1:]) or tuple(v.shape) != (T, kv.heads, kv.dv):
+        fields, (_, _, heads, cdk, cdv) = _cache_fields(cache)
+        if heads != hk or cdk != d or v.shape != (T, heads, cdv):
             raise ValueError("k and v do not match the cache's heads and channels")
-        _require(slots, torch.int64, 1, "slots")
         if slots.shape[0] != T:
             raise ValueError("slots must have one entry per token")
-    q_out = _output(out, (T, hq, d), q.device)
-    fp8bs_qk_norm_rope(QkNormRopeArgs(
-        q.data_ptr(), k.data_ptr(), v.data_ptr() if v is not None else None, *q.stride()[:2],
-        *k.stride()[:2], *(v.stride()[:2] if v is not None else (0, 0)),
-        q_weight.data_ptr() if q_weight is not None else None,
-        k_weight.data_ptr() if k_weight is not None else None, cos.data_ptr(), sin.data_ptr(),
-        positions.data_ptr(), slots.data_ptr() if slots is not None else None, q_out.data_ptr(), kv,
-        T, hq, cos.shape[0], rot_start, 2 * cos.shape[1], int(interleaved), eps), _stream())
+        v_strides = v.stride()[:2]
+    q_out = _new_output(out, (T, hq, d), q)
+    args = _pack_norm_rope(
+        q.data_ptr(), k.data_ptr(), _ptr(v), *q.stride()[:2], *k.stride()[:2], *v_strides,
+        _ptr(q_weight), _ptr(k_weight), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), _ptr(slots),
+        q_out.data_ptr(), *fields, T, hq, max_pos, rot_start, 2 * half, 1 if interleaved else 0, eps)
+    status = (_lib or load()).fp8bs_qk_norm_rope(args, _raw_stream(dev))
+    if status:
+        raise Fp8bsError("fp8bs_qk_norm_rope", status)
     return q_out if cache is not None else (q_out, k_out)
 
 
 _scratch = {}
 
 
-def _scratch_bytes(device, nbytes):
-    """Device memory of at least nbytes for one call on the current stream: one buffer per device and
-    stream, kept and grown (calls on one stream follow one another, so they can share it)."""
+def _scratch_bytes(dev, stream, nbytes):
+    """Device memory of at least nbytes for one call on `stream`: one buffer per device and stream, kept
+    and grown (calls on one stream follow one another, so they can share it) -> (pointer, bytes)."""
     import torch
-    if nbytes == 0:
-        return None
-    key = (device.index, _stream())
-    buf = _scratch.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = _scratch[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = _scratch.get((dev, stream))
+    if buf is None or buf[1] < nbytes:
+        t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=torch.device("cuda", dev))
+        buf = _scratch[(dev, stream)] = (t.data_ptr(), t.numel(), t)
     return buf
 
 
@@ -590,51 +667,64 @@ def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=Tr
     (default: T, and what the table can hold; tighter is faster). window > 0: each query sees that
     many keys at most, its own the last."""
     import torch
-    _rows(q, 3, "q")
-    kv = _kv_cache(cache)
+    i32 = torch.int32
+    rows = ((q, 3), (cache[0], 4), (cache[1], 4))
+    dense = ((page_table, i32, 2), (q_start, i32, 1), (kv_len, i32, 1))
+    dev = _device_index(q)
+    if not _fine(dev, rows, dense):
+        _rows(q, 3, "q")
+        _explain(q.device, dict(zip(("q", "cache.k", "cache.v"), rows)),
+                 dict(zip(("page_table", "q_start", "kv_len"), dense)))
+    fields, (_, page_size, heads, cdk, dv) = _cache_fields(cache)
     T, hq, dk = q.shape
-    if dk != kv.dk or hq % kv.heads:
+    if dk != cdk or hq % max(heads, 1):
         raise ValueError("q does not match the cache's channels, or its heads are no multiple")
-    _require(page_table, torch.int32, 2, "page_table")
-    _require(q_start, torch.int32, 1, "q_start")
-    _require(kv_len, torch.int32, 1, "kv_len")
     B, n = page_table.shape
     if kv_len.shape[0] != B or q_start.shape[0] != B + 1:
         raise ValueError("page_table, q_start and kv_len must agree on the number of sequences")
-    _same_device(q.device, cache=cache.k, page_table=page_table, q_start=q_start, kv_len=kv_len)
-    o = _output(out, (T, hq, kv.dv), q.device)
-    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if return_lse else None
-    args = PagedAttentionArgs(
-        q.data_ptr(), *q.stride()[:2], kv, page_table.data_ptr(), n, q_start.data_ptr(),
-        kv_len.data_ptr(), o.data_ptr(), lse.data_ptr() if return_lse else None, B, T, hq,
-        T if max_q_len is None else max_q_len,
-        n * kv.page_size if max_kv_len is None else max_kv_len, window, int(causal),
-        dk ** -0.5 if scale is None else scale, None, 0)
-    ws = _scratch_bytes(q.device, fp8bs_paged_attention_workspace_size(args))
-    if ws is not None:
-        args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
-    fp8bs_paged_attention(args, _stream())
-    return (o, lse) if return_lse else o
+    o = _new_output(out, (T, hq, dv), q)
+    lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
+    stream = _raw_stream(dev)
+    lib = _lib or load()
+    # The library says whether the workspace at hand is large enough; if not, it is asked how much it takes.
+    ws = _scratch.get((dev, stream)) or (0, 0)
+    while True:
+        args = _pack_attention(
+            q.data_ptr(), *q.stride()[:2], *fields, page_table.data_ptr(), n, q_start.data_ptr(),
+            kv_len.data_ptr(), o.data_ptr(), _ptr(lse), B, T, hq, T if max_q_len is None else max_q_len,
+            n * page_size if max_kv_len is None else max_kv_len, window, 1 if causal else 0,
+            dk ** -0.5 if scale is None else scale, ws[0], ws[1])
+        status = lib.fp8bs_paged_attention(args, stream)
+        if status == 0:
+            return (o, lse) if return_lse else o
+        if status == 1:
+            need = ctypes.c_size_t(0)
+            if lib.fp8bs_paged_attention_workspace_size(args, ctypes.byref(need)) == 0 and \
+                    need.value > ws[1]:
+                ws = _scratch_bytes(dev, stream, need.value)
+                continue
+        raise Fp8bsError("fp8bs_paged_attention", status)
 
 
 def _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale):
     import torch
-    _require(x, torch.bfloat16, 2, "x")
-    _require(router_w, torch.bfloat16, 2, "router_w")
-    if router_w.shape[1] != x.shape[1]:
+    rows = ((x, torch.bfloat16, 2), (router_w, torch.bfloat16, 2), (bias, torch.float32, 1))
+    if not _fine(_device_index(x), (), rows):
+        _require(x, torch.bfloat16, 2, "x")
+        _explain(x.device, {}, dict(zip(("x", "router_w", "bias"), rows)))
+    experts, dim = router_w.shape
+    if dim != x.shape[1]:
         raise ValueError("router_w must have x's channels")
-    if bias is not None:
-        _require(bias, torch.float32, 1, "bias")
-        if bias.shape[0] != router_w.shape[0]:
-            raise ValueError("bias must have one entry per expert")
-    _same_device(x.device, router_w=router_w, bias=bias)
+    if bias is not None and bias.shape[0] != experts:
+        raise ValueError("bias must have one entry per expert")
     if score not in ("sigmoid", "softmax"):
         raise ValueError(f"unknown score {score!r}")
+    sigmoid = score == "sigmoid"
     if normalise is None:
-        normalise = score == "sigmoid"
-    return MoeRouting(router_w.data_ptr(), bias.data_ptr() if bias is not None else None, top_k,
-                      groups, topk_groups, SCORE_SIGMOID if score == "sigmoid" else SCORE_SOFTMAX,
-                      int(normalise), route_scale)
+        normalise = sigmoid
+    return experts, _pack_routing(router_w.data_ptr(), _ptr(bias), top_k, groups, topk_groups,
+                                  SCORE_SIGMOID if sigmoid else SCORE_SOFTMAX, 1 if normalise else 0,
+                                  route_scale)
 
 
 def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_groups=1, normalise=None,
@@ -644,64 +734,71 @@ def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_gro
     to the best groups of experts; normalise (default: for sigmoid scores) makes a token's weights
     sum to route_scale."""
     import torch
-    routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
+    experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
     T, D = x.shape
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
-    fp8bs_moe_route(x.data_ptr(), routing, weights.data_ptr(), ids.data_ptr(), T, D,
-                    router_w.shape[0], _stream())
+    weights = x.new_empty((T, top_k), dtype=torch.float32)
+    ids = x.new_empty((T, top_k), dtype=torch.int32)
+    _check("fp8bs_moe_route", (_lib or load()).fp8bs_moe_route(
+        x.data_ptr(), routing, weights.data_ptr(), ids.data_ptr(), T, D, experts,
+        _raw_stream(x.get_device())))
     return weights, ids
 
 
-def _expert_shapes(x, w13, s13, w2, s2):
+def _expert_shapes(x, w13, s13, w2, s2, weights=None, ids=None):
     import torch
-    _require(x, torch.bfloat16, 2, "x")
-    _require(w13, torch.float8_e4m3fn, 3, "w13")
-    _require(w2, torch.float8_e4m3fn, 3, "w2")
-    _require(s13, torch.float32, 3, "s13")
-    _require(s2, torch.float32, 3, "s2")
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    dense = ((x, torch.bfloat16, 2), (w13, e4m3, 3), (s13, f32, 3), (w2, e4m3, 3), (s2, f32, 3),
+             (weights, f32, 2), (ids, torch.int32, 2))
+    dev = _device_index(x)
+    if not _fine(dev, (), dense):
+        _require(x, torch.bfloat16, 2, "x")
+        _explain(x.device, {}, dict(zip(("x", "w13", "s13", "w2", "s2", "weights", "ids"), dense)))
     T, D = x.shape
-    E, _, inter = w2.shape
-    if tuple(w13.shape) != (E, 2 * inter, D) or w2.shape[1] != D or \
-            tuple(s13.shape) != (E, 2 * inter // BLOCK, D // BLOCK) or \
-            tuple(s2.shape) != (E, D // BLOCK, inter // BLOCK):
+    E, rows, inter = w2.shape
+    if rows != D or w13.shape != (E, 2 * inter, D) or \
+            s13.shape != (E, 2 * inter // BLOCK, D // BLOCK) or \
+            s2.shape != (E, D // BLOCK, inter // BLOCK):
         raise ValueError("expert weight or scale shapes do not match")
-    _same_device(x.device, w13=w13, s13=s13, w2=w2, s2=s2)
-    return T, D, inter, E
+    return dev, T, D, inter, E
+
+
+def _expert_workspace(lib, dev, stream, T, D, inter, E, top_k):
+    need = ctypes.c_size_t(0)
+    _check("fp8bs_moe_workspace_size", lib.fp8bs_moe_workspace_size(T, D, inter, E, top_k,
+                                                                    ctypes.byref(need)))
+    return _scratch_bytes(dev, stream, need.value)
 
 
 def moe_experts(x, weights, ids, w13, s13, w2, s2, scale_fmt="fp32", out=None):
     """The experts of a mixture-of-experts layer for x bf16 [T <= 64, D]: w13 e4m3 [E, 2I, D] (gate
     rows, then up rows), w2 e4m3 [E, D, I], scales per 128 x 128 block; ids int32 [T, top_k] (-1: none)
     and weights fp32 [T, top_k] as moe_route gives them -> y bf16 [T, D]."""
-    import torch
-    T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
-    _require(weights, torch.float32, 2, "weights")
-    _require(ids, torch.int32, 2, "ids")
+    dev, T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2, weights, ids)
+    k = ids.shape[1]
     if weights.shape != ids.shape or ids.shape[0] != T:
         raise ValueError("weights and ids must be [T, top_k]")
-    _same_device(x.device, weights=weights, ids=ids)
-    y = _output(out, (T, D), x.device)
-    k = ids.shape[1]
-    ws = _scratch_bytes(x.device, fp8bs_moe_workspace_size(T, D, inter, E, k))
-    fp8bs_moe_experts(x.data_ptr(), weights.data_ptr(), ids.data_ptr(), w13.data_ptr(),
-                      s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr(), T, D, inter, E, k,
-                      _fmt(scale_fmt), ws.data_ptr() if ws is not None else None,
-                      ws.numel() if ws is not None else 0, _stream())
+    y = _new_output(out, (T, D), x)
+    stream = _raw_stream(dev)
+    lib = _lib or load()
+    ws = _expert_workspace(lib, dev, stream, T, D, inter, E, k)
+    _check("fp8bs_moe_experts", lib.fp8bs_moe_experts(
+        x.data_ptr(), weights.data_ptr(), ids.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
+        s2.data_ptr(), y.data_ptr(), T, D, inter, E, k, _fmt(scale_fmt), ws[0], ws[1], stream))
     return y
 
 
 def moe_layer(x, router_w, w13, s13, w2, s2, top_k, bias=None, score="sigmoid", groups=1,
               topk_groups=1, normalise=None, route_scale=1.0, scale_fmt="fp32", out=None):
     """A whole mixture-of-experts layer for x bf16 [T <= 64, D]: moe_route, then moe_experts."""
-    routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
-    T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
-    if router_w.shape[0] != E:
+    experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
+    dev, T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
+    if experts != E:
         raise ValueError("router_w must have one row per expert")
-    y = _output(out, (T, D), x.device)
-    ws = _scratch_bytes(x.device, fp8bs_moe_workspace_size(T, D, inter, E, top_k))
-    fp8bs_moe_layer(x.data_ptr(), routing, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
-                    s2.data_ptr(), y.data_ptr(), T, D, inter, E, _fmt(scale_fmt),
-                    ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
-                    _stream())
+    y = _new_output(out, (T, D), x)
+    stream = _raw_stream(dev)
+    lib = _lib or load()
+    ws = _expert_workspace(lib, dev, stream, T, D, inter, E, top_k)
+    _check("fp8bs_moe_layer", lib.fp8bs_moe_layer(
+        x.data_ptr(), routing, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr(),
+        T, D, inter, E, _fmt(scale_fmt), ws[0], ws[1], stream))
     return y
