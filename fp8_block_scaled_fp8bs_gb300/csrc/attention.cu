@@ -38,11 +38,11 @@ struct AttnCfg {
     static constexpr int VST = DK == 64 ? 4 : DK == 128 ? 2 : (NQ == 2 ? 3 : 4);
     static constexpr int SOFT_WARPS = 4 * NQ;
     static constexpr int LOAD_WARP = SOFT_WARPS;
-    static constexpr int MMA_WARP = SOFT_WARPS + 1;              // one issuer per query tile
-    static constexpr int THREADS = 32 * (SOFT_WARPS + 1 + NQ);
+    static constexpr int MMA_WARP = SOFT_WARPS + 1;
+    static constexpr int THREADS = 32 * (SOFT_WARPS + 2);
     static constexpr int CTAS = NQ == 1 && DK <= 128 ? 2 : 1;    // per SM
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
-    static constexpr int BARS = 2 * KST + 2 * VST + 2 * SBUF + 2 * NQ + 1;
+    static constexpr int BARS = 2 * KST + 2 * VST + 3 * SBUF + 2 * NQ + 1;
     static constexpr int SMEM = 1024 + NQ * Q_TILE + KST * K_TILE + VST * V_TILE + BARS * 8 + 64;
     static_assert(SMEM <= kSmemLimit, "shared memory");
 };
@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     uint64_t* v_full = k_empty + Cfg::KST;
     uint64_t* v_empty = v_full + Cfg::VST;
     uint64_t* s_full = v_empty + Cfg::VST;                // [SBUF]
-    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF]
-    uint64_t* o_done = p_full + Cfg::SBUF;                // [NQ]
+    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF][2 halves]
+    uint64_t* o_done = p_full + 2 * Cfg::SBUF;            // [NQ]
     uint64_t* drain = o_done + NQ;                        // [NQ]
     uint64_t* v_tail = drain + NQ;                        // the last, partly valid value tile
 
@@ -223,15 +223,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     if (threadIdx.x == 0) {
         for (int i = 0; i < Cfg::KST; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], NQ);
+            mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < Cfg::VST; ++i) {
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], NQ);
+            mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < Cfg::SBUF; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);
+            mbar_init(&p_full[2 * i + 1], 4);
         }
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&o_done[i], 1);
@@ -422,62 +423,84 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         record_error(FP8BS_DEVERR_DRAIN_WAIT);
                 }
             }
-        } else if (warp >= Cfg::MMA_WARP) {
-            // ---- MMA issuer of query tile q
-            const int q = warp - Cfg::MMA_WARP;
+        } else if (warp == Cfg::MMA_WARP) {
+            // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j) in two halves as the softmax
+            // hands them over, then S of the tile's next keys, which takes P's place (the tensor core
+            // works in order). With two query tiles one's products run under the other's softmax.
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV) | kIdescBMajorMN;
-            const uint32_t q_addr = smem_addr(sQ) + q * Cfg::Q_TILE;
-            const uint32_t o_tmem = tmem + Cfg::SBUF * BN + q * DV;
+            const uint32_t q_addr = smem_addr(sQ);
+            const uint32_t o_tmem = tmem + Cfg::SBUF * BN;
             bool ok = true;
-            auto qk = [&](int j) {         // S(j): buffer q (two tiles) or j % 2
+            int ended = 0;                 // query tiles whose last product has been committed
+            auto qk = [&](int q, int j) {  // S(j): buffer q (two tiles) or j % 2
                 const int st = j % Cfg::KST;
-                if (!warp_wait(&k_full[st], (j / Cfg::KST) & 1)) return false;
-                tc_fence_after();
+                if (q == 0) {
+                    if (!warp_wait(&k_full[st], (j / Cfg::KST) & 1)) return false;
+                    tc_fence_after();
+                }
                 const int buf = NQ == 2 ? q : j & 1;
                 const uint32_t k_addr = smem_addr(sK) + st * Cfg::K_TILE;
                 if (elect_one()) {
 #pragma unroll
                     for (int d = 0; d < DK / 16; ++d)
                         mma_bf16(tmem + buf * BN,
-                                 smem_desc_k_sw128(q_addr + (d / 4) * (128 * 128) + (d % 4) * 32),
+                                 smem_desc_k_sw128(q_addr + q * Cfg::Q_TILE + (d / 4) * (128 * 128) +
+                                                   (d % 4) * 32),
                                  smem_desc_k_sw128(k_addr + (d / 4) * (BN * 128) + (d % 4) * 32),
                                  idesc_qk, d > 0 ? 1u : 0u);
-                    mma_commit(&k_empty[st]);
                     mma_commit(&s_full[buf]);
+                    if (q == NQ - 1) mma_commit(&k_empty[st]);
                 }
                 __syncwarp();
                 return true;
             };
-            ok = qk(0);
-            if (ok && NQ == 1 && nt > 1) ok = qk(1);
+            for (int q = 0; ok && q < NQ; ++q) ok = qk(q, 0);
+            if (ok && NQ == 1 && nt > 1) ok = qk(0, 1);
             for (int j = 0; ok && j < nt; ++j) {
-                const int buf = NQ == 2 ? q : j & 1;
-                const uint32_t pph = NQ == 2 ? j & 1 : (j >> 1) & 1;
                 const int st = j % Cfg::VST;
-                if (!warp_wait(&v_full[st], (j / Cfg::VST) & 1) || !warp_wait(&p_full[buf], pph)) {
+                const uint32_t pph = NQ == 2 ? j & 1 : (j >> 1) & 1;
+                const uint32_t v_addr = smem_addr(sV) + st * Cfg::V_TILE;
+                if (!warp_wait(&v_full[st], (j / Cfg::VST) & 1)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t v_addr = smem_addr(sV) + st * Cfg::V_TILE;
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BN / 16; ++k)
-                        mma_bf16_ta(o_tmem, tmem + buf * BN + 8 * k,
-                                    smem_desc_mn_sw128(v_addr + k * 2048, BN * 128), idesc_pv,
-                                    j > 0 || k > 0 ? 1u : 0u);
-                    mma_commit(&v_empty[st]);
-                    mma_commit(&o_done[q]);
+                for (int q = 0; q < NQ; ++q) {
+                    const int buf = NQ == 2 ? q : j & 1;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!ok || !warp_wait(&p_full[2 * buf + half], pph)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = half * (BN / 32); k < (half + 1) * (BN / 32); ++k)
+                                mma_bf16_ta(o_tmem + q * DV, tmem + buf * BN + 8 * k,
+                                            smem_desc_mn_sw128(v_addr + k * 2048, BN * 128), idesc_pv,
+                                            j > 0 || k > 0 ? 1u : 0u);
+                            if (half == 1) {
+                                mma_commit(&o_done[q]);
+                                if (q == NQ - 1) mma_commit(&v_empty[st]);
+                                if (j == nt - 1) mma_commit(&drain[q]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (j == nt - 1) ++ended;
+                    const int next = NQ == 2 ? j + 1 : j + 2;
+                    if (next < nt) ok = qk(q, next);
                 }
-                __syncwarp();
-                const int next = NQ == 2 ? j + 1 : j + 2;
-                if (next < nt) ok = qk(next);
             }
             if (!ok && lane == 0) record_error(FP8BS_DEVERR_MMA_WAIT);
-            if (elect_one()) mma_commit(&drain[q]);
+            if (elect_one())
+                for (int q = ended; q < NQ; ++q) mma_commit(&drain[q]);
             __syncwarp();
-            if (!warp_wait(&drain[q], 0) && lane == 0) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+            for (int q = 0; q < NQ; ++q)
+                if (!warp_wait(&drain[q], 0) && lane == 0) record_error(FP8BS_DEVERR_DRAIN_WAIT);
         } else {
             // ---- softmax warps: thread = row
             const int q = warp >> 2;
@@ -552,27 +575,35 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : m * c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
 #pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) {
-                        uint32_t p[16];
+                    for (int half = 0; half < 2; ++half) {
+                        constexpr int H = BN / 2;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float2 x = __ffma2_rn(make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]),
-                                                        make_float2(c, c), make_float2(-mc, -mc));
-                            const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
-                            sum[k & 1] += p0;
-                            sum[2 + (k & 1)] += p1;
-                            p[k] = pack_bf16x2(p0, p1);
+                        for (int i = 0; i < H / 32; ++i) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int e = half * H + 32 * i + 2 * k;
+                                float2 x = __ffma2_rn(make_float2(s[e], s[e + 1]), c2, mc2);
+                                x.x = exp2_fast(x.x);
+                                x.y = exp2_fast(x.y);
+                                sum[k & 1] = __fadd2_rn(sum[k & 1], x);
+                                p[k] = pack_bf16x2(x.x, x.y);
+                            }
+                            tmem_st_16cols(s_tmem_row + half * (H / 2) + 16 * i, p);
                         }
-                        tmem_st_16cols(s_tmem_row + 16 * i, p);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * buf + half]);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_wait_st();
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                } else if (lane == 0) {
+                    mbar_arrive(&p_full[2 * buf]);
+                    mbar_arrive(&p_full[2 * buf + 1]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[buf]);
             }
             // every product of this query tile is done (o_done's parity would not tell: with two S
             // buffers the last two products may complete before this warp looks)
