@@ -73,24 +73,40 @@ extern "C" int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* str
 
 namespace {
 
-// A cache's keys or values as {channels, heads, slots, pages}, boxes of {64 channels, 1, slots, 1},
-// 128-byte swizzle. Out-of-range pages read as zero.
+// A cache's keys or values as fp8bs::AttentionModes says. Pages past the end read as zero.
 bool make_cache_map(CUtensorMap* map, const void* base, const fp8bs_kv_cache& c, int64_t d,
-                    int64_t head_stride, int64_t slot_stride, int64_t page_stride, int box_slots) {
+                    int64_t head_stride, int64_t slot_stride, int64_t page_stride, int mode, int box_slots) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     // (the stride of an axis of length one is never used, but has to be a valid one)
     auto bytes = [&](int64_t stride, int64_t n) {
         return static_cast<cuuint64_t>(n > 1 ? stride * 2 : d * 2);
     };
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.heads),
-                                static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
-    const cuuint64_t strides[3] = {bytes(head_stride, c.heads), bytes(slot_stride, c.page_size),
-                                   bytes(page_stride, c.pages)};
-    const cuuint32_t box[4] = {64u, 1u, static_cast<cuuint32_t>(box_slots), 1u};
-    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint64_t chunks = static_cast<cuuint64_t>(d / 64);
+    const cuuint64_t heads = static_cast<cuuint64_t>(c.heads), pages = static_cast<cuuint64_t>(c.pages);
+    const cuuint64_t slots = static_cast<cuuint64_t>(c.page_size);
+    cuuint64_t dims[5], strides[4];
+    cuuint32_t box[5], estr[5] = {1u, 1u, 1u, 1u, 1u};
+    int rank = 5;
+    if (mode == 2) {
+        rank = 4;
+        dims[0] = static_cast<cuuint64_t>(d), dims[1] = heads, dims[2] = slots, dims[3] = pages;
+        strides[0] = bytes(head_stride, c.heads);
+        strides[1] = bytes(slot_stride, c.page_size);
+        strides[2] = bytes(page_stride, c.pages);
+        box[0] = 64, box[1] = 1, box[2] = static_cast<cuuint32_t>(box_slots), box[3] = 1;
+    } else {
+        dims[0] = 64, dims[1] = 8, dims[2] = mode == 0 ? heads * chunks : chunks, dims[3] = slots / 8;
+        dims[4] = mode == 0 ? pages : pages * heads;
+        strides[0] = static_cast<cuuint64_t>(slot_stride) * 2;
+        strides[1] = 128;
+        strides[2] = static_cast<cuuint64_t>(slot_stride) * 16;
+        strides[3] = mode == 0 ? bytes(page_stride, c.pages) : bytes(head_stride, c.heads);
+        box[0] = 64, box[1] = 8, box[2] = static_cast<cuuint32_t>(chunks);
+        box[3] = static_cast<cuuint32_t>(box_slots / 8), box[4] = 1;
+    }
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -146,13 +162,15 @@ extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, voi
     const fp8bs::AttentionPlan plan = fp8bs::attention_plan(a, sms);
     const size_t need = fp8bs::attention_workspace(a, plan);
     if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return FP8BS_ERR_INVALID_ARG;
-    const int box_log2 = fp8bs::attention_box_log2(a.cache.page_size);
+    const fp8bs::AttentionModes modes = fp8bs::attention_modes(a.cache);
     CUtensorMap tmK, tmV;
     const fp8bs_kv_cache& c = a.cache;
-    if (!make_cache_map(&tmK, c.k, c, c.dk, c.k_head_stride, c.k_slot_stride, c.k_page_stride, 1 << box_log2) ||
-        !make_cache_map(&tmV, c.v, c, c.dv, c.v_head_stride, c.v_slot_stride, c.v_page_stride, 1 << box_log2))
+    if (!make_cache_map(&tmK, c.k, c, c.dk, c.k_head_stride, c.k_slot_stride, c.k_page_stride, modes.k,
+                        1 << modes.box_log2) ||
+        !make_cache_map(&tmV, c.v, c, c.dv, c.v_head_stride, c.v_slot_stride, c.v_page_stride, modes.v,
+                        1 << modes.box_log2))
         return FP8BS_ERR_CUDA;
-    return status_of(fp8bs::launch_paged_attention(tmK, tmV, a, box_log2, plan,
+    return status_of(fp8bs::launch_paged_attention(tmK, tmV, a, modes, plan, sms,
                                                    static_cast<cudaStream_t>(stream)));
 }
 

@@ -14,10 +14,13 @@
 // to binary32; the rounding of P (2^-9 on average per term) is of the size of the output's own.
 //
 // Two forms (AttnCfg): NQ = 2 query tiles per CTA for chunks, whose softmax warps work on one tile
-// while the tensor core works on the other; NQ = 1 with two S buffers for few rows, two CTAs per SM.
-// Keys and values come through TMA in boxes of as many slots as divide both the page and the tile.
+// while the tensor core works on the other; NQ = 1 with two S buffers for few rows.
+// Keys and values come through TMA in boxes of as many slots as divide both the page and the tile, all
+// channels of a box at once where the cache's strides allow it.
 // Few rows and long keys: the key axis is cut into pieces (AttentionPlan), each CTA leaves its
 // unnormalised O, maximum and sum, and a second kernel joins them in key order.
+#include <algorithm>
+
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
@@ -30,85 +33,34 @@ constexpr float kRescale = 8.0f;
 template <int DK_, int DV_, int NQ_>
 struct AttnCfg {
     static constexpr int DK = DK_, DV = DV_, NQ = NQ_;
-    static constexpr int BN = NQ == 2 && DK <= 128 ? 128 : 64;   // keys per tile
+    static constexpr int BN = NQ == 2 ? 128 : 64;                // keys per tile
     static constexpr int ROWS = NQ * 128;
+    static constexpr int PARTS = BN == 128 ? 2 : 1;              // P is handed over in so many parts
+    static constexpr int SLOTS = 4;                              // ring of work items
     static constexpr int SBUF = 2;                               // S buffers: per query tile, or 2
     static constexpr int K_TILE = BN * DK * 2, V_TILE = BN * DV * 2, Q_TILE = 128 * DK * 2;
-    static constexpr int KST = DK == 64 ? 4 : DK == 128 ? (NQ == 2 ? 3 : 2) : (NQ == 2 ? 3 : 4);
-    static constexpr int VST = DK == 64 ? 4 : DK == 128 ? 2 : (NQ == 2 ? 3 : 4);
+    static constexpr int KST = DK == 64 ? (NQ == 2 ? 4 : 8) : DK == 128 ? (NQ == 2 ? 3 : 6) : (NQ == 2 ? 2 : 4);
+    static constexpr int VST = DK == 64 ? (NQ == 2 ? 4 : 8) : DK == 128 ? (NQ == 2 ? 2 : 5) : (NQ == 2 ? 1 : 4);
     static constexpr int SOFT_WARPS = 4 * NQ;
-    static constexpr int LOAD_WARP = SOFT_WARPS;
-    static constexpr int MMA_WARP = SOFT_WARPS + 1;
-    static constexpr int THREADS = 32 * (SOFT_WARPS + 2);
-    static constexpr int CTAS = NQ == 1 && DK <= 128 ? 2 : 1;    // per SM
+    static constexpr int KEY_WARP = SOFT_WARPS;                  // brings the keys (and hands out the items)
+    static constexpr int VALUE_WARP = SOFT_WARPS + 1;
+    static constexpr int MMA_WARP = SOFT_WARPS + 2;
+    // (two query tiles: a whole third warpgroup beside the softmax's, for the split of registers below)
+    static constexpr int THREADS = 32 * (SOFT_WARPS + (NQ == 2 ? 4 : 3));
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
-    static constexpr int BARS = 2 * KST + 2 * VST + 3 * SBUF + 2 * NQ + 1;
+    static constexpr int BARS = 2 * KST + 2 * VST + (1 + PARTS) * SBUF + 3 * NQ + 2 + 2 * SLOTS;
     static constexpr int SMEM = 1024 + NQ * Q_TILE + KST * K_TILE + VST * V_TILE + BARS * 8 + 64;
     static_assert(SMEM <= kSmemLimit, "shared memory");
 };
 
-// A row tile of one sequence.
-struct RowTile {
-    int seq, first_row;    // first packed row (i * G + g) of the tile
-    int n;                 // new tokens of the sequence
-    int q0;                // its first query token
-    int kv;                // its keys
+// A work item: a tile of packed rows (i * G + g) of one sequence and key head, and one piece of its keys.
+struct Item {
+    int seq;               // -1: no more items; -2: a sequence out of bounds, to be passed over
+    int n, q0, kv;         // its new tokens, first query token and keys
+    int first_row, rows;   // first packed row and valid rows of the tile
+    int head, piece, pieces;   // key head; piece of the keys, of so many
+    int key_lo, key_hi;    // keys of the piece that any row attends
 };
-
-// The tile'th run of `rows` packed rows, counted over the sequences in order; seq = -1 past the last.
-// One warp: eight sequences per lane and step.
-__device__ __forceinline__ RowTile find_row_tile(const fp8bs_paged_attention_args& a, int64_t tile,
-                                                 int group, int rows, int lane) {
-    RowTile t = {-1, 0, 0, 0, 0};
-    if (a.max_q_len == 1 && group <= rows && tile < a.B) {
-        // single tokens everywhere before it: the tile is its own sequence
-        const int q0 = a.q_start[tile], q1 = a.q_start[tile + 1];
-        if (q0 == tile && q1 == tile + 1)
-            return RowTile{static_cast<int>(tile), 0, 1, q0, a.kv_len[tile]};
-    }
-    for (int64_t base = 0; base < a.B; base += 256) {
-        int start[9], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-            const int64_t b = base + 8 * lane + i;
-            start[i] = a.q_start[b < a.B ? b : a.B];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            sum += (max(start[i + 1] - start[i], 0) * group + rows - 1) / rows;
-        int incl = sum;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, m);
-            if (lane >= m) incl += o;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, incl > tile);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            if (lane == src) {
-                int64_t left = tile - (incl - sum);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int n = max(start[i + 1] - start[i], 0);
-                    const int tiles = (n * group + rows - 1) / rows;
-                    if (t.seq < 0 && left < tiles)
-                        t = RowTile{static_cast<int>(base) + 8 * lane + i,
-                                    static_cast<int>(left) * rows, n, start[i], 0};
-                    left -= tiles;
-                }
-                t.kv = a.kv_len[t.seq];
-            }
-            t.seq = __shfl_sync(0xffffffffu, t.seq, src);
-            t.first_row = __shfl_sync(0xffffffffu, t.first_row, src);
-            t.n = __shfl_sync(0xffffffffu, t.n, src);
-            t.q0 = __shfl_sync(0xffffffffu, t.q0, src);
-            t.kv = __shfl_sync(0xffffffffu, t.kv, src);
-            return t;
-        }
-        tile -= __shfl_sync(0xffffffffu, incl, 31);
-    }
-    return t;
-}
 
 // Keys [lo, hi) that the i-th new token attends.
 struct KeyRange {
@@ -121,6 +73,126 @@ __device__ __forceinline__ KeyRange keys_of(const fp8bs_paged_attention_args& a,
     r.hi = a.causal ? static_cast<int>(min(static_cast<int64_t>(kv), max(last + 1, int64_t{0}))) : kv;
     r.lo = a.window > 0 ? static_cast<int>(min(static_cast<int64_t>(kv), max(last - a.window + 1, int64_t{0}))) : 0;
     return r;
+}
+
+// Most keys that the rows of one tile attend, counted from the start of a key tile: what the pieces of a
+// sequence with n new tokens and kv keys are cut from. It grows with n and kv, so that the host's bounds give
+// a bound of it.
+__host__ __device__ inline int64_t key_span(const fp8bs_paged_attention_args& a, int rows, int64_t n,
+                                            int64_t kv) {
+    if (a.window == 0) return kv;
+    const int64_t tokens = rows / (a.q_heads / a.cache.heads) + 2;
+    const int64_t span = a.window + (a.causal && tokens < n ? tokens : n) + 128;
+    return span < kv ? span : kv;
+}
+
+// The work items in order, for one warp: sequences in order, in each the row tiles from the last (whose keys
+// are the most) to the first, for each tile its pieces, for each piece the key heads (which read the same
+// slots). Calls ask for rising items; the sequences are read 256 at a time, eight per lane.
+struct ItemFinder {
+    int base, before;       // first sequence of the chunk in hand, units (items / heads) before it
+    int start[9], kv[8];    // lane's sequences: first query tokens (and the next one's), keys
+    int units[8];           // of each
+    int incl, sum;          // of the chunk up to and with this lane, of this lane
+    bool loaded;
+};
+
+struct Cut {
+    int tiles, pieces;
+};
+
+__device__ __forceinline__ Cut cut_of(const fp8bs_paged_attention_args& a, int rows, int piece_len, int n, int kv,
+                                      int group) {
+    Cut c;
+    c.tiles = (n * group + rows - 1) / rows;
+    const unsigned span = static_cast<unsigned>(key_span(a, rows, n, max(kv, 0)));
+    c.pieces = span > piece_len ? static_cast<int>((span + piece_len - 1) / piece_len) : 1;
+    return c;
+}
+
+__device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_attention_args& a, int item,
+                                          int rows, int bn, int piece_len, int lane) {
+    Item it;
+    it.seq = -1;
+    const int heads = static_cast<int>(a.cache.heads);
+    const int group = static_cast<int>(a.q_heads / a.cache.heads);
+    const int unit = item / heads;
+    it.head = item - unit * heads;
+    while (f.base < a.B) {
+        if (!f.loaded) {
+            f.sum = 0;
+#pragma unroll
+            for (int i = 0; i < 9; ++i) {
+                const int64_t b = f.base + 8 * lane + i;
+                f.start[i] = a.q_start[b < a.B ? b : a.B];
+                if (i < 8) f.kv[i] = b < a.B ? a.kv_len[b] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int n = f.start[i + 1] - f.start[i];
+                f.units[i] = 0;
+                if (n > 0) {
+                    const Cut c = cut_of(a, rows, piece_len, n, f.kv[i], group);
+                    f.units[i] = c.tiles * c.pieces;
+                }
+                f.sum += f.units[i];
+            }
+            f.incl = f.sum;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, f.incl, m);
+                if (lane >= m) f.incl += o;
+            }
+            f.loaded = true;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, f.before + f.incl > unit);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            int seq = 0, n = 0, q0 = 0, kv = 0, tile = 0, piece = 0, pieces = 1;
+            if (lane == src) {
+                int left = unit - f.before - (f.incl - f.sum);
+                int mine = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (left >= 0 && left < f.units[i]) {
+                        seq = f.base + 8 * lane + i;
+                        n = f.start[i + 1] - f.start[i];
+                        q0 = f.start[i];
+                        kv = f.kv[i];
+                        mine = left;
+                    }
+                    left -= f.units[i];
+                }
+                const Cut c = cut_of(a, rows, piece_len, n, kv, group);
+                pieces = c.pieces;
+                tile = c.tiles - 1 - mine / c.pieces;
+                piece = mine % c.pieces;
+            }
+            it.seq = __shfl_sync(0xffffffffu, seq, src);
+            it.n = __shfl_sync(0xffffffffu, n, src);
+            it.q0 = __shfl_sync(0xffffffffu, q0, src);
+            it.kv = __shfl_sync(0xffffffffu, kv, src);
+            it.first_row = __shfl_sync(0xffffffffu, tile, src) * rows;
+            it.piece = __shfl_sync(0xffffffffu, piece, src);
+            it.pieces = __shfl_sync(0xffffffffu, pieces, src);
+            if (it.n > a.max_q_len || it.kv > a.max_kv_len || it.kv < 0 || it.q0 < 0 ||
+                it.q0 + static_cast<int64_t>(it.n) > a.T) {
+                it.seq = -2;
+                return it;
+            }
+            it.rows = min(rows, it.n * group - it.first_row);
+            const int lo = keys_of(a, it.n, it.kv, it.first_row / group).lo;
+            const int hi = keys_of(a, it.n, it.kv, (it.first_row + it.rows - 1) / group).hi;
+            const int64_t p0 = lo / bn * bn + static_cast<int64_t>(it.piece) * piece_len;
+            it.key_lo = static_cast<int>(max(static_cast<int64_t>(lo), p0));
+            it.key_hi = static_cast<int>(min(static_cast<int64_t>(hi), p0 + piece_len));
+            return it;
+        }
+        f.before += __shfl_sync(0xffffffffu, f.incl, 31);
+        f.base += 256;
+        f.loaded = false;
+    }
+    return it;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -145,13 +217,21 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// TMA load of one box {64 channels, 1 head, slots, 1 page} of a cache.
 __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar,
                                             int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3, int32_t c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
 }
 
@@ -166,13 +246,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
-// Descriptor of an MN-major operand with 128-byte swizzle: blocks of 64 channels x all keys, `block`
-// bytes apart; within a block one key per 128-byte row, 8-key swizzle atoms 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t block) {
+// Keys and values lie in shared memory as [8 keys][64 channels]: one key per 128-byte row, 128-byte swizzle, the
+// blocks of 1024 bytes of the same 8 keys one after another, 8-key groups `group` bytes apart. The keys' product
+// reads them K-major, the values' product MN-major (its leading offset is the step to the next 64 channels).
+__device__ __forceinline__ uint64_t smem_desc_groups(uint32_t addr, uint32_t group) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(block >> 4) << 16;         // leading byte offset: next 64 channels
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;          // stride byte offset: next 8 keys
+    d |= static_cast<uint64_t>(1024 >> 4) << 16;
+    d |= static_cast<uint64_t>(group >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
@@ -186,39 +267,141 @@ struct AttnParts {
     int64_t rows;  // T * q_heads
 };
 
+// One warp's state in bringing keys or values.
+struct Stream {
+    int n;         // tiles so far, over all items
+    int tails;     // partly valid value tiles so far
+};
+
+// The key tiles k0, k0 + BN, ... (nt of them) of an item into the ring of KEYS or values, by TMA in boxes of
+// 2^box_log2 slots. The pages of 32 boxes are looked up at once, one per lane, while those before are in use, and
+// each box is issued by a lane of its own (one lane for all: 64 ragged sequences with pages of 16 slots took 273
+// instead of 204 us, a chunk of 4096 over 8192 keys 364 instead of 335). The last value tile is
+// cleared past the sequence's end before it counts: whatever stands there must not meet a probability of zero.
+template <class Cfg, bool KEYS>
+__device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, const fp8bs_paged_attention_args& a,
+                                            const Item& it, int k0, int nt, int box_log2, int mode, uint8_t* ring,
+                                            uint64_t* full, uint64_t* empty, uint64_t* tail, int2* window,
+                                            int lane) {
+    constexpr int STAGES = KEYS ? Cfg::KST : Cfg::VST;
+    constexpr int TILE = KEYS ? Cfg::K_TILE : Cfg::V_TILE;
+    constexpr int CH = (KEYS ? Cfg::DK : Cfg::DV) / 64;
+    constexpr int BN = Cfg::BN;
+    const int box = 1 << box_log2;
+    const int boxes = BN >> box_log2;
+    const int page_size = static_cast<int>(a.cache.page_size);
+    const int heads = static_cast<int>(a.cache.heads);
+    const int head = it.head, kv = it.kv;
+    const int32_t* table = a.page_table + it.seq * a.table_stride;
+    auto lookup = [&](int w) {               // boxes 32 w .. 32 w + 31 of the item
+        const int64_t key = k0 + (static_cast<int64_t>(w) * 32 + lane) * box;
+        int2 at = make_int2(0, 0);
+        if (key < kv) {
+            const int p = static_cast<int>(key) / page_size;
+            at.y = static_cast<int>(key) - p * page_size;
+            at.x = table[p];
+        }
+        return at;
+    };
+    int2 next = lookup(0);
+    for (int j = 0; j < nt; ++j) {
+        const int key0 = k0 + j * BN;
+        const int live = min(boxes, (kv - key0 + box - 1) >> box_log2);
+        const int st = s.n % STAGES;
+        if (!warp_wait(&empty[st], ((s.n / STAGES) & 1) ^ 1)) return false;
+        const bool partial = !KEYS && kv - key0 < BN;
+        uint64_t* bar = partial ? tail : &full[st];
+        const uint32_t dst = smem_addr(ring) + st * TILE;
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live * box * CH * 128));
+        for (int b = 0; b < live;) {
+            const int first = j * boxes + b;
+            if ((first & 31) == 0) {
+                // a page outside the cache: a coordinate past the end, which reads as zeros
+                if (static_cast<unsigned>(next.x) >= static_cast<unsigned>(a.cache.pages)) {
+                    next.x = static_cast<int>(a.cache.pages);
+                    if (KEYS && k0 + (first + lane) * int64_t{1} * box < kv) record_error(FP8BS_DEVERR_INDEX);
+                }
+                window[lane] = next;
+                next = lookup((first >> 5) + 1);
+                __syncwarp();
+            }
+            const int count = min(32 - (first & 31), live - b);
+            __syncwarp();
+            if (lane < count) {
+                const int2 at = window[(first + lane) & 31];
+                const int key = (b + lane) << box_log2;           // of the tile
+                if (mode == 0)
+                    tma_load_5d(dst + key * (CH * 128), map, bar, 0, 0, head * CH, at.y >> 3, at.x);
+                else if (mode == 1)
+                    tma_load_5d(dst + key * (CH * 128), map, bar, 0, 0, 0, at.y >> 3, at.x * heads + head);
+                else
+                    for (int c = 0; c < CH; ++c)
+                        tma_load_4d(dst + (key >> 3) * (CH * 1024) + c * 1024 + (key & 7) * 128, map, bar,
+                                    c * 64, head, at.y, at.x);
+            }
+            __syncwarp();
+            b += count;
+        }
+        if (partial) {
+            if (!warp_wait(tail, s.tails & 1)) return false;
+            ++s.tails;
+            const int keep = kv - key0;
+            for (int i = lane; i < (BN - keep) * CH * 8; i += 32) {
+                const int key = keep + i / (CH * 8);
+                const int c = i / 8 % CH;
+                *reinterpret_cast<uint4*>(ring + st * TILE + (key >> 3) * (CH * 1024) + c * 1024 +
+                                          (key & 7) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+        }
+        ++s.n;
+    }
+    return true;
+}
+
+// After a wait that ran out: the copies of the ring's last tiles, so that none is still writing shared memory
+// when the CTA ends.
+template <int STAGES>
+__device__ __forceinline__ void drain_tiles(const Stream& s, uint64_t* full) {
+    record_error(FP8BS_DEVERR_PRODUCER_WAIT);
+    for (int i = max(0, s.n - STAGES); i < s.n; ++i)
+        if (!mbar_wait(&full[i % STAGES], (i / STAGES) & 1, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+}
+
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV,
-                           const __grid_constant__ fp8bs_paged_attention_args a, const int box_log2,
-                           const int piece_len, const int pieces, const AttnParts parts) {
+                           const __grid_constant__ fp8bs_paged_attention_args a,
+                           const AttentionModes modes, const int piece_len, const int pieces, const AttnParts parts) {
     constexpr int DK = Cfg::DK, DV = Cfg::DV, NQ = Cfg::NQ, BN = Cfg::BN;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ RowTile s_tile;
+    __shared__ Item s_item[Cfg::SLOTS];
+    __shared__ int2 s_window[2][32];                      // (page, slot) of 32 boxes: keys', values'
     __shared__ uint32_t s_tmem;
     uint8_t* smem = align_1024(smem_raw);
     uint8_t* sQ = smem;                                   // [NQ][DK/64][128 rows][128 bytes]
-    uint8_t* sK = sQ + NQ * Cfg::Q_TILE;                  // [KST][DK/64][BN][128 bytes]
-    uint8_t* sV = sK + Cfg::KST * Cfg::K_TILE;            // [VST][DV/64][BN][128 bytes]
+    uint8_t* sK = sQ + NQ * Cfg::Q_TILE;                  // [KST][BN/8][DK/64][8 keys][128 bytes]
+    uint8_t* sV = sK + Cfg::KST * Cfg::K_TILE;            // [VST][BN/8][DV/64][8 keys][128 bytes]
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sV + Cfg::VST * Cfg::V_TILE);
     uint64_t* k_empty = k_full + Cfg::KST;
     uint64_t* v_full = k_empty + Cfg::KST;
     uint64_t* v_empty = v_full + Cfg::VST;
     uint64_t* s_full = v_empty + Cfg::VST;                // [SBUF]
-    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF][2 halves]
-    uint64_t* o_done = p_full + 2 * Cfg::SBUF;            // [NQ]
-    uint64_t* drain = o_done + NQ;                        // [NQ]
-    uint64_t* v_tail = drain + NQ;                        // the last, partly valid value tile
+    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF][PARTS]
+    uint64_t* q_full = p_full + Cfg::PARTS * Cfg::SBUF;   // [NQ] queries of an item
+    uint64_t* o_done = q_full + NQ;                       // [NQ] each product with V
+    uint64_t* o_last = o_done + NQ;                       // [NQ] the last one of an item
+    uint64_t* v_tail = o_last + NQ;                       // an item's last, partly valid value tile
+    uint64_t* i_full = v_tail + 1;                        // [SLOTS]
+    uint64_t* i_empty = i_full + Cfg::SLOTS;              // [SLOTS]
+    uint64_t* drain = i_empty + Cfg::SLOTS;               // all products, when given up
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int heads = static_cast<int>(a.cache.heads);
     const int group = static_cast<int>(a.q_heads / a.cache.heads);
-    // heads fastest: neighbouring CTAs read the same slots; later tiles (longer keys) first
-    const int64_t tiles = gridDim.x / heads;
-    const int64_t tile = tiles - 1 - blockIdx.x / heads;
-    const int head = blockIdx.x % heads;
-    const int piece = blockIdx.y;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < Cfg::KST; ++i) {
@@ -231,411 +414,257 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         }
         for (int i = 0; i < Cfg::SBUF; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[2 * i], 4);
-            mbar_init(&p_full[2 * i + 1], 4);
+            for (int k = 0; k < Cfg::PARTS; ++k) mbar_init(&p_full[Cfg::PARTS * i + k], 4);
         }
         for (int i = 0; i < NQ; ++i) {
+            mbar_init(&q_full[i], 4);
             mbar_init(&o_done[i], 1);
-            mbar_init(&drain[i], 1);
+            mbar_init(&o_last[i], 1);
         }
         mbar_init(v_tail, 1);
+        mbar_init(drain, 1);
+        for (int i = 0; i < Cfg::SLOTS; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], Cfg::SOFT_WARPS + 2);
+        }
         fence_barrier_init();
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
-    }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (warp == 0) {
-        const RowTile t = find_row_tile(a, tile, group, Cfg::ROWS, lane);
-        if (lane == 0) {
-            s_tile = t;
-            if (t.seq >= 0 && (t.n > a.max_q_len || t.kv > a.max_kv_len || t.kv < 0 ||
-                               t.q0 < 0 || t.q0 + static_cast<int64_t>(t.n) > a.T)) {
-                record_error(FP8BS_DEVERR_INDEX);
-                s_tile.seq = -1;
-            }
-        }
     }
     if (warp == Cfg::MMA_WARP) tmem_alloc(&s_tmem, Cfg::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const RowTile rt = s_tile;
+    grid_dependency_wait();
+    grid_launch_dependents();
 
-    // Keys of the tile: [key_lo, key_hi) over all its rows, cut to this piece, in whole key tiles.
-    const int rows_all = rt.n * group;
-    const int rows = min(Cfg::ROWS, rows_all - rt.first_row);       // valid rows of this CTA
-    int key_lo = 0, key_hi = 0;
-    if (rt.seq >= 0) {
-        key_lo = keys_of(a, rt.n, rt.kv, rt.first_row / group).lo;
-        key_hi = keys_of(a, rt.n, rt.kv, (rt.first_row + rows - 1) / group).hi;
-        const int64_t p0 = static_cast<int64_t>(piece) * piece_len;
-        key_lo = static_cast<int>(max(static_cast<int64_t>(key_lo), p0));
-        key_hi = static_cast<int>(min(static_cast<int64_t>(key_hi), p0 + piece_len));
-    }
-    const int k0 = key_lo / BN * BN;
-    const int nt = key_hi > key_lo ? (key_hi - k0 + BN - 1) / BN : 0;
+    // An item's key tiles start here, and are so many.
+    auto first_tile = [](const Item& it) { return it.key_lo / BN * BN; };
+    auto key_tiles = [&](const Item& it) {
+        return it.key_hi > it.key_lo ? (it.key_hi - first_tile(it) + BN - 1) / BN : 0;
+    };
+    // The x-th item of this CTA (x counts from 0), for the other warps: to be waited for, and given back.
+    auto item_ready = [&](int x) { return warp_wait(&i_full[x % Cfg::SLOTS], (x / Cfg::SLOTS) & 1); };
+    auto item_done = [&](int x) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[x % Cfg::SLOTS]);
+    };
 
-    if (rt.seq >= 0 && nt == 0) {
-        // No key for any row: zeros (or, of several pieces, an empty part).
-        for (int r = threadIdx.x; r < rows; r += Cfg::THREADS) {
-            const int pr = rt.first_row + r;
-            const int64_t row =
-                (rt.q0 + pr / group) * a.q_heads + head * group + pr % group;
-            if (pieces > 1) {
-                parts.ml[piece * parts.rows + row] = make_float2(-INFINITY, 0.0f);
-            } else {
-                uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * DV);
-                for (int c = 0; c < DV / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
-                if (a.lse) a.lse[row] = -INFINITY;
-            }
-        }
-    } else if (rt.seq >= 0) {
-        // Queries into shared memory (K-major, 128-byte swizzle); a negative scale turns their signs,
-        // so that the row maximum is always that of the largest S.
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-        for (int i = threadIdx.x; i < Cfg::ROWS * (DK / 8); i += Cfg::THREADS) {
-            const int r = i / (DK / 8);
-            const int c = i - r * (DK / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows) {
-                const int pr = rt.first_row + r;
-                const int tok = pr / group;
-                v = __ldg(reinterpret_cast<const uint4*>(
-                              static_cast<const __nv_bfloat16*>(a.q) +
-                              (rt.q0 + tok) * a.q_token_stride +
-                              (head * group + pr - tok * group) * a.q_head_stride) + c);
-                v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-            }
-            *reinterpret_cast<uint4*>(sQ + (r >> 7) * Cfg::Q_TILE + (c >> 3) * (128 * 128) +
-                                      (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();
-
-        if (warp == Cfg::LOAD_WARP) {
-            // ---- TMA producer: all lanes issue, lane l the boxes l, l + 32, ... of a tile.
-            const int box = 1 << box_log2;
-            const int boxes = BN >> box_log2;
-            const int page_size = static_cast<int>(a.cache.page_size);
-            const int32_t* table = a.page_table + rt.seq * a.table_stride;
-            const int per_lane = (boxes + 31) / 32;
-            constexpr int MAXB = BN / 32;
-            int page[MAXB], slot[MAXB];
-            auto lookup = [&](int j) {
+    // Two query tiles, registers: 168 x 384 threads at launch; the softmax's row of S needs more, the third
+    // warpgroup less (200 x 256 + 96 x 128 = 63488 of 64512).
+    if (warp < Cfg::SOFT_WARPS) {
+        if constexpr (NQ == 2) regs_inc<200>();
+        // ---- softmax warps: thread = row of query tile q
+        const int q = warp >> 2;
+        const int quarter = warp & 3;
+        const int r = q * 128 + quarter * 32 + lane;          // row of the item's tile
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
+        // (a scale of zero: any tiny factor keeps -inf apart from the finite scores)
+        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        // Queries of query tile q into shared memory (K-major, 128-byte swizzle), valid rows only (what the
+        // others hold is of no consequence: rows do not meet). A negative scale turns their signs, so that
+        // the row maximum is always that of the largest S.
+        auto load_queries = [&](const Item& it) {
+            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+            constexpr int PIECES = DK / 8;                           // 16-byte pieces of a row
+            constexpr int BATCH = 8;
+            const int here = max(0, min(128, it.rows - q * 128));
+            const int tid = threadIdx.x & 127;
+#pragma unroll 1
+            for (int i0 = tid; i0 < here * PIECES; i0 += 128 * BATCH) {
+                uint4 v[BATCH];
 #pragma unroll
-                for (int i = 0; i < MAXB; ++i) {
-                    const int b = lane + 32 * i;
-                    const int key = k0 + j * BN + b * box;
-                    page[i] = -1;
-                    slot[i] = 0;
-                    if (i < per_lane && b < boxes && key < rt.kv) {
-                        const int pg = key / page_size;
-                        slot[i] = key - pg * page_size;
-                        page[i] = table[pg];
+                for (int i = 0; i < BATCH; ++i) {
+                    const int e = i0 + i * 128;
+                    const int row = e / PIECES;
+                    if (row < here) {
+                        const int pr = it.first_row + q * 128 + row;
+                        const int tok = pr / group;
+                        v[i] = __ldg(reinterpret_cast<const uint4*>(
+                                         static_cast<const __nv_bfloat16*>(a.q) +
+                                         (it.q0 + tok) * a.q_token_stride +
+                                         (it.head * group + pr - tok * group) * a.q_head_stride) +
+                                     e % PIECES);
                     }
                 }
-            };
-            bool ok = true;
-            int kst = 0, vst = 0;
-            uint32_t kph = 0, vph = 0;
-            int k_issued = 0, v_issued = 0;
-            bool tail_issued = false;
-            lookup(0);
-            for (int j = 0; ok && j < nt; ++j) {
-                int pg[MAXB], sl[MAXB];
-                const int key0 = k0 + j * BN;
-                const int live = min(boxes, (rt.kv - key0 + box - 1) >> box_log2);
-                bool bad = false;
 #pragma unroll
-                for (int i = 0; i < MAXB; ++i) {
-                    pg[i] = page[i];
-                    sl[i] = slot[i];
-                    const int b = lane + 32 * i;
-                    // out of the cache: a coordinate past the end, which reads as zeros
-                    if (i < per_lane && b < live && (pg[i] < 0 || pg[i] >= a.cache.pages)) {
-                        bad = true;
-                        pg[i] = static_cast<int>(a.cache.pages);
+                for (int i = 0; i < BATCH; ++i) {
+                    const int e = i0 + i * 128;
+                    const int row = e / PIECES;
+                    const int ch = e % PIECES;
+                    if (row < here) {
+                        v[i].x ^= flip; v[i].y ^= flip; v[i].z ^= flip; v[i].w ^= flip;
+                        *reinterpret_cast<uint4*>(sQ + q * Cfg::Q_TILE + (ch >> 3) * (128 * 128) +
+                                                  row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v[i];
                     }
                 }
-                if (bad) record_error(FP8BS_DEVERR_INDEX);
-                if (j + 1 < nt) lookup(j + 1);
-                // keys
-                if (!warp_wait(&k_empty[kst], kph ^ 1)) { ok = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(&k_full[kst], static_cast<uint32_t>(live * box * DK * 2));
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < MAXB; ++i) {
-                    const int b = lane + 32 * i;
-                    if (i < per_lane && b < live)
-#pragma unroll
-                        for (int d = 0; d < DK / 64; ++d)
-                            tma_load_4d(smem_addr(sK) + kst * Cfg::K_TILE + d * (BN * 128) + b * box * 128,
-                                        &tmK, &k_full[kst], d * 64, head, sl[i], pg[i]);
-                }
-                ++k_issued;
-                if (++kst == Cfg::KST) { kst = 0; kph ^= 1; }
-                // values; those of the last tile are cleared past the sequence's end before they count
-                if (!warp_wait(&v_empty[vst], vph ^ 1)) { ok = false; break; }
-                const bool partial = rt.kv - key0 < BN;
-                uint64_t* bar = partial ? v_tail : &v_full[vst];
-                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live * box * DV * 2));
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < MAXB; ++i) {
-                    const int b = lane + 32 * i;
-                    if (i < per_lane && b < live)
-#pragma unroll
-                        for (int d = 0; d < DV / 64; ++d)
-                            tma_load_4d(smem_addr(sV) + vst * Cfg::V_TILE + d * (BN * 128) + b * box * 128,
-                                        &tmV, bar, d * 64, head, sl[i], pg[i]);
-                }
-                if (partial) {
-                    tail_issued = true;
-                    if (!warp_wait(v_tail, 0)) { ok = false; break; }
-                    const int keep = rt.kv - key0;
-                    for (int i = lane; i < (BN - keep) * 8 * (DV / 64); i += 32) {
-                        const int d = i / ((BN - keep) * 8);
-                        const int rem = i - d * (BN - keep) * 8;
-                        *reinterpret_cast<uint4*>(sV + vst * Cfg::V_TILE + d * (BN * 128) +
-                                                  keep * 128 + rem * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&v_full[vst]);
-                } else {
-                    ++v_issued;
-                }
-                if (++vst == Cfg::VST) { vst = 0; vph ^= 1; }
             }
-            if (!ok) {
-                // drain what is in flight before the CTA gives up its shared memory
-                if (lane == 0) {
-                    record_error(FP8BS_DEVERR_PRODUCER_WAIT);
-                    for (int i = max(0, k_issued - Cfg::KST); i < k_issued; ++i)
-                        if (!mbar_wait(&k_full[i % Cfg::KST], (i / Cfg::KST) & 1, kDrainLimitNs))
-                            record_error(FP8BS_DEVERR_DRAIN_WAIT);
-                    for (int i = max(0, v_issued - Cfg::VST); i < v_issued; ++i)
-                        if (!mbar_wait(&v_full[i % Cfg::VST], (i / Cfg::VST) & 1, kDrainLimitNs))
-                            record_error(FP8BS_DEVERR_DRAIN_WAIT);
-                    if (tail_issued && !mbar_wait(v_tail, 0, kDrainLimitNs))
-                        record_error(FP8BS_DEVERR_DRAIN_WAIT);
-                }
-            }
-        } else if (warp == Cfg::MMA_WARP) {
-            // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j) in two halves as the softmax
-            // hands them over, then S of the tile's next keys, which takes P's place (the tensor core
-            // works in order). With two query tiles one's products run under the other's softmax.
-            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV) | kIdescBMajorMN;
-            const uint32_t q_addr = smem_addr(sQ);
-            const uint32_t o_tmem = tmem + Cfg::SBUF * BN;
-            bool ok = true;
-            int ended = 0;                 // query tiles whose last product has been committed
-            auto qk = [&](int q, int j) {  // S(j): buffer q (two tiles) or j % 2
-                const int st = j % Cfg::KST;
-                if (q == 0) {
-                    if (!warp_wait(&k_full[st], (j / Cfg::KST) & 1)) return false;
-                    tc_fence_after();
-                }
-                const int buf = NQ == 2 ? q : j & 1;
-                const uint32_t k_addr = smem_addr(sK) + st * Cfg::K_TILE;
-                if (elect_one()) {
-#pragma unroll
-                    for (int d = 0; d < DK / 16; ++d)
-                        mma_bf16(tmem + buf * BN,
-                                 smem_desc_k_sw128(q_addr + q * Cfg::Q_TILE + (d / 4) * (128 * 128) +
-                                                   (d % 4) * 32),
-                                 smem_desc_k_sw128(k_addr + (d / 4) * (BN * 128) + (d % 4) * 32),
-                                 idesc_qk, d > 0 ? 1u : 0u);
-                    mma_commit(&s_full[buf]);
-                    if (q == NQ - 1) mma_commit(&k_empty[st]);
-                }
-                __syncwarp();
-                return true;
-            };
-            for (int q = 0; ok && q < NQ; ++q) ok = qk(q, 0);
-            if (ok && NQ == 1 && nt > 1) ok = qk(0, 1);
-            for (int j = 0; ok && j < nt; ++j) {
-                const int st = j % Cfg::VST;
-                const uint32_t pph = NQ == 2 ? j & 1 : (j >> 1) & 1;
-                const uint32_t v_addr = smem_addr(sV) + st * Cfg::V_TILE;
-                if (!warp_wait(&v_full[st], (j / Cfg::VST) & 1)) {
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const int buf = NQ == 2 ? q : j & 1;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!ok || !warp_wait(&p_full[2 * buf + half], pph)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = half * (BN / 32); k < (half + 1) * (BN / 32); ++k)
-                                mma_bf16_ta(o_tmem + q * DV, tmem + buf * BN + 8 * k,
-                                            smem_desc_mn_sw128(v_addr + k * 2048, BN * 128), idesc_pv,
-                                            j > 0 || k > 0 ? 1u : 0u);
-                            if (half == 1) {
-                                mma_commit(&o_done[q]);
-                                if (q == NQ - 1) mma_commit(&v_empty[st]);
-                                if (j == nt - 1) mma_commit(&drain[q]);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    if (!ok) break;
-                    if (j == nt - 1) ++ended;
-                    const int next = NQ == 2 ? j + 1 : j + 2;
-                    if (next < nt) ok = qk(q, next);
-                }
-            }
-            if (!ok && lane == 0) record_error(FP8BS_DEVERR_MMA_WAIT);
-            if (elect_one())
-                for (int q = ended; q < NQ; ++q) mma_commit(&drain[q]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            for (int q = 0; q < NQ; ++q)
-                if (!warp_wait(&drain[q], 0) && lane == 0) record_error(FP8BS_DEVERR_DRAIN_WAIT);
-        } else {
-            // ---- softmax warps: thread = row
-            const int q = warp >> 2;
-            const int quarter = warp & 3;
-            const int r = q * 128 + quarter * 32 + lane;          // row of the CTA
-            const bool idle = q * 128 + quarter * 32 >= rows;     // no valid row in this warp
-            const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-            const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
-            // (a scale of zero: any tiny factor keeps -inf apart from the finite scores)
-            const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-            const int pr = rt.first_row + min(r, rows - 1);
-            const KeyRange kr = keys_of(a, rt.n, rt.kv, pr / group);
-            // tiles that need no mask for any row of this warp's query tile
-            const int last_row = min(rows, (q + 1) * 128) - 1;
-            const int full_hi = keys_of(a, rt.n, rt.kv, (rt.first_row + min(q * 128, rows - 1)) / group).hi;
-            const int full_lo = keys_of(a, rt.n, rt.kv, (rt.first_row + max(last_row, 0)) / group).lo;
-            const int row_lo = max(kr.lo, key_lo), row_hi = min(kr.hi, key_hi);
+            if (lane == 0) mbar_arrive(&q_full[q]);
+        };
+        // An item's output rows as (token, query head).
+        auto out_row = [&](const Item& it, int row) {
+            const int pr = it.first_row + row;
+            const int tok = pr / group;
+            return (it.q0 + tok) * a.q_heads + it.head * group + (pr - tok * group);
+        };
+        bool ok = true;
+        int n0 = 0, used = 0;
+        ok = item_ready(0);
+        if (ok && s_item[0].seq >= 0 && key_tiles(s_item[0]) > 0) load_queries(s_item[0]);
+        for (int x = 0; ok && s_item[x % Cfg::SLOTS].seq >= 0; ++x) {
+            const Item& it = s_item[x % Cfg::SLOTS];
+            const int nt = key_tiles(it);
+            const int k0 = first_tile(it);
+            const bool live = r < it.rows;
+            const bool idle = q * 128 + quarter * 32 >= it.rows;     // no valid row in this warp
+            if (live && it.piece == 0)
+                // pieces that this sequence does not have are empty
+                for (int p = it.pieces; p < pieces; ++p)
+                    parts.ml[p * parts.rows + out_row(it, r)] = make_float2(-INFINITY, 0.0f);
             float m = -INFINITY;           // maximum in use, raw score
             float l = 0.0f;
-            bool ok = true;
-            for (int j = 0; j < nt; ++j) {
-                const int buf = NQ == 2 ? q : j & 1;
-                const uint32_t sph = NQ == 2 ? j & 1 : (j >> 1) & 1;
-                if (!warp_wait(&s_full[buf], sph)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (!idle) {
-                    const uint32_t s_tmem_row = tmem + lanes + buf * BN;
-                    float s[BN];
-#pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) tmem_ld_32cols(s_tmem_row + 32 * i, s + 32 * i);
-#pragma unroll
-                    for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_32(s + 32 * i);
-                    const int kb = k0 + j * BN;
-                    if (kb < full_lo || kb < key_lo || kb + BN > full_hi || kb + BN > key_hi) {
-                        const int lo = row_lo - kb, hi = row_hi - kb;
-#pragma unroll
-                        for (int i = 0; i < BN; ++i)
-                            if (i < lo || i >= hi) s[i] = -INFINITY;
+            if (nt > 0) {
+                const KeyRange kr =
+                    keys_of(a, it.n, it.kv, (it.first_row + min(r, it.rows - 1)) / group);
+                // tiles that need no mask for any row of this query tile
+                const int last_row = min(it.rows, (q + 1) * 128) - 1;
+                const int full_hi = min(it.key_hi,
+                    keys_of(a, it.n, it.kv, (it.first_row + min(q * 128, it.rows - 1)) / group).hi);
+                const int full_lo = max(it.key_lo,
+                    keys_of(a, it.n, it.kv, (it.first_row + max(last_row, 0)) / group).lo);
+                const int row_lo = max(kr.lo, it.key_lo), row_hi = min(kr.hi, it.key_hi);
+                for (int j = 0; j < nt; ++j) {
+                    const int n = n0 + j;
+                    const int buf = NQ == 2 ? q : n & 1;
+                    const uint32_t sph = NQ == 2 ? n & 1 : (n >> 1) & 1;
+                    if (!warp_wait(&s_full[buf], sph)) {
+                        ok = false;
+                        break;
                     }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
+                    tc_fence_after();
+                    if (!idle) {
+                        const uint32_t s_tmem_row = tmem + lanes + buf * BN;
+                        float s[BN];
 #pragma unroll
-                    for (int i = 4; i < BN; i += 4) {
-                        mx[0] = fmaxf(mx[0], s[i]);
-                        mx[1] = fmaxf(mx[1], s[i + 1]);
-                        mx[2] = fmaxf(mx[2], s[i + 2]);
-                        mx[3] = fmaxf(mx[3], s[i + 3]);
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float keep = grow ? exp2_fast((m - top) * c) : 1.0f;
-                        if (grow) m = top;
-                        l *= keep;
-                        if (j > 0) {
-                            if (!warp_wait(&o_done[q], (j - 1) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                        for (int i = 0; i < BN / 32; ++i) tmem_ld_32cols(s_tmem_row + 32 * i, s + 32 * i);
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_32(s + 32 * i);
+                        const int kb = k0 + j * BN;
+                        if (kb < full_lo || kb + BN > full_hi) {
+                            const int lo = row_lo - kb, hi = row_hi - kb;
+#pragma unroll
+                            for (int i = 0; i < BN; ++i)
+                                if (i < lo || i >= hi) s[i] = -INFINITY;
+                        }
+                        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int i = 4; i < BN; i += 4) {
+                            mx[0] = fmaxf(mx[0], s[i]);
+                            mx[1] = fmaxf(mx[1], s[i + 1]);
+                            mx[2] = fmaxf(mx[2], s[i + 2]);
+                            mx[3] = fmaxf(mx[3], s[i + 3]);
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float keep = grow ? exp2_fast((m - top) * c) : 1.0f;
+                            if (grow) m = top;
+                            l *= keep;
+                            if (j > 0) {
+                                if (!warp_wait(&o_done[q], (n - 1) & 1)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < DV / 32; ++i) {
-                                float o[32];
-                                tmem_ld_32cols(o_tmem + 32 * i, o);
-                                tmem_wait_ld_32(o);
+                                for (int i = 0; i < DV / 32; ++i) {
+                                    float o[32];
+                                    tmem_ld_32cols(o_tmem + 32 * i, o);
+                                    tmem_wait_ld_32(o);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= keep;
-                                tmem_st_32cols(o_tmem + 32 * i, reinterpret_cast<const uint32_t*>(o));
+                                    for (int k = 0; k < 32; ++k) o[k] *= keep;
+                                    tmem_st_32cols(o_tmem + 32 * i, reinterpret_cast<const uint32_t*>(o));
+                                }
                             }
                         }
-                    }
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                        const float mc = m == -INFINITY ? 0.0f : m * c;
+                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                        const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        constexpr int H = BN / 2;
+                        for (int part = 0; part < Cfg::PARTS; ++part) {
+                            constexpr int H = BN / Cfg::PARTS;
 #pragma unroll
-                        for (int i = 0; i < H / 32; ++i) {
-                            uint32_t p[16];
+                            for (int i = 0; i < H / 32; ++i) {
+                                uint32_t p[16];
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const int e = half * H + 32 * i + 2 * k;
-                                float2 x = __ffma2_rn(make_float2(s[e], s[e + 1]), c2, mc2);
-                                x.x = exp2_fast(x.x);
-                                x.y = exp2_fast(x.y);
-                                sum[k & 1] = __fadd2_rn(sum[k & 1], x);
-                                p[k] = pack_bf16x2(x.x, x.y);
+                                for (int k = 0; k < 16; ++k) {
+                                    const int e = part * H + 32 * i + 2 * k;
+                                    float2 y = __ffma2_rn(make_float2(s[e], s[e + 1]), c2, mc2);
+                                    y.x = exp2_fast(y.x);
+                                    y.y = exp2_fast(y.y);
+                                    sum[k & 1] = __fadd2_rn(sum[k & 1], y);
+                                    p[k] = pack_bf16x2(y.x, y.y);
+                                }
+                                tmem_st_16cols(s_tmem_row + part * (H / 2) + 16 * i, p);
                             }
-                            tmem_st_16cols(s_tmem_row + half * (H / 2) + 16 * i, p);
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_full[Cfg::PARTS * buf + part]);
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * buf + half]);
+                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    } else if (lane == 0) {
+                        for (int part = 0; part < Cfg::PARTS; ++part)
+                            mbar_arrive(&p_full[Cfg::PARTS * buf + part]);
                     }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                } else if (lane == 0) {
-                    mbar_arrive(&p_full[2 * buf]);
-                    mbar_arrive(&p_full[2 * buf + 1]);
                 }
+                n0 += nt;
             }
-            // every product of this query tile is done (o_done's parity would not tell: with two S
-            // buffers the last two products may complete before this warp looks)
-            if (ok && !warp_wait(&drain[q], 0)) ok = false;
-            if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
-            tc_fence_after();
+            // The next item's queries: every S of this one has been computed (this warp has seen the last),
+            // so their place is free, and the next S can be computed while this O is written out.
+            if (ok) ok = item_ready(x + 1);
+            const Item& next = s_item[(x + 1) % Cfg::SLOTS];
+            if (ok && next.seq >= 0 && key_tiles(next) > 0) load_queries(next);
+            if (nt > 0) {
+                if (ok && !warp_wait(&o_last[q], used & 1)) ok = false;
+                ++used;
+                tc_fence_after();
+            }
             if (ok && !idle) {
-                const int64_t row = (rt.q0 + pr / group) * a.q_heads + head * group + pr % group;
-                const bool live = r < rows;
+                const int64_t row = live ? out_row(it, r) : 0;
                 const float mc = m == -INFINITY ? -INFINITY : m * c;
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 if (pieces > 1) {
-                    float* dst = parts.o + (piece * parts.rows + row) * DV;
+                    float* dst = parts.o + (it.piece * parts.rows + row) * DV;
+                    if (nt > 0)
 #pragma unroll
-                    for (int i = 0; i < DV / 32; ++i) {
-                        float o[32];
-                        tmem_ld_32cols(o_tmem + 32 * i, o);
-                        tmem_wait_ld_32(o);
-                        if (live)
+                        for (int i = 0; i < DV / 32; ++i) {
+                            float o[32];
+                            tmem_ld_32cols(o_tmem + 32 * i, o);
+                            tmem_wait_ld_32(o);
+                            if (live)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                *reinterpret_cast<float4*>(dst + 32 * i + 4 * k) =
-                                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    }
-                    if (live) parts.ml[piece * parts.rows + row] = make_float2(mc, l);
+                                for (int k = 0; k < 8; ++k)
+                                    *reinterpret_cast<float4*>(dst + 32 * i + 4 * k) =
+                                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                    if (live) parts.ml[it.piece * parts.rows + row] = make_float2(mc, l);
                 } else {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * DV);
 #pragma unroll
                     for (int i = 0; i < DV / 32; ++i) {
                         float o[32];
-                        tmem_ld_32cols(o_tmem + 32 * i, o);
-                        tmem_wait_ld_32(o);
+                        if (nt > 0) {
+                            tmem_ld_32cols(o_tmem + 32 * i, o);
+                            tmem_wait_ld_32(o);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+                        }
                         if (live)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
@@ -649,6 +678,169 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         a.lse[row] = l > 0.0f ? (mc + log2_fast(l)) * 0.6931471805599453f : -INFINITY;
                 }
             }
+            tc_fence_before();
+            item_done(x);
+        }
+        if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
+    } else {
+        if constexpr (NQ == 2) regs_dec<96>();
+        if (warp == Cfg::KEY_WARP) {
+            // ---- hands out the items and brings their keys
+            ItemFinder finder;
+            finder.base = finder.before = 0;
+            finder.loaded = false;
+            bool ok = true;
+            Stream ks = {0, 0};
+            int x = 0;
+            for (int64_t round = 0; ok; ++round) {
+                // every other round backwards: long items and short ones even out
+                const int64_t at = round * gridDim.x +
+                                   (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                const Item it = find_item(finder, a, static_cast<int>(min(at, int64_t{INT32_MAX})), Cfg::ROWS,
+                                          BN, piece_len, lane);
+                if (it.seq == -2) {
+                    if (lane == 0) record_error(FP8BS_DEVERR_INDEX);
+                    continue;
+                }
+                if (!warp_wait(&i_empty[x % Cfg::SLOTS], ((x / Cfg::SLOTS) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    s_item[x % Cfg::SLOTS] = it;
+                    mbar_arrive(&i_full[x % Cfg::SLOTS]);
+                }
+                __syncwarp();
+                ++x;
+                if (it.seq < 0) break;
+                const int nt = key_tiles(it);
+                if (nt == 0) continue;
+                // (the first queries come first: behind a full ring of keys they take several times as long)
+                if (ks.n == 0)
+                    for (int q = 0; ok && q < NQ; ++q) ok = warp_wait(&q_full[q], 0);
+                ok = ok && bring_tiles<Cfg, true>(ks, &tmK, a, it, first_tile(it), nt, modes.box_log2, modes.k, sK,
+                                                  k_full, k_empty, nullptr, s_window[0], lane);
+            }
+            if (!ok && lane == 0) drain_tiles<Cfg::KST>(ks, k_full);
+        } else if (warp == Cfg::VALUE_WARP) {
+            // ---- brings the items' values
+            bool ok = true;
+            Stream vs = {0, 0};
+            for (int x = 0; ok; ++x) {
+                ok = item_ready(x);
+                if (!ok) break;
+                const Item it = s_item[x % Cfg::SLOTS];
+                item_done(x);
+                if (it.seq < 0) break;
+                const int nt = key_tiles(it);
+                if (nt == 0) continue;
+                if (vs.n == 0)
+                    for (int q = 0; ok && q < NQ; ++q) ok = warp_wait(&q_full[q], 0);
+                ok = ok && bring_tiles<Cfg, false>(vs, &tmV, a, it, first_tile(it), nt, modes.box_log2, modes.v,
+                                                   sV, v_full, v_empty, v_tail, s_window[1], lane);
+            }
+            if (!ok && lane == 0) {
+                drain_tiles<Cfg::VST>(vs, v_full);
+                mbar_wait(v_tail, vs.tails & 1, kDrainLimitNs);
+            }
+        } else if (warp == Cfg::MMA_WARP) {
+            // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j) in the parts that the softmax hands
+            // over, then S of the tile's next keys, which takes P's place (the tensor core works in order).
+            // With two query tiles one's products run under the other's softmax.
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV) | kIdescBMajorMN;
+            // descriptors of the first stages; those of other stages and steps lie at constant distances (in
+            // units of 16 bytes, which do not carry out of the address field)
+            const uint64_t q_desc = smem_desc_k_sw128(smem_addr(sQ));
+            const uint64_t k_desc = smem_desc_groups(smem_addr(sK), DK / 64 * 1024);
+            const uint64_t v_desc = smem_desc_groups(smem_addr(sV), DV / 64 * 1024);
+            const uint32_t o_tmem = tmem + Cfg::SBUF * BN;
+            bool ok = true;
+            int n0 = 0;                        // key tiles of the items before
+            int used = 0;                      // items with keys before
+            // S(n): buffer q (two tiles) or n % 2, keys of tile n
+            auto qk = [&](int q, int n) {
+                const int st = n % Cfg::KST;
+                if (q == 0) {
+                    if (!warp_wait(&k_full[st], (n / Cfg::KST) & 1)) return false;
+                    tc_fence_after();
+                }
+                const int buf = NQ == 2 ? q : n & 1;
+                const uint64_t kd = k_desc + static_cast<uint32_t>(st * (Cfg::K_TILE / 16));
+                if (elect_one()) {
+#pragma unroll
+                    for (int d = 0; d < DK / 16; ++d)
+                        mma_bf16(tmem + buf * BN,
+                                 q_desc + (q * Cfg::Q_TILE + (d / 4) * (128 * 128) + (d % 4) * 32) / 16,
+                                 kd + ((d / 4) * 1024 + (d % 4) * 32) / 16, idesc_qk, d > 0 ? 1u : 0u);
+                    mma_commit(&s_full[buf]);
+                    if (q == NQ - 1) mma_commit(&k_empty[st]);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (int x = 0; ok; ++x) {
+                if (!item_ready(x)) {
+                    ok = false;
+                    break;
+                }
+                const int seq = s_item[x % Cfg::SLOTS].seq;
+                const int nt = __shfl_sync(0xffffffffu, key_tiles(s_item[x % Cfg::SLOTS]), 0);
+                item_done(x);
+                if (seq < 0) break;
+                if (nt == 0) continue;
+                for (int q = 0; ok && q < NQ; ++q)
+                    ok = warp_wait(&q_full[q], used & 1) && qk(q, n0);
+                if (ok && NQ == 1 && nt > 1) ok = qk(0, n0 + 1);
+                for (int j = 0; ok && j < nt; ++j) {
+                    const int n = n0 + j;
+                    const int st = n % Cfg::VST;
+                    const uint32_t pph = NQ == 2 ? n & 1 : (n >> 1) & 1;
+                    const uint64_t vd = v_desc + static_cast<uint32_t>(st * (Cfg::V_TILE / 16));
+                    if (!warp_wait(&v_full[st], (n / Cfg::VST) & 1)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        const int buf = NQ == 2 ? q : n & 1;
+#pragma unroll
+                        for (int part = 0; part < Cfg::PARTS; ++part) {
+                            if (!ok || !warp_wait(&p_full[Cfg::PARTS * buf + part], pph)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int k = part * (BN / 16 / Cfg::PARTS);
+                                     k < (part + 1) * (BN / 16 / Cfg::PARTS); ++k)
+                                    mma_bf16_ta(o_tmem + q * DV, tmem + buf * BN + 8 * k,
+                                                vd + k * (DV / 64 * 2048 / 16), idesc_pv,
+                                                j > 0 || k > 0 ? 1u : 0u);
+                                if (part == Cfg::PARTS - 1) {
+                                    mma_commit(&o_done[q]);
+                                    if (q == NQ - 1) mma_commit(&v_empty[st]);
+                                    if (j == nt - 1) mma_commit(&o_last[q]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        const int next = NQ == 2 ? j + 1 : j + 2;
+                        if (next < nt) ok = qk(q, n0 + next);
+                    }
+                }
+                n0 += nt;
+                ++used;
+            }
+            if (!ok) {
+                // abandoned: the products in flight still read shared memory; let them end
+                if (lane == 0) record_error(FP8BS_DEVERR_MMA_WAIT);
+                if (elect_one()) mma_commit(drain);
+                __syncwarp();
+                if (!warp_wait(drain, 0) && lane == 0) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+            }
         }
     }
     tc_fence_before();
@@ -657,35 +849,64 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     if (warp == Cfg::MMA_WARP) tmem_dealloc(tmem, Cfg::TMEM_COLS);
 }
 
-// Join the pieces of a row in key order: one warp per row, the pieces' maxima and sums across lanes,
-// then DV / 32 channels per lane.
-template <int DV>
+// Join the pieces of a row: WPR warps per row, warp w of them the pieces w, w + WPR, ... in key order, DV / 32
+// channels per lane; the warps' sums are added in warp order. Bound by latency when the rows are few: the pieces'
+// maxima and sums are read by all lanes at once, and no piece's load waits for another's.
+template <int DV, int WPR>
 __global__ void __launch_bounds__(128) attention_join_kernel(const AttnParts parts, int pieces,
                                                              __nv_bfloat16* out, float* lse) {
+    constexpr int PER = DV / 32;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= parts.rows) return;
+    const int warp = (threadIdx.x >> 5) % WPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / WPR) + (threadIdx.x >> 5) / WPR;
+    if (row >= parts.rows) return;               // (whole blocks where a row's warps meet)
+    // lane i: piece i * WPR + warp and, of more than 32 WPR pieces, every 32 WPR-th after it
     float top = -INFINITY;
     for (int p = lane; p < pieces; p += 32) top = fmaxf(top, parts.ml[p * parts.rows + row].x);
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    constexpr int PER = DV / 32;
     float o[PER] = {}, l = 0.0f;
-    if (top > -INFINITY) {
-        for (int p = 0; p < pieces; ++p) {
-            const float2 ml = parts.ml[p * parts.rows + row];
-            if (ml.x == -INFINITY) continue;
-            const float w = exp2_fast(ml.x - top);
-            l = fmaf(w, ml.y, l);
-            const float* src = parts.o + (p * parts.rows + row) * DV + PER * lane;
-#pragma unroll
-            for (int i = 0; i < PER; i += 2) {
-                const float2 v = *reinterpret_cast<const float2*>(src + i);
-                o[i] = fmaf(w, v.x, o[i]);
-                o[i + 1] = fmaf(w, v.y, o[i + 1]);
+    for (int base = 0; base < pieces; base += 32 * WPR) {
+        const int mine = base + WPR * lane + warp;
+        float w = 0.0f;
+        if (mine < pieces) {
+            const float2 ml = parts.ml[mine * parts.rows + row];
+            if (ml.x > -INFINITY) {
+                w = exp2_fast(ml.x - top);
+                l = fmaf(w, ml.y, l);
             }
+        }
+        const int count = min(32, (pieces - base - warp + WPR - 1) / WPR);
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (wi > 0.0f) {                     // (an empty piece's O has not been written)
+                const float* src = parts.o + ((base + WPR * i + warp) * parts.rows + row) * DV + PER * lane;
+#pragma unroll
+                for (int k = 0; k < PER; k += 2) {
+                    const float2 f = *reinterpret_cast<const float2*>(src + k);
+                    o[k] = fmaf(wi, f.x, o[k]);
+                    o[k + 1] = fmaf(wi, f.y, o[k + 1]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+    if constexpr (WPR > 1) {
+        __shared__ float s_o[WPR][DV];
+        __shared__ float s_l[WPR];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) s_o[warp][PER * lane + k] = o[k];
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 1; w < WPR; ++w) {
+            l += s_l[w];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) o[k] += s_o[w][PER * lane + k];
         }
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -721,19 +942,27 @@ AttnParts attention_parts(const fp8bs_paged_attention_args& a, const AttentionPl
 
 template <class Cfg>
 cudaError_t launch_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                             const fp8bs_paged_attention_args& a, int box_log2,
-                             const AttentionPlan& plan, cudaStream_t stream) {
+                             const fp8bs_paged_attention_args& a, const AttentionModes& modes,
+                             const AttentionPlan& plan, int num_sms, cudaStream_t stream) {
     auto kernel = paged_attention_kernel<Cfg>;
     cudaError_t e = set_smem(kernel, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     const AttnParts parts = attention_parts(a, plan);
-    const dim3 grid(static_cast<unsigned>(tile_bound(a, Cfg::ROWS) * a.cache.heads),
-                    static_cast<unsigned>(plan.pieces));
-    e = launch_pdl(kernel, grid, Cfg::THREADS, Cfg::SMEM, stream, tmK, tmV, a, box_log2, plan.piece_len,
+    const int64_t items = tile_bound(a, Cfg::ROWS) * a.cache.heads * plan.pieces;
+    if (items >= INT32_MAX) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
+    e = launch_pdl(kernel, grid, Cfg::THREADS, Cfg::SMEM, stream, tmK, tmV, a, modes, plan.piece_len,
                    plan.pieces, parts);
     if (e != cudaSuccess || plan.pieces == 1) return e;
-    return launch_pdl(attention_join_kernel<Cfg::DV>, static_cast<unsigned>((parts.rows + 3) / 4), 128, 0,
-                      stream, parts, plan.pieces, static_cast<__nv_bfloat16*>(a.out), a.lse);
+    // Many pieces of few rows: four warps a row; else a warp each (more blocks than the GPU holds at once would
+    // keep the next kernel from starting: 4096 rows of 8 pieces took 30 us with four warps each, none to be seen
+    // with one).
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+    if (parts.rows <= 1024)
+        return launch_pdl(attention_join_kernel<Cfg::DV, 4>, static_cast<unsigned>(parts.rows), 128, 0, stream,
+                          parts, plan.pieces, out, a.lse);
+    return launch_pdl(attention_join_kernel<Cfg::DV, 1>, static_cast<unsigned>((parts.rows + 3) / 4), 128, 0,
+                      stream, parts, plan.pieces, out, a.lse);
 }
 
 }  // namespace
@@ -741,31 +970,31 @@ cudaError_t launch_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
     const bool two = two_tiles(a);
     const int64_t items = tile_bound(a, two ? 256 : 128) * a.cache.heads;
-    const int64_t slots = static_cast<int64_t>(num_sms) * (!two && a.cache.dk <= 128 ? 2 : 1);
-    const int64_t keys = a.max_kv_len > 0 ? a.max_kv_len : 1;
-    AttentionPlan p;
-    int64_t len;
+    int64_t keys = key_span(a, two ? 256 : 128, a.max_q_len, a.max_kv_len);
+    if (keys < 1) keys = 1;
+    int64_t len = keys;
     if (two) {
-        // chunks: only to fill the GPU, in pieces long enough to pay for the joining
-        const int64_t want = items >= slots ? 1 : slots / items;
-        len = (keys + want - 1) / want;
-        if (len < 512) len = 512;
-    } else {
-        // few rows: as many pieces as fill the GPU once, and none so long that the longest sequence
-        // of a ragged batch finishes last on its own
-        len = (items * keys + slots - 1) / slots;
-        if (len > 1024) len = 1024;
-        if (len < 128) len = 128;
-        if (items >= 8 * slots) len = keys;
+        // chunks that do not fill the GPU: the number of pieces with the lowest time, in keys, of the busiest
+        // CTA, where a piece costs as much as 512 keys more (queries, output, its part of the join)
+        int64_t best = keys;
+        for (int64_t p = 2; items < num_sms && p <= 16 && keys / p >= 256; ++p) {
+            const int64_t l = ((keys + p - 1) / p + 127) / 128 * 128;
+            const int64_t time = (items * p + num_sms - 1) / num_sms * (l + 512);
+            if (time < best) {
+                best = time;
+                len = l;
+            }
+        }
+    } else if (items < 8 * num_sms) {
+        // few rows: one CTA's share of all keys; many shares' worth in pieces of 1024 at most, so that the
+        // longest sequence of a ragged batch does not finish last on its own
+        const int64_t share = (items * keys + num_sms - 1) / num_sms;
+        len = std::max<int64_t>(share < 4096 ? share : 1024, 128);
     }
-    len = (len + 127) / 128 * 128;
-    if (len > (int64_t{1} << 30)) len = int64_t{1} << 30;
+    len = std::min<int64_t>((len + 127) / 128 * 128, int64_t{1} << 30);
+    AttentionPlan p;
     p.piece_len = static_cast<int>(len);
     p.pieces = static_cast<int>((keys + len - 1) / len);
-    if (p.pieces > 65535) {
-        p.piece_len = static_cast<int>(((keys + 65534) / 65535 + 127) / 128 * 128);
-        p.pieces = static_cast<int>((keys + p.piece_len - 1) / p.piece_len);
-    }
     return p;
 }
 
@@ -776,27 +1005,44 @@ size_t attention_workspace(const fp8bs_paged_attention_args& a, const AttentionP
 }
 
 cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                   const fp8bs_paged_attention_args& a, int box_log2,
-                                   const AttentionPlan& plan, cudaStream_t stream) {
+                                   const fp8bs_paged_attention_args& a, const AttentionModes& modes,
+                                   const AttentionPlan& plan, int num_sms, cudaStream_t stream) {
     const bool two = two_tiles(a);
     switch (a.cache.dk) {
         case 64:
-            return two ? launch_attention<AttnCfg<64, 64, 2>>(tmK, tmV, a, box_log2, plan, stream)
-                       : launch_attention<AttnCfg<64, 64, 1>>(tmK, tmV, a, box_log2, plan, stream);
+            return two ? launch_attention<AttnCfg<64, 64, 2>>(tmK, tmV, a, modes, plan, num_sms, stream)
+                       : launch_attention<AttnCfg<64, 64, 1>>(tmK, tmV, a, modes, plan, num_sms, stream);
         case 128:
-            return two ? launch_attention<AttnCfg<128, 128, 2>>(tmK, tmV, a, box_log2, plan, stream)
-                       : launch_attention<AttnCfg<128, 128, 1>>(tmK, tmV, a, box_log2, plan, stream);
+            return two ? launch_attention<AttnCfg<128, 128, 2>>(tmK, tmV, a, modes, plan, num_sms, stream)
+                       : launch_attention<AttnCfg<128, 128, 1>>(tmK, tmV, a, modes, plan, num_sms, stream);
         default:
-            return two ? launch_attention<AttnCfg<192, 128, 2>>(tmK, tmV, a, box_log2, plan, stream)
-                       : launch_attention<AttnCfg<192, 128, 1>>(tmK, tmV, a, box_log2, plan, stream);
+            return two ? launch_attention<AttnCfg<192, 128, 2>>(tmK, tmV, a, modes, plan, num_sms, stream)
+                       : launch_attention<AttnCfg<192, 128, 1>>(tmK, tmV, a, modes, plan, num_sms, stream);
     }
 }
 
-int attention_box_log2(int64_t page_size) {
-    // slots per TMA box: the largest power of two that divides the page and the key tiles (64 or 128)
-    int l = 0;
-    while (l < 6 && page_size % (int64_t{2} << l) == 0) ++l;
-    return l;
+namespace {
+
+// How a cache's rows of `d` channels can be fetched (AttentionModes).
+int fetch_mode(const fp8bs_kv_cache& c, int64_t d, int64_t head_stride, int64_t page_stride) {
+    if (c.page_size % 8 != 0) return 2;
+    if (c.heads == 1 || head_stride == d) return 0;
+    if (c.pages == 1 || page_stride == c.heads * head_stride)
+        return c.pages * c.heads < (int64_t{1} << 31) ? 1 : 2;
+    return 2;
+}
+
+}  // namespace
+
+AttentionModes attention_modes(const fp8bs_kv_cache& c) {
+    AttentionModes m;
+    m.k = fetch_mode(c, c.dk, c.k_head_stride, c.k_page_stride);
+    m.v = fetch_mode(c, c.dv, c.v_head_stride, c.v_page_stride);
+    // slots per box: the largest power of two that divides the page and the smaller key tile
+    const int most = m.k == 2 || m.v == 2 ? 3 : 6;
+    m.box_log2 = 0;
+    while (m.box_log2 < most && c.page_size % (int64_t{2} << m.box_log2) == 0) ++m.box_log2;
+    return m;
 }
 
 cudaError_t read_error_attention(unsigned int* out, bool clear, cudaStream_t stream) {

@@ -194,12 +194,19 @@ struct AttentionPlan {
 };
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms);
 size_t attention_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan);
-// tmK, tmV: the cache as {channels, heads, slots, pages} with boxes {64, 1, 2^box_log2, 1} and
-// 128-byte swizzle.
-int attention_box_log2(int64_t page_size);
+// How keys and values are fetched, by mode:
+//   0  5-D map {64 channels, 8 slots, heads * d/64, page_size/8, pages}: pages of a multiple of 8 slots, heads
+//      next to one another
+//   1  5-D map {64 channels, 8 slots, d/64, page_size/8, pages * heads}: likewise, a page's heads one after another
+//   2  4-D map {d channels, heads, slots, pages}: any strides; 64 channels of at most 8 slots at a time
+// in boxes of 2^box_log2 slots (the same for both), 128-byte swizzle. Shared memory receives [8 slots][d/64].
+struct AttentionModes {
+    int k, v, box_log2;
+};
+AttentionModes attention_modes(const fp8bs_kv_cache& c);
 cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                   const fp8bs_paged_attention_args& a, int box_log2,
-                                   const AttentionPlan& plan, cudaStream_t stream);
+                                   const fp8bs_paged_attention_args& a, const AttentionModes& modes,
+                                   const AttentionPlan& plan, int num_sms, cudaStream_t stream);
 
 // Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
 constexpr int kMoeMaxTokens = 64;
