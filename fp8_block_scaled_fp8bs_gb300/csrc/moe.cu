@@ -21,9 +21,12 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int MOE_PROMOTE_WARP0 = 2;                  // warps 2..5 promote (TMEM lanes warp % 4)
-constexpr int MOE_ISSUER2 = 6;
-constexpr int MOE_THREADS = 7 * 32;
+// Warps of both kernels: 0 brings the stages, 1 and 10 issue the MMAs of the first and second weight tile of a
+// stage, 2..5 promote the first, 6..9 the second (TMEM lanes: warp % 4).
+constexpr int MOE_PROMOTE_WARP0 = 2;
+constexpr int MOE_PROMOTE_WARPS = 8;
+constexpr int MOE_ISSUER2 = MOE_PROMOTE_WARP0 + MOE_PROMOTE_WARPS;
+constexpr int MOE_THREADS = (MOE_ISSUER2 + 1) * 32;
 constexpr int MOE_NBUF = 4;                           // TMEM buffers (K blocks in flight)
 constexpr int kMaxExperts = 512;
 
@@ -92,17 +95,18 @@ struct ScaleStream {
     }
 };
 
-// Barrier 1 of the four promotion warps, and whether any of their threads failed: all of them learn of it
+// A named barrier of `THREADS` promotion threads, and whether any of their threads failed: all of them learn of it
 // together, so that none is left waiting.
-__device__ __forceinline__ bool promotion_any(bool failed) {
+template <int THREADS>
+__device__ __forceinline__ bool promotion_any(int barrier, bool failed) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, 1, 128, q;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"(failed ? 1 : 0)
+        : "r"(failed ? 1 : 0), "r"(barrier), "n"(THREADS)
         : "memory");
     return r != 0;
 }
@@ -120,19 +124,83 @@ __device__ __forceinline__ void promote(float* acc, const float* v, const float*
     }
 }
 
+// A stage of both kernels: two weight tiles and the activations they share.
 template <int MT>
-struct UpCfg {
+struct MoeCfg {
     static constexpr int X_TILE = MT * BK;
     static constexpr int STAGE = 2 * A_TILE + X_TILE;
+    static constexpr int F_BYTES = MT * 4;                   // (down) factors of the tokens
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(MOE_NBUF * 2 * MT);
-    static int fixed(int nkb) { return 1024 + nkb * MT * 4 + 4 * MT * 4 + moe_bar_bytes(kMaxStages); }
+    // shared memory beside the stages
+    static constexpr int up_fixed(int nkb) {
+        return 1024 + nkb * MT * 4 + 4 * MT * 4 + MT * BM * 4 + moe_bar_bytes(kMaxStages);
+    }
+    static constexpr int down_fixed() { return 1024 + kMaxStages * F_BYTES + moe_bar_bytes(kMaxStages); }
+    static int stages(int fixed) {
+        const int s = (kSmemLimit - 6144 - fixed) / STAGE;   // (Routing is static)
+        return s < kMaxStages ? s : kMaxStages;
+    }
 };
+
+// The MMAs of one weight tile of every stage: half 0 or 1.
+template <int MT>
+__device__ __forceinline__ void issue_half(int half, int total, int stages, const uint8_t* sW, const uint8_t* sX,
+                                           uint32_t tmem, const MoeBars& bar) {
+    constexpr uint32_t idesc = idesc_e4m3_f32(BM, MT);
+    const uint64_t w0 = smem_desc_k_sw128(smem_addr(sW) + half * A_TILE);
+    const uint64_t x0 = smem_desc_k_sw128(smem_addr(sX));
+    int st = 0;
+    uint32_t phase = 0;
+    for (int n = 0; n < total; ++n) {
+        const int buf = n % MOE_NBUF;
+        if (!mbar_wait(&bar.tempty[buf], ((n / MOE_NBUF) & 1) ^ 1) || !mbar_wait(&bar.full[st], phase)) {
+            record_error(FP8BS_DEVERR_MMA_WAIT);
+            break;
+        }
+        tc_fence_after();
+        const uint64_t w = w0 + static_cast<uint32_t>(st * (2 * A_TILE / 16));
+        const uint64_t x = x0 + static_cast<uint32_t>(st * (MT * BK / 16));
+        const uint32_t d = tmem + static_cast<uint32_t>((2 * buf + half) * MT);
+#pragma unroll
+        for (int j = 0; j < BK / MMA_K; ++j)
+            mma_f8(d, w + j * MMA_K / 16, x + j * MMA_K / 16, idesc, j > 0 ? 1u : 0u);
+        mma_commit(&bar.empty[st]);
+        mma_commit(&bar.tfull[buf]);
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+    mma_commit(bar.drain);
+    if (!mbar_wait(bar.drain, 0, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+}
+
+// One K block's partial of this thread's row, taken from TMEM (MT columns at t0), the buffer handed back, scaled
+// and added to acc.
+template <int MT>
+__device__ __forceinline__ void promote_block(float* acc, uint32_t t0, const float* xs, float s, uint64_t* tempty,
+                                              int lane) {
+    float v[MT];
+    if constexpr (MT == 16) {
+        tmem_ld_16cols(t0, v);
+        tmem_wait_ld_16(v);
+    } else {
+#pragma unroll
+        for (int c = 0; c < MT / 32; ++c) tmem_ld_32cols(t0 + 32 * c, v + 32 * c);
+#pragma unroll
+        for (int c = 0; c < MT / 32; ++c) tmem_wait_ld_32(v + 32 * c);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(tempty);
+    promote<MT>(acc, v, xs, s);
+}
 
 template <int MT>
 __global__ void __launch_bounds__(MOE_THREADS, 1)
     moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const MoeArgs a, const float* xs, uint8_t* h8, float* hs, const int stages) {
-    using Cfg = UpCfg<MT>;
+    using Cfg = MoeCfg<MT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Routing rt;
     __shared__ uint32_t s_tmem;
@@ -142,7 +210,8 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     uint8_t* sX = sW + stages * 2 * A_TILE;                  // [stages][MT x 128]
     float* sXs = reinterpret_cast<float*>(sX + stages * Cfg::X_TILE);   // [nkb][MT] scales of x
     float* sMax = sXs + nkb * MT;                            // [4][MT]
-    const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sMax + 4 * MT), stages);
+    float* sU = sMax + 4 * MT;                               // [MT][128] the up product, for the gate's warps
+    const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sU + MT * BM), stages);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -153,7 +222,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         }
         for (int i = 0; i < MOE_NBUF; ++i) {
             mbar_init(&bar.tfull[i], 2);
-            mbar_init(&bar.tempty[i], 4);
+            mbar_init(&bar.tempty[i], MOE_PROMOTE_WARPS);
         }
         mbar_init(bar.drain, 2);
         fence_barrier_init();
@@ -207,36 +276,13 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                         record_error(FP8BS_DEVERR_DRAIN_WAIT);
         }
     } else if (warp == 1 || warp == MOE_ISSUER2) {
-        if (lane == 0) {
-            const int half = warp == 1 ? 0 : 1;              // gate or up tile
-            constexpr uint32_t idesc = idesc_e4m3_f32(BM, MT);
-            for (int n = 0; n < total; ++n) {
-                const int st = n % stages;
-                const int buf = n % MOE_NBUF;
-                if (!mbar_wait(&bar.tempty[buf], ((n / MOE_NBUF) & 1) ^ 1) ||
-                    !mbar_wait(&bar.full[st], (n / stages) & 1)) {
-                    record_error(FP8BS_DEVERR_MMA_WAIT);
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t w = smem_addr(sW + (2 * st + half) * A_TILE);
-                const uint32_t x = smem_addr(sX + st * Cfg::X_TILE);
-                const uint32_t d = tmem + static_cast<uint32_t>((2 * buf + half) * MT);
-#pragma unroll
-                for (int j = 0; j < BK / MMA_K; ++j)
-                    mma_f8(d, smem_desc_k_sw128(w + j * MMA_K), smem_desc_k_sw128(x + j * MMA_K), idesc,
-                           j > 0 ? 1u : 0u);
-                mma_commit(&bar.empty[st]);
-                mma_commit(&bar.tfull[buf]);
-            }
-            mma_commit(bar.drain);
-            if (!mbar_wait(bar.drain, 0, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
-        }
+        if (lane == 0) issue_half<MT>(warp == 1 ? 0 : 1, total, stages, sW, sX, tmem, bar);
     } else {
+        const int half = (warp - MOE_PROMOTE_WARP0) >> 2;    // gate or up
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;                   // row of the tile = channel of the block
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        auto scale_of = [&](int n, int half) {
+        const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * MT);
+        auto scale_of = [&](int n) {
             if (n >= total) return 0.0f;
             const int m = n / nkb;
             const int item = blockIdx.x + m * gridDim.x;
@@ -245,74 +291,52 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                                   (item - act * iblocks);
             return __ldg(a.s13 + block * nkb + (n - m * nkb));
         };
-        auto gate_scale = [&](int n) { return scale_of(n, 0); };
-        auto up_scale = [&](int n) { return scale_of(n, 1); };
-        ScaleStream<decltype(gate_scale)> gs(lane, gate_scale);
-        ScaleStream<decltype(up_scale)> us(lane, up_scale);
+        ScaleStream<decltype(scale_of)> ws(lane, scale_of);
         bool ok = true;
         int n = 0;
-        for (int m = 0; ok && m < mine; ++m) {
-            float g[MT], u[MT];
+        for (int m = 0; m < mine; ++m) {
+            float g[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) g[i] = u[i] = 0.0f;
-            for (int kb = 0; kb < nkb; ++kb, ++n) {
-                const float sg = gs.at(n, lane, gate_scale);
-                const float su = us.at(n, lane, up_scale);
+            for (int i = 0; i < MT; ++i) g[i] = 0.0f;
+            for (int kb = 0; ok && kb < nkb; ++kb, ++n) {
+                const float s = ws.at(n, lane, scale_of);
                 const int buf = n % MOE_NBUF;
                 if (!warp_wait(&bar.tfull[buf], (n / MOE_NBUF) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t t0 = tmem + lanes + static_cast<uint32_t>(2 * buf * MT);
-                const float* xk = sXs + kb * MT;
-                if constexpr (MT == 16) {
-                    float v[16], w[16];
-                    tmem_ld_16cols(t0, v);
-                    tmem_ld_16cols(t0 + 16, w);
-                    tmem_wait_ld_16(v);
-                    tmem_wait_ld_16(w);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.tempty[buf]);
-                    promote<16>(g, v, xk, sg);
-                    promote<16>(u, w, xk, su);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < MT / 32; ++c) {
-                        float v[32], w[32];
-                        tmem_ld_32cols(t0 + 32 * c, v);
-                        tmem_ld_32cols(t0 + MT + 32 * c, w);
-                        tmem_wait_ld_32(v);
-                        tmem_wait_ld_32(w);
-                        if (c + 1 == MT / 32) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bar.tempty[buf]);
-                        }
-                        promote<32>(g + 32 * c, v, xk + 32 * c, sg);
-                        promote<32>(u + 32 * c, w, xk + 32 * c, su);
-                    }
-                }
+                promote_block<MT>(g, t0 + static_cast<uint32_t>(2 * buf * MT), sXs + kb * MT, s,
+                                  &bar.tempty[buf], lane);
             }
-            // h of this block of 128 channels: block maxima across the four warps, codes, factors
             const int item = blockIdx.x + m * gridDim.x;
             const int act = item / iblocks;
             const int ib = item - act * iblocks;
             const int e = rt.active[act];
             const unsigned long long mask = rt.mask[e];
+            // The up product goes to the gate's warps through shared memory (barrier 2: its place is free again).
+            if (half == 1) {
+                if (m > 0) asm volatile("bar.sync 2, 256;" ::: "memory");
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    if ((mask >> t) & 1) sU[t * BM + r] = g[t];
+            }
+            if (promotion_any<256>(1, !ok)) {
+                ok = false;
+                break;
+            }
+            if (half == 1) continue;
+            // h of this block of 128 channels: block maxima across the four warps, codes, factors
 #pragma unroll
             for (int t = 0; t < MT; ++t)
-                if (ok && ((mask >> t) & 1)) {
-                    g[t] = g[t] / (1.0f + expf(-g[t])) * u[t];
+                if ((mask >> t) & 1) {
+                    g[t] = g[t] / (1.0f + expf(-g[t])) * sU[t * BM + r];
                     const float mag = fmaxf(fabsf(g[t]), 0.0f);          // (NaN counts as nothing)
                     const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
                     if (lane == 0) sMax[quarter * MT + t] = __uint_as_float(top);
                 }
-            if (promotion_any(!ok)) {
-                ok = false;
-                break;
-            }
+            if (m + 1 < mine) asm volatile("bar.arrive 2, 256;" ::: "memory");
+            asm volatile("bar.sync 3, 128;" ::: "memory");
             uint8_t* out = h8 + static_cast<int64_t>(act) * a.T * a.I + ib * BK + r;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                 }
                 hs[(static_cast<int64_t>(act) * iblocks + ib) * kMoeMaxTokens + r] = f;
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");       // sMax is free again
+            asm volatile("bar.sync 3, 128;" ::: "memory");       // sMax is free again
         }
         if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
     }
@@ -347,48 +371,34 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, Cfg::TMEM_COLS);
 }
 
-template <int MT>
-struct DownCfg {
-    static constexpr int X_TILE = MT * BK;
-    static constexpr int F_BYTES = MT * 4;                   // factors of the tokens
-    static constexpr int STAGE = A_TILE + X_TILE;
-    static constexpr uint32_t TMEM_COLS = tmem_cols_for(MOE_NBUF * MT);
-    static constexpr int MAX_STAGES = 11;
-    static constexpr int FIXED = 1024 + moe_bar_bytes(MAX_STAGES);
-    static constexpr int fit = (kSmemLimit - 10240 - FIXED) / (STAGE + F_BYTES);   // (Routing is static)
-    static constexpr int STAGES = fit < MAX_STAGES ? fit : MAX_STAGES;
-    static constexpr int SMEM = FIXED + STAGES * (STAGE + F_BYTES);
-};
-
-// One cluster per 128 output channels; its C CTAs share the (expert, K block) units evenly and add their
-// sums in rank order.
+// One cluster per 256 output channels (two tiles of 128 rows, which share the activations); its C CTAs share the
+// (expert, K block) units evenly and add their sums in rank order.
 template <int MT>
 __global__ void __launch_bounds__(MOE_THREADS, 1)
     moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
-                    const MoeArgs a, const float* hs, const int C) {
-    using Cfg = DownCfg<MT>;
-    constexpr int S = Cfg::STAGES;
+                    const MoeArgs a, const float* hs, const int C, const int stages) {
+    using Cfg = MoeCfg<MT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Routing rt;
     __shared__ uint32_t s_tmem;
     uint8_t* smem = align_1024(smem_raw);
-    uint8_t* sW = smem;                                      // [S][128 x 128]
-    uint8_t* sX = sW + S * A_TILE;                           // [S][MT x 128]
-    float* sF = reinterpret_cast<float*>(sX + S * Cfg::X_TILE);   // [S][MT]
-    const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sF + S * MT), S);
+    uint8_t* sW = smem;                                      // [stages][2][128 x 128]
+    uint8_t* sX = sW + stages * 2 * A_TILE;                  // [stages][MT x 128]
+    float* sF = reinterpret_cast<float*>(sX + stages * Cfg::X_TILE);   // [stages][MT]
+    const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sF + stages * MT), stages);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int slab = blockIdx.x / C;
-    const int rank = blockIdx.x - slab * C;
+    const int pair = blockIdx.x / C;
+    const int rank = blockIdx.x - pair * C;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < stages; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], 1 + 4);
+            mbar_init(&bar.empty[i], 2 + MOE_PROMOTE_WARPS);
         }
         for (int i = 0; i < MOE_NBUF; ++i) {
-            mbar_init(&bar.tfull[i], 1);
-            mbar_init(&bar.tempty[i], 4);
+            mbar_init(&bar.tfull[i], 2);
+            mbar_init(&bar.tempty[i], MOE_PROMOTE_WARPS);
         }
         mbar_init(bar.drain, 2);
         fence_barrier_init();
@@ -411,33 +421,37 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         if (lane == 0) {
             const uint64_t keep = l2_policy_evict_last();
             const uint64_t stream = l2_policy_evict_first();
+            // (the second tile of the last pair may lie past D: it reads the next expert's rows, or zeros past
+            // the last one's, and is not stored)
             auto load_w = [&](int n) {
-                const int st = n % S;
+                const int st = n % stages;
                 const int act = (u0 + n) / nkb;
                 const int kb = u0 + n - act * nkb;
+                const int row = rt.active[act] * a.D + pair * 2 * BM;
+                uint8_t* w = sW + st * 2 * A_TILE;
                 mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE + Cfg::F_BYTES);
-                tma_load_2d_hint(sW + st * A_TILE, &tmW, &bar.full[st], kb * BK,
-                                 rt.active[act] * a.D + slab * BM, stream);
+                tma_load_2d_hint(w, &tmW, &bar.full[st], kb * BK, row, stream);
+                tma_load_2d_hint(w + A_TILE, &tmW, &bar.full[st], kb * BK, row + BM, stream);
             };
             auto load_h = [&](int n) {
-                const int st = n % S;
+                const int st = n % stages;
                 const int act = (u0 + n) / nkb;
                 const int kb = u0 + n - act * nkb;
                 tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmH, &bar.full[st], kb * BK, act * a.T, keep);
                 bulk_load(sF + st * MT, hs + (static_cast<int64_t>(act) * nkb + kb) * kMoeMaxTokens,
                           Cfg::F_BYTES, &bar.full[st]);
             };
-            const int ahead = min(S, total);
+            const int ahead = min(stages, total);
             for (int n = 0; n < ahead; ++n) load_w(n);
             grid_dependency_wait();
             grid_launch_dependents();
             for (int n = 0; n < ahead; ++n) load_h(n);
             int n = ahead;
             for (; n < total; ++n) {
-                if (!mbar_wait(&bar.empty[n % S], ((n / S) & 1) ^ 1)) {
+                if (!mbar_wait(&bar.empty[n % stages], ((n / stages) & 1) ^ 1)) {
                     record_error(FP8BS_DEVERR_PRODUCER_WAIT);
-                    for (int i = max(0, n - S); i < n; ++i)
-                        if (!mbar_wait(&bar.full[i % S], (i / S) & 1, kDrainLimitNs))
+                    for (int i = max(0, n - stages); i < n; ++i)
+                        if (!mbar_wait(&bar.full[i % stages], (i / stages) & 1, kDrainLimitNs))
                             record_error(FP8BS_DEVERR_DRAIN_WAIT);
                     break;
                 }
@@ -447,38 +461,17 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         }
     } else if (warp == 1 || warp == MOE_ISSUER2) {
         grid_dependency_wait();
-        if (lane == 0) {
-            const int me = warp == 1 ? 0 : 1;                // every other K block
-            constexpr uint32_t idesc = idesc_e4m3_f32(BM, MT);
-            for (int n = me; n < total; n += 2) {
-                const int st = n % S;
-                const int buf = n % MOE_NBUF;
-                if (!mbar_wait(&bar.tempty[buf], ((n / MOE_NBUF) & 1) ^ 1) ||
-                    !mbar_wait(&bar.full[st], (n / S) & 1)) {
-                    record_error(FP8BS_DEVERR_MMA_WAIT);
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t w = smem_addr(sW + st * A_TILE);
-                const uint32_t x = smem_addr(sX + st * Cfg::X_TILE);
-                const uint32_t d = tmem + static_cast<uint32_t>(buf * MT);
-#pragma unroll
-                for (int j = 0; j < BK / MMA_K; ++j)
-                    mma_f8(d, smem_desc_k_sw128(w + j * MMA_K), smem_desc_k_sw128(x + j * MMA_K), idesc,
-                           j > 0 ? 1u : 0u);
-                mma_commit(&bar.empty[st]);
-                mma_commit(&bar.tfull[buf]);
-            }
-            mma_commit(bar.drain);
-            if (!mbar_wait(bar.drain, 0, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
-        }
+        if (lane == 0) issue_half<MT>(warp == 1 ? 0 : 1, total, stages, sW, sX, tmem, bar);
     } else {
         grid_dependency_wait();
+        const int half = (warp - MOE_PROMOTE_WARP0) >> 2;
         const int quarter = warp & 3;
-        const int r = quarter * 32 + lane;                   // output channel of the slab
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const int r = quarter * 32 + lane;
+        const int slab = 2 * pair + half;                    // this thread's output channel: slab * 128 + r
+        const bool inside = slab * BM < a.D;
+        const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * MT);
         auto scale_of = [&](int n) {
-            if (n >= total) return 0.0f;
+            if (n >= total || !inside) return 0.0f;
             const int act = (u0 + n) / nkb;
             const int kb = u0 + n - act * nkb;
             return __ldg(a.s2 + (static_cast<int64_t>(rt.active[act]) * (a.D / BK) + slab) * nkb + kb);
@@ -488,57 +481,44 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i] = 0.0f;
         bool ok = true;
+        int st = 0;
+        uint32_t phase = 0;
         for (int n = 0; n < total; ++n) {
             const float s = ss.at(n, lane, scale_of);
             const int buf = n % MOE_NBUF;
-            const int st = n % S;
             // (the products are done, so the stage has landed; its barrier orders the factors' copy)
-            if (!warp_wait(&bar.tfull[buf], (n / MOE_NBUF) & 1) ||
-                !warp_wait(&bar.full[st], (n / S) & 1)) {
+            if (!warp_wait(&bar.tfull[buf], (n / MOE_NBUF) & 1) || !warp_wait(&bar.full[st], phase)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const uint32_t t0 = tmem + lanes + static_cast<uint32_t>(buf * MT);
-            const float* f = sF + st * MT;
-            if constexpr (MT == 16) {
-                float v[16];
-                tmem_ld_16cols(t0, v);
-                tmem_wait_ld_16(v);
-                tc_fence_before();
-                promote<16>(acc, v, f, s);
-            } else {
-#pragma unroll
-                for (int c = 0; c < MT / 32; ++c) {
-                    float v[32];
-                    tmem_ld_32cols(t0 + 32 * c, v);
-                    tmem_wait_ld_32(v);
-                    if (c + 1 == MT / 32) tc_fence_before();
-                    promote<32>(acc + 32 * c, v, f + 32 * c, s);
-                }
-            }
+            promote_block<MT>(acc, t0 + static_cast<uint32_t>(2 * buf * MT), sF + st * MT, s, &bar.tempty[buf],
+                              lane);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bar.tempty[buf]);
-                mbar_arrive(&bar.empty[st]);
+            if (lane == 0) mbar_arrive(&bar.empty[st]);
+            if (++st == stages) {
+                st = 0;
+                phase ^= 1;
             }
         }
         if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
         __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + slab * BM + r;
         if (C == 1) {
+            if (inside)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                if (t < a.T) y[static_cast<int64_t>(t) * a.D] = __float2bfloat16_rn(acc[t]);
+                for (int t = 0; t < MT; ++t)
+                    if (t < a.T) y[static_cast<int64_t>(t) * a.D] = __float2bfloat16_rn(acc[t]);
         } else {
-            // CTA q of the cluster adds up tokens q * per .. of every rank's sums: [rank][token][channel]
-            const int per = MT / C;
+            // CTA q of the cluster adds up tokens q * per .. of every rank's sums: [rank][token][256 channels]
+            const int per = (MT + C - 1) / C;
+            const int col = half * BM + r;
             const uint32_t recv = smem_addr(smem);
             cluster_sync();                                  // every CTA is done with its stages
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int q = t / per;
                 st_shared_cluster_f32(
-                    mapa_shared(recv + static_cast<uint32_t>(((rank * per + t - q * per) * BM + r) * 4),
+                    mapa_shared(recv + static_cast<uint32_t>(((rank * per + t - q * per) * 2 * BM + col) * 4),
                                 static_cast<uint32_t>(q)),
                     acc[t]);
             }
@@ -547,13 +527,13 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             for (int i = 0; i < per; ++i) {
                 const int t = rank * per + i;
                 if (t >= a.T) break;
-                float v = got[i * BM + r];
-                for (int q = 1; q < C; ++q) v += got[(q * per + i) * BM + r];
-                y[static_cast<int64_t>(t) * a.D] = __float2bfloat16_rn(v);
+                float v = got[i * 2 * BM + col];
+                for (int q = 1; q < C; ++q) v += got[(q * per + i) * 2 * BM + col];
+                if (inside) y[static_cast<int64_t>(t) * a.D] = __float2bfloat16_rn(v);
             }
         }
     }
-    if (C > 1 && !(warp >= MOE_PROMOTE_WARP0 && warp < MOE_PROMOTE_WARP0 + 4)) {
+    if (C > 1 && !(warp >= MOE_PROMOTE_WARP0 && warp < MOE_PROMOTE_WARP0 + MOE_PROMOTE_WARPS)) {
         cluster_sync();
         cluster_sync();
     }
@@ -566,32 +546,33 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
 template <int MT>
 cudaError_t launch_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspace& w, int num_sms,
                            cudaStream_t stream) {
+    using Cfg = MoeCfg<MT>;
     const int nkb = a.D / BK;
-    const int fixed = UpCfg<MT>::fixed(nkb) + 10240;         // Routing and a margin are static
-    int stages = (kSmemLimit - fixed) / UpCfg<MT>::STAGE;
-    if (stages > kMaxStages) stages = kMaxStages;
-    if (stages < 2) return cudaErrorInvalidValue;
-    const int smem = UpCfg<MT>::fixed(nkb) + stages * UpCfg<MT>::STAGE;
-    cudaError_t e = set_smem(moe_up_kernel<MT>, smem);
-    if (e == cudaSuccess) e = set_smem(moe_down_kernel<MT>, DownCfg<MT>::SMEM);
+    const int up_stages = Cfg::stages(Cfg::up_fixed(nkb));
+    const int down_stages = Cfg::stages(Cfg::down_fixed());
+    if (up_stages < 2 || down_stages < 2) return cudaErrorInvalidValue;
+    const int up_smem = Cfg::up_fixed(nkb) + up_stages * Cfg::STAGE;
+    const int down_smem = Cfg::down_fixed() + down_stages * Cfg::STAGE;
+    cudaError_t e = set_smem(moe_up_kernel<MT>, up_smem);
+    if (e == cudaSuccess) e = set_smem(moe_down_kernel<MT>, down_smem);
     if (e != cudaSuccess) return e;
     const int most_active = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
     const int64_t items = static_cast<int64_t>(most_active) * (a.I / BK);
     const int grid = static_cast<int>(items < num_sms ? items : num_sms);
     const float* xs = reinterpret_cast<const float*>(a.ws + w.xs);
     float* hs = reinterpret_cast<float*>(a.ws + w.hs);
-    e = launch_pdl(moe_up_kernel<MT>, grid, MOE_THREADS, smem, stream, m.w13, m.x8, a, xs, a.ws + w.h8, hs,
-                   stages);
+    e = launch_pdl(moe_up_kernel<MT>, grid, MOE_THREADS, up_smem, stream, m.w13, m.x8, a, xs, a.ws + w.h8, hs,
+                   up_stages);
     if (e != cudaSuccess) return e;
-    // The most CTAs per slab that still leave every cluster of the grid its own SMs.
-    const int slabs = a.D / BM;
-    int C = 1;
-    while (C < kMaxSplit && slabs * C * 2 <= num_sms && most_active * (a.I / BK) >= 2 * C) C *= 2;
-    while (C > 1 && max_active_clusters(reinterpret_cast<const void*>(moe_down_kernel<MT>), MOE_THREADS,
-                                        DownCfg<MT>::SMEM, C) < slabs)
-        C /= 2;
-    return launch_pdl_cluster(moe_down_kernel<MT>, dim3(slabs * C), MOE_THREADS, DownCfg<MT>::SMEM, stream, C,
-                              false, m.w2, m.h8, a, hs, C);
+    // The most CTAs per pair of slabs that leave every cluster of the grid its own SMs and each CTA work.
+    const int pairs = (a.D / BM + 1) / 2;
+    int C = kMaxSplit;
+    while (C > 1 && (static_cast<int64_t>(pairs) * C > num_sms || items < 2 * C ||
+                     max_active_clusters(reinterpret_cast<const void*>(moe_down_kernel<MT>), MOE_THREADS,
+                                         down_smem, C) < pairs))
+        --C;
+    return launch_pdl_cluster(moe_down_kernel<MT>, dim3(pairs * C), MOE_THREADS, down_smem, stream, C, false,
+                              m.w2, m.h8, a, hs, C, down_stages);
 }
 
 }  // namespace
