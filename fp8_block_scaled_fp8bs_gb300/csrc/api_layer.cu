@@ -225,7 +225,7 @@ int run_experts(const fp8bs::MoeWorkspace& ws, const float* weights, const int32
     fp8bs::MoeMaps m;
     const int mt = fp8bs::moe_token_rows(T);
     if (!make_map(&m.w13, w13, E * 2 * I, D, 128) || !make_map(&m.w2, w2, E * D, I, 128) ||
-        !make_map(&m.x8, a.ws + ws.x8, T, D, mt) || !make_map(&m.h8, a.ws + ws.h8, ws.active * T, I, mt))
+        !make_map(&m.x8, a.ws + ws.x8, T, D, mt > 16 ? 1 : mt) || !make_map(&m.h8, a.ws + ws.h8, ws.active * T, I, mt))
         return FP8BS_ERR_CUDA;
     return status_of(fp8bs::launch_moe_experts(m, a, ws, sms, static_cast<cudaStream_t>(stream)));
 }

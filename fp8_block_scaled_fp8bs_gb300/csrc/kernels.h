@@ -234,8 +234,8 @@ struct MoeArgs {
 };
 // Rows of the token side of the MMAs (the boxes of x8 and h8).
 int moe_token_rows(int64_t T);
-// w13 [E*2I, D], w2 [E*D, I]: boxes {128, 128}; x8 [T, D], h8 [active*T, I]: boxes
-// {128, moe_token_rows(T)}.
+// w13 [E*2I, D], w2 [E*D, I]: boxes {128, 128}; h8 [active*T, I]: boxes {128, moe_token_rows(T)}; x8
+// [T, D]: the same up to 16 rows, else single rows, which the up kernel gathers.
 struct MoeMaps {
     CUtensorMap w13, w2, x8, h8;
 };

@@ -5,10 +5,10 @@
 //   moe_down_kernel  y[t] = sum over active experts of weight[t, e] * W2 h, in binary32, bf16 once
 //
 // Bound by the weights' bytes: 3 D I per active expert, read once, while the tokens (64 at most) are few.
-// So 128 rows of weights take the MMA's M side and all T tokens its N side, for every active expert:
-// the products of tokens that did not choose the expert cost the tensor core what nothing else needs
-// (128 x MT x 128 per 16 KB of weights), and the activations need no gather. The partial of each K block
-// is scaled and added to binary32 registers by the promotion warps, as in gemm_swapab.cu.
+// So 128 rows of weights take the MMA's M side and the tokens its N side. The up kernel takes up to 16
+// tokens whole, of more it gathers those that chose the expert (TMA, four rows at a time); the down kernel takes
+// all. The partial of each K block is scaled and added to binary32 registers by the promotion warps, as in
+// gemm_swapab.cu.
 //
 // The choices meet the products in the factors: the up kernel writes zero codes and a zero factor for a
 // token that did not choose the expert, and otherwise the factor (block scale of h) * (weight of the
@@ -80,6 +80,22 @@ __device__ __forceinline__ MoeBars carve_bars(uint8_t* p, int stages) {
 
 constexpr int moe_bar_bytes(int stages) { return (2 * stages + 2 * MOE_NBUF + 1) * 8; }
 
+// Position of the i-th set bit (counting from 0); there are more than i.
+__device__ __forceinline__ int nth_bit(unsigned long long mask, int i) {
+    for (; i > 0; --i) mask &= mask - 1;
+    return __ffsll(mask) - 1;
+}
+
+// Rows r0 .. r3 of a map with boxes of one row, one after another at dst.
+__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t col,
+                                            int32_t r0, int32_t r1, int32_t r2, int32_t r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(col), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
+
 // Scales of the weights along a CTA's sequence of K blocks: lane l of a warp holds those of blocks
 // 32 c + l of chunk c, the next chunk's already on their way.
 template <typename Load>
@@ -132,8 +148,10 @@ struct MoeCfg {
     static constexpr int F_BYTES = MT * 4;                   // (down) factors of the tokens
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(MOE_NBUF * 2 * MT);
     // shared memory beside the stages
+    // More than 16 tokens: the up kernel gathers the rows of those that chose the expert.
+    static constexpr bool GATHER = MT > 16;
     static constexpr int up_fixed(int nkb) {
-        return 1024 + nkb * MT * 4 + 4 * MT * 4 + MT * BM * 4 + moe_bar_bytes(kMaxStages);
+        return 1024 + nkb * MT * 4 * (GATHER ? 2 : 1) + 5 * MT * 4 + MT * BM * 4 + moe_bar_bytes(kMaxStages);
     }
     static constexpr int down_fixed() { return 1024 + kMaxStages * F_BYTES + moe_bar_bytes(kMaxStages); }
     static int stages(int fixed) {
@@ -142,11 +160,21 @@ struct MoeCfg {
     }
 };
 
-// The MMAs of one weight tile of every stage: half 0 or 1.
-template <int MT>
-__device__ __forceinline__ void issue_half(int half, int total, int stages, const uint8_t* sW, const uint8_t* sX,
-                                           uint32_t tmem, const MoeBars& bar) {
-    constexpr uint32_t idesc = idesc_e4m3_f32(BM, MT);
+// After a wait that ran out: the copies of the last stages, so that none is still writing shared memory when the
+// CTA ends.
+__device__ __forceinline__ void drain_stages(const MoeBars& bar, int stages, int n) {
+    record_error(FP8BS_DEVERR_PRODUCER_WAIT);
+    for (int i = max(0, n - stages); i < n; ++i)
+        if (!mbar_wait(&bar.full[i % stages], (i / stages) & 1, kDrainLimitNs)) record_error(FP8BS_DEVERR_DRAIN_WAIT);
+}
+
+// The MMAs of one weight tile (half 0 or 1) of every stage; rows_of(m): rows of activations, a multiple of 16, of
+// the m-th run of `per` stages.
+template <int MT, typename Rows>
+__device__ __forceinline__ void issue_half(int half, int total, int per, int stages, const uint8_t* sW,
+                                           const uint8_t* sX, uint32_t tmem, const MoeBars& bar, Rows rows_of) {
+    uint32_t idesc = 0;
+    int left = 0, run = 0;
     const uint64_t w0 = smem_desc_k_sw128(smem_addr(sW) + half * A_TILE);
     const uint64_t x0 = smem_desc_k_sw128(smem_addr(sX));
     int st = 0;
@@ -158,6 +186,11 @@ __device__ __forceinline__ void issue_half(int half, int total, int stages, cons
             break;
         }
         tc_fence_after();
+        if (left == 0) {
+            idesc = idesc_e4m3_f32(BM, rows_of(run++));
+            left = per;
+        }
+        --left;
         const uint64_t w = w0 + static_cast<uint32_t>(st * (2 * A_TILE / 16));
         const uint64_t x = x0 + static_cast<uint32_t>(st * (MT * BK / 16));
         const uint32_t d = tmem + static_cast<uint32_t>((2 * buf + half) * MT);
@@ -201,6 +234,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const MoeArgs a, const float* xs, uint8_t* h8, float* hs, const int stages) {
     using Cfg = MoeCfg<MT>;
+    constexpr bool GATHER = Cfg::GATHER;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Routing rt;
     __shared__ uint32_t s_tmem;
@@ -209,8 +243,10 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     uint8_t* sW = smem;                                      // [stages][gate, up][128 x 128]
     uint8_t* sX = sW + stages * 2 * A_TILE;                  // [stages][MT x 128]
     float* sXs = reinterpret_cast<float*>(sX + stages * Cfg::X_TILE);   // [nkb][MT] scales of x
-    float* sMax = sXs + nkb * MT;                            // [4][MT]
-    float* sU = sMax + 4 * MT;                               // [MT][128] the up product, for the gate's warps
+    float* sGs = sXs + nkb * MT;                             // (GATHER) [nkb][MT] those of the item's rows
+    float* sMax = sGs + (GATHER ? nkb * MT : 0);             // [4][MT]
+    float* sScale = sMax + 4 * MT;                           // [MT]
+    float* sU = sScale + MT;                                 // [MT][128] products for the other half's warps
     const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sU + MT * BM), stages);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -247,36 +283,56 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     const int total = mine * nkb;
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_last();
-            const uint64_t stream = l2_policy_evict_first();
-            int n = 0;
-            bool ok = true;
-            for (int m = 0; ok && m < mine; ++m) {
-                const int item = blockIdx.x + m * gridDim.x;
-                const int act = item / iblocks;
-                const int row = rt.active[act] * 2 * a.I + (item - act * iblocks) * BM;
-                for (int kb = 0; kb < nkb; ++kb, ++n) {
-                    const int st = n % stages;
-                    if (!mbar_wait(&bar.empty[st], ((n / stages) & 1) ^ 1)) {
-                        record_error(FP8BS_DEVERR_PRODUCER_WAIT);
-                        ok = false;
-                        break;
+        // Lanes 0 and 1 bring the weight tiles, lane 2 the activations; GATHER: lane 2 + i rows 4i .. 4i + 3 of those
+        // that chose the expert (a row past them: any).
+        const uint64_t policy = lane < 2 ? l2_policy_evict_first() : l2_policy_evict_last();
+        int n = 0;
+        bool ok = true;
+        for (int m = 0; ok && m < mine; ++m) {
+            const int item = blockIdx.x + m * gridDim.x;
+            const int act = item / iblocks;
+            const int e = rt.active[act];
+            const int row = e * 2 * a.I + (item - act * iblocks) * BM + (lane == 1 ? a.I : 0);
+            int tok[4] = {0, 0, 0, 0};
+            int gathers = 0;
+            if constexpr (GATHER) {
+                unsigned long long mask = rt.mask[e];
+                gathers = (__popcll(mask) + 3) / 4;
+                if (lane >= 2 && lane < 2 + gathers) {
+                    for (int i = 0; i < 4 * (lane - 2); ++i) mask &= mask - 1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        tok[i] = mask ? __ffsll(mask) - 1 : tok[0];
+                        mask &= mask - 1;
                     }
-                    mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE);
-                    uint8_t* w = sW + st * 2 * A_TILE;
-                    tma_load_2d_hint(w, &tmW, &bar.full[st], kb * BK, row, stream);
-                    tma_load_2d_hint(w + A_TILE, &tmW, &bar.full[st], kb * BK, row + a.I, stream);
-                    tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmX, &bar.full[st], kb * BK, 0, keep);
                 }
             }
-            if (!ok)
-                for (int i = max(0, n - stages); i < n; ++i)
-                    if (!mbar_wait(&bar.full[i % stages], (i / stages) & 1, kDrainLimitNs))
-                        record_error(FP8BS_DEVERR_DRAIN_WAIT);
+            const uint32_t bytes = 2 * A_TILE + (GATHER ? gathers * 4 * BK : Cfg::X_TILE);
+            for (int kb = 0; kb < nkb; ++kb, ++n) {
+                const int st = n % stages;
+                if (!warp_wait(&bar.empty[st], ((n / stages) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
+                __syncwarp();
+                if (lane < 2)
+                    tma_load_2d_hint(sW + (2 * st + lane) * A_TILE, &tmW, &bar.full[st], kb * BK, row, policy);
+                else if (GATHER && lane < 2 + gathers)
+                    tma_gather4(sX + st * Cfg::X_TILE + (lane - 2) * 4 * BK, &tmX, &bar.full[st], kb * BK, tok[0],
+                                tok[1], tok[2], tok[3]);
+                else if (!GATHER && lane == 2)
+                    tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmX, &bar.full[st], kb * BK, 0, policy);
+            }
         }
+        if (!ok && lane == 0) drain_stages(bar, stages, n);
     } else if (warp == 1 || warp == MOE_ISSUER2) {
-        if (lane == 0) issue_half<MT>(warp == 1 ? 0 : 1, total, stages, sW, sX, tmem, bar);
+        if (lane == 0)
+            issue_half<MT>(warp == 1 ? 0 : 1, total, nkb, stages, sW, sX, tmem, bar, [&](int m) {
+                if (!GATHER) return MT;
+                const int act = (static_cast<int>(blockIdx.x) + m * static_cast<int>(gridDim.x)) / iblocks;
+                return (__popcll(rt.mask[rt.active[act]]) + 15) / 16 * 16;
+            });
     } else {
         const int half = (warp - MOE_PROMOTE_WARP0) >> 2;    // gate or up
         const int quarter = warp & 3;
@@ -298,6 +354,25 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             float g[MT];
 #pragma unroll
             for (int i = 0; i < MT; ++i) g[i] = 0.0f;
+            const int item = blockIdx.x + m * gridDim.x;
+            const int act = item / iblocks;
+            const int ib = item - act * iblocks;
+            const int e = rt.active[act];
+            const unsigned long long mask = rt.mask[e];
+            // the item's columns: its rows of x, or all tokens
+            const int cols = GATHER ? __popcll(mask) : a.T;
+            const float* scales = sXs;
+            if constexpr (GATHER) {
+                // the scales of the item's rows, side by side (barrier 1: no warp reads the last item's any more)
+                const int x = threadIdx.x - MOE_PROMOTE_WARP0 * 32;
+                const int i = x % MT;
+                if (i < cols) {
+                    const int t = nth_bit(mask, i);
+                    for (int kb = x / MT; kb < nkb; kb += 256 / MT) sGs[kb * MT + i] = sXs[kb * MT + t];
+                }
+                asm volatile("bar.sync 4, 256;" ::: "memory");
+                scales = sGs;
+            }
             for (int kb = 0; ok && kb < nkb; ++kb, ++n) {
                 const float s = ws.at(n, lane, scale_of);
                 const int buf = n % MOE_NBUF;
@@ -306,62 +381,89 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                promote_block<MT>(g, t0 + static_cast<uint32_t>(2 * buf * MT), sXs + kb * MT, s,
-                                  &bar.tempty[buf], lane);
+                const uint32_t at = t0 + static_cast<uint32_t>(2 * buf * MT);
+                if (GATHER && cols <= 16)
+                    promote_block<16>(g, at, scales + kb * MT, s, &bar.tempty[buf], lane);
+                else if (MT > 32 && cols <= 32)
+                    promote_block<32>(g, at, scales + kb * MT, s, &bar.tempty[buf], lane);
+                else
+                    promote_block<MT>(g, at, scales + kb * MT, s, &bar.tempty[buf], lane);
             }
-            const int item = blockIdx.x + m * gridDim.x;
-            const int act = item / iblocks;
-            const int ib = item - act * iblocks;
-            const int e = rt.active[act];
-            const unsigned long long mask = rt.mask[e];
-            // The up product goes to the gate's warps through shared memory (barrier 2: its place is free again).
-            if (half == 1) {
-                if (m > 0) asm volatile("bar.sync 2, 256;" ::: "memory");
+            // h = silu(gate) * up. The gate's warps take the first half of the columns, the up product's warps the
+            // others, four at a time (one after another, they are all latency: 41000 cycles for 16 tokens, half as
+            // much as the item's weights take); each side hands the other what it needs through shared memory.
+            const int tid = threadIdx.x - MOE_PROMOTE_WARP0 * 32;
+            const int mid = (cols + 7) / 8 * 4;
+            auto here = [&](int c) { return (4 * c < mid) == (half == 0); };
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    if ((mask >> t) & 1) sU[t * BM + r] = g[t];
-            }
+            for (int c = 0; c < MT / 4; ++c)
+                if (4 * c < cols && !here(c))
+#pragma unroll
+                    for (int i = 4 * c; i < 4 * c + 4; ++i) sU[i * BM + r] = g[i];
             if (promotion_any<256>(1, !ok)) {
                 ok = false;
                 break;
             }
-            if (half == 1) continue;
-            // h of this block of 128 channels: block maxima across the four warps, codes, factors
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                if ((mask >> t) & 1) {
-                    g[t] = g[t] / (1.0f + expf(-g[t])) * sU[t * BM + r];
-                    const float mag = fmaxf(fabsf(g[t]), 0.0f);          // (NaN counts as nothing)
-                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
-                    if (lane == 0) sMax[quarter * MT + t] = __uint_as_float(top);
-                }
-            if (m + 1 < mine) asm volatile("bar.arrive 2, 256;" ::: "memory");
-            asm volatile("bar.sync 3, 128;" ::: "memory");
-            uint8_t* out = h8 + static_cast<int64_t>(act) * a.T * a.I + ib * BK + r;
+            for (int c = 0; c < MT / 4; ++c)
+                if (4 * c < cols && here(c)) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-                if (t < a.T) {
-                    uint8_t code = 0;
-                    if ((mask >> t) & 1) {
-                        const float top = fmaxf(fmaxf(sMax[t], sMax[MT + t]),
-                                                fmaxf(sMax[2 * MT + t], sMax[3 * MT + t]));
-                        const float sc = block_scale(top, a.ue8m0);
-                        code = static_cast<uint8_t>(pack_e4m3x2(__fdiv_rn(g[t], sc), 0.0f));
+                    for (int i = 4 * c; i < 4 * c + 4; ++i) {
+                        const float other = sU[i * BM + r];
+                        const float gate = half == 0 ? g[i] : other;
+                        g[i] = __fdividef(gate, 1.0f + __expf(-gate)) * (half == 0 ? other : g[i]);
+                        const float mag = fmaxf(fabsf(g[i]), 0.0f);          // (NaN counts as nothing)
+                        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(mag));
+                        if (lane == 0) sMax[quarter * MT + i] = __uint_as_float(top);
                     }
-                    out[static_cast<int64_t>(t) * a.I] = code;
                 }
-            if (r < MT) {
-                float f = 0.0f;
-                if (r < a.T && ((mask >> r) & 1)) {
-                    float w = 0.0f;
-                    for (int j = 0; j < a.top_k; ++j)
-                        if (a.ids[r * a.top_k + j] == e) w += a.weights[r * a.top_k + j];
-                    f = w * block_scale(fmaxf(fmaxf(sMax[r], sMax[MT + r]),
-                                              fmaxf(sMax[2 * MT + r], sMax[3 * MT + r])), a.ue8m0);
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            // One thread per column: the block's scale, its reciprocal, and the factor of the down product. The
+            // factors of the tokens that did not choose the expert are zero, and their codes.
+            const int64_t out0 = static_cast<int64_t>(act) * a.T * a.I + ib * BK;
+            if (tid < MT) {
+                float* factor = hs + (static_cast<int64_t>(act) * iblocks + ib) * kMoeMaxTokens;
+                if (tid < cols) {
+                    const float sc = block_scale(fmaxf(fmaxf(sMax[tid], sMax[MT + tid]),
+                                                       fmaxf(sMax[2 * MT + tid], sMax[3 * MT + tid])), a.ue8m0);
+                    sScale[tid] = sc;
+                    const int t = GATHER ? nth_bit(mask, tid) : tid;
+                    if ((mask >> t) & 1) {
+                        float w = 0.0f;
+                        for (int j = 0; j < a.top_k; ++j)
+                            if (a.ids[t * a.top_k + j] == e) w += a.weights[t * a.top_k + j];
+                        factor[t] = w * sc;
+                    }
                 }
-                hs[(static_cast<int64_t>(act) * iblocks + ib) * kMoeMaxTokens + r] = f;
+                if (tid >= a.T || !((mask >> tid) & 1)) factor[tid] = 0.0f;
+            } else {
+                for (int i = tid - MT; i < a.T * (BK / 16); i += 256 - MT) {
+                    const int t = i / (BK / 16);
+                    if (!((mask >> t) & 1))
+                        *reinterpret_cast<uint4*>(h8 + out0 + static_cast<int64_t>(t) * a.I + i % (BK / 16) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                }
             }
-            asm volatile("bar.sync 3, 128;" ::: "memory");       // sMax is free again
+            asm volatile("bar.sync 3, 256;" ::: "memory");
+            unsigned long long rest = mask;
+#pragma unroll
+            for (int c = 0; c < MT / 4; ++c)
+                if (4 * c < cols) {
+#pragma unroll
+                    for (int i = 4 * c; i < 4 * c + 4; ++i) {
+                        int t = i;
+                        if constexpr (GATHER) {
+                            t = rest ? __ffsll(rest) - 1 : 0;
+                            rest &= rest - 1;
+                        }
+                        if (here(c) && i < cols && ((mask >> t) & 1)) {
+                            const float sc = sScale[i];
+                            const float q = div_by_scale(g[i], sc, __frcp_rn(sc));
+                            h8[out0 + static_cast<int64_t>(t) * a.I + r] =
+                                static_cast<uint8_t>(pack_e4m3x2(q, 0.0f));
+                        }
+                    }
+                }
         }
         if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
     }
@@ -418,50 +520,43 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     const int total = static_cast<int>(static_cast<int64_t>(rank + 1) * units / C) - u0;
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_last();
-            const uint64_t stream = l2_policy_evict_first();
-            // (the second tile of the last pair may lie past D: it reads the next expert's rows, or zeros past
-            // the last one's, and is not stored)
-            auto load_w = [&](int n) {
-                const int st = n % stages;
-                const int act = (u0 + n) / nkb;
-                const int kb = u0 + n - act * nkb;
-                const int row = rt.active[act] * a.D + pair * 2 * BM;
-                uint8_t* w = sW + st * 2 * A_TILE;
-                mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE + Cfg::F_BYTES);
-                tma_load_2d_hint(w, &tmW, &bar.full[st], kb * BK, row, stream);
-                tma_load_2d_hint(w + A_TILE, &tmW, &bar.full[st], kb * BK, row + BM, stream);
-            };
-            auto load_h = [&](int n) {
-                const int st = n % stages;
-                const int act = (u0 + n) / nkb;
-                const int kb = u0 + n - act * nkb;
-                tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmH, &bar.full[st], kb * BK, act * a.T, keep);
+        // One lane for each of a stage's four copies (see the up kernel): the two weight tiles, h, the factors. (The
+        // second tile of the last pair may lie past D: it reads the next expert's rows, or zeros past the last
+        // one's, and is not stored.)
+        const uint64_t policy = lane < 2 ? l2_policy_evict_first() : l2_policy_evict_last();
+        auto load = [&](int n, bool weights, bool h) {
+            const int st = n % stages;
+            const int act = (u0 + n) / nkb;
+            const int kb = u0 + n - act * nkb;
+            if (weights) {
+                if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE + Cfg::F_BYTES);
+                __syncwarp();
+            }
+            const bool w = lane < 2;
+            if ((w && weights) || (lane == 2 && h))
+                tma_load_2d_hint(w ? sW + (2 * st + lane) * A_TILE : sX + st * Cfg::X_TILE, w ? &tmW : &tmH,
+                                 &bar.full[st], kb * BK,
+                                 w ? rt.active[act] * a.D + (2 * pair + lane) * BM : act * a.T, policy);
+            if (lane == 3 && h)
                 bulk_load(sF + st * MT, hs + (static_cast<int64_t>(act) * nkb + kb) * kMoeMaxTokens,
                           Cfg::F_BYTES, &bar.full[st]);
-            };
-            const int ahead = min(stages, total);
-            for (int n = 0; n < ahead; ++n) load_w(n);
-            grid_dependency_wait();
-            grid_launch_dependents();
-            for (int n = 0; n < ahead; ++n) load_h(n);
-            int n = ahead;
-            for (; n < total; ++n) {
-                if (!mbar_wait(&bar.empty[n % stages], ((n / stages) & 1) ^ 1)) {
-                    record_error(FP8BS_DEVERR_PRODUCER_WAIT);
-                    for (int i = max(0, n - stages); i < n; ++i)
-                        if (!mbar_wait(&bar.full[i % stages], (i / stages) & 1, kDrainLimitNs))
-                            record_error(FP8BS_DEVERR_DRAIN_WAIT);
-                    break;
-                }
-                load_w(n);
-                load_h(n);
+        };
+        const int ahead = min(stages, total);
+        for (int n = 0; n < ahead; ++n) load(n, true, false);
+        grid_dependency_wait();
+        grid_launch_dependents();
+        for (int n = 0; n < ahead; ++n) load(n, false, true);
+        int n = ahead;
+        for (; n < total; ++n) {
+            if (!warp_wait(&bar.empty[n % stages], ((n / stages) & 1) ^ 1)) {
+                if (lane == 0) drain_stages(bar, stages, n);
+                break;
             }
+            load(n, true, true);
         }
     } else if (warp == 1 || warp == MOE_ISSUER2) {
         grid_dependency_wait();
-        if (lane == 0) issue_half<MT>(warp == 1 ? 0 : 1, total, stages, sW, sX, tmem, bar);
+        if (lane == 0) issue_half<MT>(warp == 1 ? 0 : 1, total, total, stages, sW, sX, tmem, bar, [](int) { return MT; });
     } else {
         grid_dependency_wait();
         const int half = (warp - MOE_PROMOTE_WARP0) >> 2;
@@ -566,11 +661,12 @@ cudaError_t launch_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspac
     if (e != cudaSuccess) return e;
     // The most CTAs per pair of slabs that leave every cluster of the grid its own SMs and each CTA work.
     const int pairs = (a.D / BM + 1) / 2;
+    // (Powers of two: five CTAs instead of four for 28 pairs took 324 instead of 303 us at 64 tokens.)
     int C = kMaxSplit;
     while (C > 1 && (static_cast<int64_t>(pairs) * C > num_sms || items < 2 * C ||
                      max_active_clusters(reinterpret_cast<const void*>(moe_down_kernel<MT>), MOE_THREADS,
                                          down_smem, C) < pairs))
-        --C;
+        C /= 2;
     return launch_pdl_cluster(moe_down_kernel<MT>, dim3(pairs * C), MOE_THREADS, down_smem, stream, C, false,
                               m.w2, m.h8, a, hs, C, down_stages);
 }
