@@ -151,7 +151,7 @@ struct MoeCfg {
     // More than 16 tokens: the up kernel gathers the rows of those that chose the expert.
     static constexpr bool GATHER = MT > 16;
     static constexpr int up_fixed(int nkb) {
-        return 1024 + nkb * MT * 4 * (GATHER ? 2 : 1) + 5 * MT * 4 + MT * BM * 4 + moe_bar_bytes(kMaxStages);
+        return 1024 + nkb * MT * 4 * (GATHER ? 2 : 1) + 7 * MT * 4 + MT * BM * 4 + moe_bar_bytes(kMaxStages);
     }
     static constexpr int down_fixed() { return 1024 + kMaxStages * F_BYTES + moe_bar_bytes(kMaxStages); }
     static int stages(int fixed) {
@@ -245,8 +245,9 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     float* sXs = reinterpret_cast<float*>(sX + stages * Cfg::X_TILE);   // [nkb][MT] scales of x
     float* sGs = sXs + nkb * MT;                             // (GATHER) [nkb][MT] those of the item's rows
     float* sMax = sGs + (GATHER ? nkb * MT : 0);             // [4][MT]
-    float* sScale = sMax + 4 * MT;                           // [MT]
-    float* sU = sScale + MT;                                 // [MT][128] products for the other half's warps
+    float2* sScale = reinterpret_cast<float2*>(sMax + 4 * MT);   // [MT] scale of a column's block, its reciprocal
+    int* sTok = reinterpret_cast<int*>(sScale + MT);         // [MT] its token, or -1
+    float* sU = reinterpret_cast<float*>(sTok + MT);                                 // [MT][128] products for the other half's warps
     const MoeBars bar = carve_bars(reinterpret_cast<uint8_t*>(sU + MT * BM), stages);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -393,6 +394,16 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             // others, four at a time (one after another, they are all latency: 41000 cycles for 16 tokens, half as
             // much as the item's weights take); each side hands the other what it needs through shared memory.
             const int tid = threadIdx.x - MOE_PROMOTE_WARP0 * 32;
+            float route_w = 0.0f;              // thread tid: the expert's weight for column tid's token
+            if (tid < cols) {
+                const int t = GATHER ? nth_bit(mask, tid) : tid;
+#pragma unroll 8
+                for (int j = 0; j < a.top_k; ++j) {
+                    const int id = a.ids[t * a.top_k + j];
+                    const float w = a.weights[t * a.top_k + j];
+                    route_w += id == e ? w : 0.0f;
+                }
+            }
             const int mid = (cols + 7) / 8 * 4;
             auto here = [&](int c) { return (4 * c < mid) == (half == 0); };
 #pragma unroll
@@ -426,14 +437,10 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                 if (tid < cols) {
                     const float sc = block_scale(fmaxf(fmaxf(sMax[tid], sMax[MT + tid]),
                                                        fmaxf(sMax[2 * MT + tid], sMax[3 * MT + tid])), a.ue8m0);
-                    sScale[tid] = sc;
                     const int t = GATHER ? nth_bit(mask, tid) : tid;
-                    if ((mask >> t) & 1) {
-                        float w = 0.0f;
-                        for (int j = 0; j < a.top_k; ++j)
-                            if (a.ids[t * a.top_k + j] == e) w += a.weights[t * a.top_k + j];
-                        factor[t] = w * sc;
-                    }
+                    sScale[tid] = make_float2(sc, __frcp_rn(sc));
+                    sTok[tid] = (mask >> t) & 1 ? t : -1;
+                    if ((mask >> t) & 1) factor[t] = route_w * sc;
                 }
                 if (tid >= a.T || !((mask >> tid) & 1)) factor[tid] = 0.0f;
             } else {
@@ -445,23 +452,18 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                 }
             }
             asm volatile("bar.sync 3, 256;" ::: "memory");
-            unsigned long long rest = mask;
 #pragma unroll
             for (int c = 0; c < MT / 4; ++c)
-                if (4 * c < cols) {
+                if (4 * c < cols && here(c)) {
+                    const int4 t4 = *reinterpret_cast<const int4*>(sTok + 4 * c);
+                    const int tok[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-                    for (int i = 4 * c; i < 4 * c + 4; ++i) {
-                        int t = i;
-                        if constexpr (GATHER) {
-                            t = rest ? __ffsll(rest) - 1 : 0;
-                            rest &= rest - 1;
-                        }
-                        if (here(c) && i < cols && ((mask >> t) & 1)) {
-                            const float sc = sScale[i];
-                            const float q = div_by_scale(g[i], sc, __frcp_rn(sc));
-                            h8[out0 + static_cast<int64_t>(t) * a.I + r] =
-                                static_cast<uint8_t>(pack_e4m3x2(q, 0.0f));
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 sc = sScale[4 * c + i];
+                        const uint8_t code = static_cast<uint8_t>(
+                            pack_e4m3x2(div_by_scale(g[4 * c + i], sc.x, sc.y), 0.0f));
+                        if (4 * c + i < cols && tok[i] >= 0)
+                            h8[out0 + static_cast<int64_t>(tok[i]) * a.I + r] = code;
                     }
                 }
         }

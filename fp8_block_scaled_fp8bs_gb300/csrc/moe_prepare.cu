@@ -19,6 +19,7 @@ constexpr int PREP_CLUSTER = 8;
 constexpr int PREP_TOKENS = 4;
 constexpr int PREP_THREADS = 256;
 constexpr int PREP_EXPERTS = 4;     // experts a warp computes at once
+constexpr int PREP_AHEAD = 4;       // 16-byte pieces of each of their rows a lane has in flight
 constexpr int kMaxExperts = 512;
 
 struct PrepArgs {
@@ -34,11 +35,15 @@ struct PrepArgs {
     float route_scale;
 };
 
-// Larger key = better choice: the value's order, then the lower index. Never 0.
-__device__ __forceinline__ uint64_t choice_key(float v, int e) {
+// Unsigned integers in the order of the floats.
+__device__ __forceinline__ uint32_t order_of(float v) {
     const uint32_t b = __float_as_uint(v);
-    const uint32_t ord = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return (static_cast<uint64_t>(ord) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e));
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// Larger key = better choice: the value's order, then the lower index.
+__device__ __forceinline__ uint64_t choice_key(float v, int e) {
+    return (static_cast<uint64_t>(order_of(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e));
 }
 
 // The choice for one token by one warp: logits in sc[0..E) (shared memory), replaced by scores.
@@ -93,18 +98,19 @@ __device__ __forceinline__ void choose(const PrepArgs& a, float* sc, float* ch, 
     float total = 0.0f;
     int mine = 0;               // lane j keeps the j-th choice
     for (int j = 0; j < a.top_k; ++j) {
-        uint64_t best = 0;
-        for (int i = 0, e = lane; e < E; ++i, e += 32)
-            if (!((taken >> i) & 1u)) {
-                const uint64_t key = choice_key(ch[e], e);
-                best = key > best ? key : best;
+        uint32_t best = 0;
+        int at = 0x7FFFFFFF;
+        for (int i = 0, e = lane; e < E; ++i, e += 32) {
+            const uint32_t key = order_of(ch[e]);
+            if (!((taken >> i) & 1u) && (at == 0x7FFFFFFF || key > best)) {
+                best = key;
+                at = e;
             }
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) {
-            const uint64_t o = __shfl_xor_sync(0xffffffffu, best, i);
-            best = o > best ? o : best;
         }
-        const int e = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+        // (a lane without experts left holds the lowest key and no index)
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = static_cast<int>(
+            __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(at) : 0x7FFFFFFFu));
         if ((e & 31) == lane) taken |= 1u << (e >> 5);
         total += sc[e];
         if (lane == j) mine = e;
@@ -135,6 +141,21 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
 
     grid_dependency_wait();
     grid_launch_dependents();
+    // The router's weights of the warp's first experts are on their way before x.
+    const int pieces = nbr * (BK / 8);               // 16-byte pieces of this CTA's channels
+    uint4 wv[PREP_EXPERTS][PREP_AHEAD];
+    auto load_weights = [&](int e0, int c0) {
+#pragma unroll
+        for (int i = 0; i < PREP_EXPERTS; ++i) {
+            const uint4* row = a.router_w + (static_cast<int64_t>(min(e0 + i, a.E - 1)) * a.D + b0 * BK) / 8;
+#pragma unroll
+            for (int k = 0; k < PREP_AHEAD; ++k) {
+                const int c = c0 + 32 * k + lane;
+                wv[i][k] = c < pieces ? __ldg(row + c) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+    if (a.router_w && warp * PREP_EXPERTS < a.E) load_weights(warp * PREP_EXPERTS, 0);
     // x into shared memory and its codes and scales out: 8 lanes per block of 128.
     const int tasks = PREP_TOKENS * nbr;
     for (int base = warp * 4; base < tasks; base += PREP_THREADS / 8) {
@@ -168,46 +189,51 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
     cluster_sync();                // x staged; every CTA of the cluster is running
     // Partial logits: a warp takes PREP_EXPERTS experts at a time, its lanes the channels.
     const uint32_t part0 = mapa_shared(smem_addr(part), 0);
-    const int pieces = nbr * (BK / 8);
+    constexpr int VALUES = PREP_EXPERTS * PREP_TOKENS;
+    static_assert(VALUES == 16, "the reduction below hands each pair of lanes one value");
     for (int e0 = warp * PREP_EXPERTS; e0 < a.E; e0 += PREP_THREADS / 32 * PREP_EXPERTS) {
-        float acc[PREP_EXPERTS][PREP_TOKENS] = {};
-        const uint4* wrow[PREP_EXPERTS];
+        float acc[VALUES] = {};                      // [expert][token]
+        for (int c0 = 0; c0 < pieces; c0 += 32 * PREP_AHEAD) {
+            if (c0 > 0 || e0 > warp * PREP_EXPERTS) load_weights(e0, c0);
 #pragma unroll
-        for (int i = 0; i < PREP_EXPERTS; ++i)
-            wrow[i] = a.router_w +
-                      (static_cast<int64_t>(min(e0 + i, a.E - 1)) * a.D + b0 * BK) / 8;
-#pragma unroll 2
-        for (int c = lane; c < pieces; c += 32) {
-            uint4 wv[PREP_EXPERTS];
+            for (int h = 0; h < PREP_AHEAD; ++h) {
+                const int c = min(c0 + 32 * h + lane, pieces - 1);       // (past the end the weights are zero)
+                if (c0 + 32 * h >= pieces) break;
 #pragma unroll
-            for (int i = 0; i < PREP_EXPERTS; ++i) wv[i] = __ldg(wrow[i] + c);
+                for (int k = 0; k < PREP_TOKENS; ++k) {
+                    const uint4 xv = sx[k * pitch + c];
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-            for (int k = 0; k < PREP_TOKENS; ++k) {
-                const uint4 xv = sx[k * pitch + c];
-                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    for (int i = 0; i < PREP_EXPERTS; ++i) {
+                        const uint32_t ww[4] = {wv[i][h].x, wv[i][h].y, wv[i][h].z, wv[i][h].w};
+                        float& t = acc[i * PREP_TOKENS + k];
 #pragma unroll
-                for (int i = 0; i < PREP_EXPERTS; ++i) {
-                    const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[i][k] = fmaf(bf16_lo(xw[j]), bf16_lo(ww[j]), acc[i][k]);
-                        acc[i][k] = fmaf(bf16_hi(xw[j]), bf16_hi(ww[j]), acc[i][k]);
+                        for (int j = 0; j < 4; ++j) {
+                            t = fmaf(bf16_lo(xw[j]), bf16_lo(ww[j]), t);
+                            t = fmaf(bf16_hi(xw[j]), bf16_hi(ww[j]), t);
+                        }
                     }
                 }
             }
         }
+        // 16 values over 32 lanes: in each step a lane keeps one half of them and hands its partner the other, so
+        // that lanes 2v and 2v + 1 end with value v.
 #pragma unroll
-        for (int i = 0; i < PREP_EXPERTS; ++i)
+        for (int half = 8; half > 0; half >>= 1) {
+            const bool upper = lane & (2 * half);
 #pragma unroll
-            for (int k = 0; k < PREP_TOKENS; ++k) {
-                float v = acc[i][k];
-#pragma unroll
-                for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-                if (lane == 0 && e0 + i < a.E)
-                    st_shared_cluster_f32(
-                        part0 + static_cast<uint32_t>(((rank * PREP_TOKENS + k) * a.E + e0 + i) * 4),
-                        v);
+            for (int i = 0; i < half; ++i) {
+                const float send = upper ? acc[i] : acc[i + half];
+                const float keep = upper ? acc[i + half] : acc[i];
+                acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
             }
+        }
+        const float v = acc[0] + __shfl_xor_sync(0xffffffffu, acc[0], 1);
+        const int value = lane >> 1;
+        const int e = e0 + value / PREP_TOKENS;
+        if ((lane & 1) == 0 && e < a.E)
+            st_shared_cluster_f32(
+                part0 + static_cast<uint32_t>(((rank * PREP_TOKENS + value % PREP_TOKENS) * a.E + e) * 4), v);
     }
     cluster_sync();
     if (rank != 0) return;
