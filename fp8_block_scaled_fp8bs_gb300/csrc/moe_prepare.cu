@@ -46,79 +46,101 @@ __device__ __forceinline__ uint64_t choice_key(float v, int e) {
     return (static_cast<uint64_t>(order_of(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(e));
 }
 
-// The choice for one token by one warp: logits in sc[0..E) (shared memory), replaced by scores.
-__device__ __forceinline__ void choose(const PrepArgs& a, float* sc, float* ch, int64_t t, int lane) {
+// The choice for one token by one warp: logits in sc[0..E), biases in ch[0..E) (shared memory). Lane l holds the
+// scores of experts l, l + 32, ...: J of them at most.
+template <int J>
+__device__ __forceinline__ void choose(const PrepArgs& a, const float* sc, float* ch, int64_t t, int lane) {
     const int E = a.E;
-    if (a.score == FP8BS_SCORE_SIGMOID) {
-        for (int e = lane; e < E; e += 32) sc[e] = 1.0f / (1.0f + expf(-sc[e]));
-    } else {
-        float m = -INFINITY;
-        for (int e = lane; e < E; e += 32) m = fmaxf(m, sc[e]);
+    float score[J];
 #pragma unroll
-        for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+    for (int i = 0; i < J; ++i) score[i] = lane + 32 * i < E ? sc[lane + 32 * i] : -INFINITY;
+    if (a.score == FP8BS_SCORE_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < J; ++i) score[i] = 1.0f / (1.0f + expf(-score[i]));
+    } else {
+        float m = score[0];
+#pragma unroll
+        for (int i = 1; i < J; ++i) m = fmaxf(m, score[i]);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         float sum = 0.0f;
-        for (int e = lane; e < E; e += 32) {
-            sc[e] = expf(sc[e] - m);
-            sum += sc[e];
+#pragma unroll
+        for (int i = 0; i < J; ++i) {
+            score[i] = expf(score[i] - m);
+            sum += score[i];
         }
 #pragma unroll
-        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-        for (int e = lane; e < E; e += 32) sc[e] /= sum;
+        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+#pragma unroll
+        for (int i = 0; i < J; ++i) score[i] /= sum;
     }
-    for (int e = lane; e < E; e += 32) ch[e] = a.bias ? sc[e] + a.bias[e] : sc[e];
-    __syncwarp();
+    float choice[J];
+#pragma unroll
+    for (int i = 0; i < J; ++i) choice[i] = a.bias && lane + 32 * i < E ? score[i] + ch[lane + 32 * i] : score[i];
+    unsigned keep = 0xFFFFFFFFu;       // bit g: group g stays
+    const int per = E / a.groups;
     if (a.groups > 1) {
-        const int per = E / a.groups;
-        float rank = -INFINITY;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+            if (lane + 32 * i < E) ch[lane + 32 * i] = choice[i];
+        __syncwarp();
+        float m1 = -INFINITY, m2 = -INFINITY;      // lane g: the two highest of group g
         if (lane < a.groups) {
-            float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 4
             for (int i = 0; i < per; ++i) {
                 const float v = ch[lane * per + i];
-                if (v > m1) {
-                    m2 = m1;
-                    m1 = v;
-                } else if (v > m2) {
-                    m2 = v;
-                }
+                m2 = fmaxf(m2, fminf(m1, v));
+                m1 = fmaxf(m1, v);
             }
-            rank = a.bias && per > 1 ? m1 + m2 : m1;
         }
-        const uint64_t key = choice_key(rank, lane);
+        const uint64_t key = choice_key(a.bias && per > 1 ? m1 + m2 : m1, lane);
         int better = 0;
-        for (int g = 0; g < a.groups; ++g)
-            better += __shfl_sync(0xffffffffu, key, g) > key ? 1 : 0;
-        const unsigned keep = __ballot_sync(0xffffffffu, lane < a.groups && better < a.topk_groups);
-        __syncwarp();
-        for (int e = lane; e < E; e += 32)
-            if (!((keep >> (e / per)) & 1u)) ch[e] = -INFINITY;
-        __syncwarp();
+#pragma unroll 4
+        for (int g = 0; g < a.groups; ++g) better += __shfl_sync(0xffffffffu, key, g) > key ? 1 : 0;
+        keep = __ballot_sync(0xffffffffu, lane < a.groups && better < a.topk_groups);
     }
-    // top_k rounds of a warp-wide maximum; lane l holds experts l, l + 32, ...
-    unsigned taken = 0;
-    float total = 0.0f;
-    int mine = 0;               // lane j keeps the j-th choice
+    // Keys in the order of the choices; 0: not to be had (no expert, a group that is out, taken).
+    uint32_t key[J];
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = e < E && (a.groups == 1 || (keep >> (e / per)) & 1u) ? max(order_of(choice[i]), 1u) : 0u;
+    }
+    // top_k rounds of the highest key, of equal ones the lowest index
+    float mine_score = 0.0f;           // lane j keeps the j-th choice
+    int mine = 0;
     for (int j = 0; j < a.top_k; ++j) {
-        uint32_t best = 0;
-        int at = 0x7FFFFFFF;
-        for (int i = 0, e = lane; e < E; ++i, e += 32) {
-            const uint32_t key = order_of(ch[e]);
-            if (!((taken >> i) & 1u) && (at == 0x7FFFFFFF || key > best)) {
-                best = key;
-                at = e;
+        uint32_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < J; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
             }
-        }
-        // (a lane without experts left holds the lowest key and no index)
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         const int e = static_cast<int>(
-            __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(at) : 0x7FFFFFFFu));
-        if ((e & 31) == lane) taken |= 1u << (e >> 5);
-        total += sc[e];
-        if (lane == j) mine = e;
+            __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(lane + 32 * at) : 0xFFFFFFFFu));
+        float s = score[0];
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+            if (e == lane + 32 * i) {
+                key[i] = 0;
+                s = score[i];
+            }
+        s = __shfl_sync(0xffffffffu, s, e & 31);
+        if (lane == j) {
+            mine = e;
+            mine_score = s;
+        }
     }
+    float total = mine_score;          // (lanes past top_k hold 0)
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
     if (lane < a.top_k) {
         a.ids[t * a.top_k + lane] = mine;
-        const float w = a.normalise ? sc[mine] / total : sc[mine];
-        a.weights[t * a.top_k + lane] = w * a.route_scale;
+        a.weights[t * a.top_k + lane] = (a.normalise ? mine_score / total : mine_score) * a.route_scale;
     }
 }
 
@@ -139,6 +161,7 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
     float* part = reinterpret_cast<float*>(sx + PREP_TOKENS * pitch);  // CTA 0: [rank][tokens][E]
     float* choice = part + PREP_CLUSTER * PREP_TOKENS * a.E;             // CTA 0: [tokens][E]
 
+    if (a.router_w) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     grid_dependency_wait();
     grid_launch_dependents();
     // The router's weights of the warp's first experts are on their way before x.
@@ -186,7 +209,10 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
         }
     }
     if (!a.router_w) return;       // uniform over the grid
-    cluster_sync();                // x staged; every CTA of the cluster is running
+    __syncthreads();               // x staged
+    // CTA 0 gets the biases where the choice will look for them.
+    if (rank == 0 && a.bias && warp < nt)
+        for (int e = lane; e < a.E; e += 32) choice[warp * a.E + e] = __ldg(a.bias + e);
     // Partial logits: a warp takes PREP_EXPERTS experts at a time, its lanes the channels.
     const uint32_t part0 = mapa_shared(smem_addr(part), 0);
     constexpr int VALUES = PREP_EXPERTS * PREP_TOKENS;
@@ -228,6 +254,8 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
                 acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
             }
         }
+        // (every CTA of the cluster has to be running before the first store into another's memory)
+        if (e0 == warp * PREP_EXPERTS) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         const float v = acc[0] + __shfl_xor_sync(0xffffffffu, acc[0], 1);
         const int value = lane >> 1;
         const int e = e0 + value / PREP_TOKENS;
@@ -235,6 +263,7 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
             st_shared_cluster_f32(
                 part0 + static_cast<uint32_t>(((rank * PREP_TOKENS + value % PREP_TOKENS) * a.E + e) * 4), v);
     }
+    if (warp * PREP_EXPERTS >= a.E) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     cluster_sync();
     if (rank != 0) return;
     for (int i = threadIdx.x; i < PREP_TOKENS * a.E; i += PREP_THREADS) {
@@ -243,7 +272,17 @@ __global__ void __launch_bounds__(PREP_THREADS) moe_prepare_kernel(const PrepArg
         part[i] = v;               // slot of rank 0: logits [tokens][E]
     }
     __syncthreads();
-    if (warp < nt) choose(a, part + warp * a.E, choice + warp * a.E, t0 + warp, lane);
+    if (warp >= nt) return;
+    const float* logits = part + warp * a.E;
+    float* mine = choice + warp * a.E;
+    if (a.E <= 32)
+        choose<1>(a, logits, mine, t0 + warp, lane);
+    else if (a.E <= 64)
+        choose<2>(a, logits, mine, t0 + warp, lane);
+    else if (a.E <= 256)
+        choose<8>(a, logits, mine, t0 + warp, lane);
+    else
+        choose<16>(a, logits, mine, t0 + warp, lane);
 }
 
 }  // namespace
