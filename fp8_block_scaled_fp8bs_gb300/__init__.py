@@ -477,8 +477,8 @@ def fp8_gemm_grouped(a, a_s, b, b_s, row_offsets, scale_fmt="fp32", out=None):
 # ------------------------------------------------------------- around the products of a decoder layer
 #
 # These calls take microseconds on the GPU, so their host side is kept short: one pass over the tensors'
-# attributes decides whether everything is as it should be (_fine), and only if it is not do the checks that
-# say what is wrong run; the C structures are packed in one go (the ctypes structures above, field by field,
+# attributes decides whether everything is as it should be, and only if it is not do the checks that say what
+# is wrong run (_explain); the C structures are packed in one go (the ctypes structures above, field by field,
 # cost several microseconds a call).
 
 class PagedCache(NamedTuple):
@@ -499,29 +499,25 @@ assert (_KV_SIZE, _NORM_ROPE_SIZE, _ATTENTION_SIZE, _ROUTING_SIZE) == tuple(
     ctypes.sizeof(c) for c in (KvCache, QkNormRopeArgs, PagedAttentionArgs, MoeRouting))
 
 
-def _fine(dev, rows, dense):
-    """Whether every (tensor, ndim) of rows is bf16 with contiguous rows, and every (tensor, dtype, ndim) of
-    dense contiguous (None: absent), all on the CUDA device `dev`."""
-    import torch
-    bf16 = torch.bfloat16
-    try:
-        for t, ndim in rows:
-            if t.dtype is not bf16 or t.get_device() != dev or t.dim() != ndim or t.stride(-1) != 1:
-                return False
-        for t, dtype, ndim in dense:
-            if t is not None and (t.dtype is not dtype or t.get_device() != dev or t.dim() != ndim or
-                                  not t.is_contiguous()):
-                return False
-    except (AttributeError, IndexError):
-        return False
-    return dev >= 0
+class _Types:
+    """torch's types, looked up once (the package itself does not import torch)."""
+    ready = False
+
+    def load(self):
+        import torch
+        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.i64, self.e4m3 = torch.int64, torch.float8_e4m3fn
+        self.empty = torch.empty
+        self.ready = True
+        return self
 
 
-def _device_index(t):
-    try:
-        return t.get_device()
-    except AttributeError:
-        return -1
+_types = _Types()
+
+
+def _dense(t, dtype, dev, shape):
+    """Whether t is a contiguous tensor of this type and shape on CUDA device `dev`."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
 def _rows(t, ndim, name):
@@ -537,7 +533,7 @@ def _rows(t, ndim, name):
 
 
 def _explain(device, rows, dense):
-    """The checks of _fine, one by one, with what is wrong. rows: {name: (tensor, ndim)}, dense: {name:
+    """The checks of types, devices and layouts, one by one, with what is wrong. rows: {name: (tensor, ndim)}, dense: {name:
     (tensor, dtype, ndim)}."""
     for name, (t, ndim) in rows.items():
         _rows(t, ndim, name)
@@ -563,25 +559,10 @@ def _raw_stream(dev):
     return _stream_of(dev)
 
 
-def _cache_fields(cache):
-    """The fields of a fp8bs_kv_cache, and (pages, page size, heads, dk, dv)."""
-    k, v = cache
-    shape, vshape = k.shape, v.shape
-    if shape[:3] != vshape[:3]:
-        raise ValueError("cache.k and cache.v must have the same pages, page size and heads")
-    sizes = (shape[0], shape[1], shape[2], shape[3], vshape[3])
-    return (k.data_ptr(), v.data_ptr(), *sizes, *k.stride()[:3], *v.stride()[:3]), sizes
-
-
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
 def _new_output(out, shape, like):
-    """The bf16 output of `shape`: new on the device of `like`, or the caller's `out`, checked."""
+    """The bf16 output of `shape`: new on the device of `like` (bf16), or the caller's `out`, checked."""
     if out is None:
-        import torch
-        return like.new_empty(shape, dtype=torch.bfloat16)
+        return _types.empty(shape, dtype=_types.bf16, device=like.device)
     return _output(out, shape, like.device)
 
 
@@ -591,53 +572,63 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     [T, Hk, D] by positions int32 [T]; cos, sin fp32 [max_positions, R/2] rotate the channels
     rot_start .. rot_start+R-1. With a PagedCache, the keys and v bf16 [T, Hk, Dv] go to its slots
     int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k)."""
-    import torch
-    rows = [(q, 3), (k, 3)]
-    if cache is not None:
-        rows += [(v, 3), (cache[0], 4), (cache[1], 4)]
-    elif v is not None or slots is not None:
-        raise ValueError("v and slots need a cache")
-    dev = _device_index(q)
-    if not _fine(dev, rows, ((cos, torch.float32, 2), (sin, torch.float32, 2),
-                             (positions, torch.int32, 1), (q_weight, torch.bfloat16, 1),
-                             (k_weight, torch.bfloat16, 1), (slots, torch.int64, 1))):
+    ty = _types if _types.ready else _types.load()
+    bf16 = ty.bf16
+    if cache is None:
+        if v is not None or slots is not None:
+            raise ValueError("v and slots need a cache")
+    elif v is None or slots is None:
+        raise ValueError("a cache needs v and slots")
+    try:
+        T, hq, d = q.shape
+        hk = k.shape[1]
+        max_pos, half = table = cos.shape
+        dev = q.get_device()
+        q0, q1, q2 = q.stride()
+        k0, k1, k2 = k.stride()
+        fine = (dev >= 0 and q.dtype is bf16 and q2 == 1 and k.dtype is bf16 and k2 == 1 and
+                k.shape == (T, hk, d) and k.get_device() == dev and _dense(cos, ty.f32, dev, table) and
+                _dense(sin, ty.f32, dev, table) and _dense(positions, ty.i32, dev, (T,)) and
+                (q_weight is None or _dense(q_weight, bf16, dev, (d,))) and
+                (k_weight is None or _dense(k_weight, bf16, dev, (d,))))
+        if cache is not None:
+            ck, cv = cache
+            pages, page_size, heads, cd = ck.shape
+            dv = cv.shape[3]
+            v0, v1, v2 = v.stride()
+            ck_strides, cv_strides = ck.stride(), cv.stride()
+            fine = (fine and v.dtype is bf16 and v2 == 1 and v.shape == (T, hk, dv) and
+                    v.get_device() == dev and ck.dtype is bf16 and ck_strides[3] == 1 and
+                    heads == hk and cd == d and ck.get_device() == dev and cv.dtype is bf16 and
+                    cv_strides[3] == 1 and cv.shape == (pages, page_size, hk, dv) and
+                    cv.get_device() == dev and _dense(slots, ty.i64, dev, (T,)))
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if not fine:
         _rows(q, 3, "q")
-        if cache is not None and (v is None or slots is None):
-            raise ValueError("a cache needs v and slots")
-        _explain(q.device, dict(zip(("q", "k", "v", "cache.k", "cache.v"), rows)),
-                 {"cos": (cos, torch.float32, 2), "sin": (sin, torch.float32, 2),
-                  "positions": (positions, torch.int32, 1), "q_weight": (q_weight, torch.bfloat16, 1),
-                  "k_weight": (k_weight, torch.bfloat16, 1), "slots": (slots, torch.int64, 1)})
-    T, hq, d = q.shape
-    tk, hk, dk = k.shape
-    max_pos, half = cos.shape
-    if tk != T or dk != d:
-        raise ValueError("q and k must have the same tokens and channels")
-    if sin.shape != cos.shape:
-        raise ValueError("cos and sin must have the same shape")
-    if positions.shape[0] != T:
-        raise ValueError("positions must have one entry per token")
-    if (q_weight is not None and q_weight.shape[0] != d) or \
-            (k_weight is not None and k_weight.shape[0] != d):
-        raise ValueError(f"q_weight and k_weight must have {d} entries")
+        _explain(q.device, {"q": (q, 3), "k": (k, 3),
+                            **({} if cache is None else {"v": (v, 3), "cache.k": (cache[0], 4),
+                                                         "cache.v": (cache[1], 4)})},
+                 {"cos": (cos, ty.f32, 2), "sin": (sin, ty.f32, 2), "positions": (positions, ty.i32, 1),
+                  "q_weight": (q_weight, bf16, 1), "k_weight": (k_weight, bf16, 1),
+                  "slots": (slots, ty.i64, 1)})
+        raise ValueError("the shapes of q [T, Hq, D], k [T, Hk, D], v [T, Hk, Dv], cos and sin "
+                         "[max_positions, R/2], positions and slots [T], the weights [D] and the cache "
+                         "[pages, page_size, Hk, D or Dv] do not match")
     if cache is None:
         k_out = k.new_empty((T, hk, d))
         fields = (k_out.data_ptr(), 0, min(T, 1), max(T, 1), hk, d, d, 0, hk * d, d, 0, 0, 0)
-        v_strides = (0, 0)
+        v_ptr = v0 = v1 = slots_ptr = 0
     else:
-        if slots is None:
-            raise ValueError("a cache needs v and slots")
-        fields, (_, _, heads, cdk, cdv) = _cache_fields(cache)
-        if heads != hk or cdk != d or v.shape != (T, heads, cdv):
-            raise ValueError("k and v do not match the cache's heads and channels")
-        if slots.shape[0] != T:
-            raise ValueError("slots must have one entry per token")
-        v_strides = v.stride()[:2]
+        fields = (ck.data_ptr(), cv.data_ptr(), pages, page_size, hk, d, dv, *ck_strides[:3],
+                  *cv_strides[:3])
+        v_ptr, slots_ptr = v.data_ptr(), slots.data_ptr()
     q_out = _new_output(out, (T, hq, d), q)
     args = _pack_norm_rope(
-        q.data_ptr(), k.data_ptr(), _ptr(v), *q.stride()[:2], *k.stride()[:2], *v_strides,
-        _ptr(q_weight), _ptr(k_weight), cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), _ptr(slots),
-        q_out.data_ptr(), *fields, T, hq, max_pos, rot_start, 2 * half, 1 if interleaved else 0, eps)
+        q.data_ptr(), k.data_ptr(), v_ptr, q0, q1, k0, k1, v0, v1,
+        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+        cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), slots_ptr, q_out.data_ptr(), *fields, T, hq,
+        max_pos, rot_start, 2 * half, 1 if interleaved else 0, eps)
     status = (_lib or load()).fp8bs_qk_norm_rope(args, _raw_stream(dev))
     if status:
         raise Fp8bsError("fp8bs_qk_norm_rope", status)
@@ -666,32 +657,42 @@ def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=Tr
     [B+1] and kv_len int32 [B] are on the GPU; max_q_len and max_kv_len bound them for the host
     (default: T, and what the table can hold; tighter is faster). window > 0: each query sees that
     many keys at most, its own the last."""
-    import torch
-    i32 = torch.int32
-    rows = ((q, 3), (cache[0], 4), (cache[1], 4))
-    dense = ((page_table, i32, 2), (q_start, i32, 1), (kv_len, i32, 1))
-    dev = _device_index(q)
-    if not _fine(dev, rows, dense):
+    ty = _types if _types.ready else _types.load()
+    bf16, i32 = ty.bf16, ty.i32
+    ck, cv = cache
+    try:
+        T, hq, dk = q.shape
+        pages, page_size, heads, cdk = ck.shape
+        dv = cv.shape[3]
+        B, n = table = page_table.shape
+        dev = q.get_device()
+        q0, q1, q2 = q.stride()
+        ck_strides, cv_strides = ck.stride(), cv.stride()
+        fine = (dev >= 0 and q.dtype is bf16 and q2 == 1 and dk == cdk and hq % heads == 0 and
+                ck.dtype is bf16 and ck_strides[3] == 1 and ck.get_device() == dev and
+                cv.dtype is bf16 and cv_strides[3] == 1 and cv.get_device() == dev and
+                cv.shape == (pages, page_size, heads, dv) and _dense(page_table, i32, dev, table) and
+                _dense(q_start, i32, dev, (B + 1,)) and _dense(kv_len, i32, dev, (B,)))
+    except (AttributeError, ValueError, TypeError, ZeroDivisionError):
+        fine = False
+    if not fine:
         _rows(q, 3, "q")
-        _explain(q.device, dict(zip(("q", "cache.k", "cache.v"), rows)),
-                 dict(zip(("page_table", "q_start", "kv_len"), dense)))
-    fields, (_, page_size, heads, cdk, dv) = _cache_fields(cache)
-    T, hq, dk = q.shape
-    if dk != cdk or hq % max(heads, 1):
-        raise ValueError("q does not match the cache's channels, or its heads are no multiple")
-    B, n = page_table.shape
-    if kv_len.shape[0] != B or q_start.shape[0] != B + 1:
-        raise ValueError("page_table, q_start and kv_len must agree on the number of sequences")
+        _explain(q.device, {"q": (q, 3), "cache.k": (ck, 4), "cache.v": (cv, 4)},
+                 {"page_table": (page_table, i32, 2), "q_start": (q_start, i32, 1),
+                  "kv_len": (kv_len, i32, 1)})
+        raise ValueError("the shapes of q [T, Hq, Dk], the cache [pages, page_size, Hk, Dk or Dv] (Hk "
+                         "dividing Hq), page_table [B, n], q_start [B+1] and kv_len [B] do not match")
     o = _new_output(out, (T, hq, dv), q)
-    lse = q.new_empty((T, hq), dtype=torch.float32) if return_lse else None
+    lse = ty.empty((T, hq), dtype=ty.f32, device=q.device) if return_lse else None
     stream = _raw_stream(dev)
     lib = _lib or load()
     # The library says whether the workspace at hand is large enough; if not, it is asked how much it takes.
     ws = _scratch.get((dev, stream)) or (0, 0)
     while True:
         args = _pack_attention(
-            q.data_ptr(), *q.stride()[:2], *fields, page_table.data_ptr(), n, q_start.data_ptr(),
-            kv_len.data_ptr(), o.data_ptr(), _ptr(lse), B, T, hq, T if max_q_len is None else max_q_len,
+            q.data_ptr(), q0, q1, ck.data_ptr(), cv.data_ptr(), pages, page_size, heads, dk, dv,
+            *ck_strides[:3], *cv_strides[:3], page_table.data_ptr(), n, q_start.data_ptr(),
+            kv_len.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(), B, T, hq, T if max_q_len is None else max_q_len,
             n * page_size if max_kv_len is None else max_kv_len, window, 1 if causal else 0,
             dk ** -0.5 if scale is None else scale, ws[0], ws[1])
         status = lib.fp8bs_paged_attention(args, stream)
@@ -707,24 +708,30 @@ def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=Tr
 
 
 def _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale):
-    import torch
-    rows = ((x, torch.bfloat16, 2), (router_w, torch.bfloat16, 2), (bias, torch.float32, 1))
-    if not _fine(_device_index(x), (), rows):
-        _require(x, torch.bfloat16, 2, "x")
-        _explain(x.device, {}, dict(zip(("x", "router_w", "bias"), rows)))
-    experts, dim = router_w.shape
-    if dim != x.shape[1]:
-        raise ValueError("router_w must have x's channels")
-    if bias is not None and bias.shape[0] != experts:
-        raise ValueError("bias must have one entry per expert")
-    if score not in ("sigmoid", "softmax"):
+    """(CUDA device, experts, the packed fp8bs_moe_routing), checked."""
+    ty = _types if _types.ready else _types.load()
+    try:
+        T, D = x.shape
+        experts = router_w.shape[0]
+        dev = x.get_device()
+        fine = (dev >= 0 and x.dtype is ty.bf16 and x.is_contiguous() and
+                _dense(router_w, ty.bf16, dev, (experts, D)) and
+                (bias is None or _dense(bias, ty.f32, dev, (experts,))))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fine = False
+    if not fine:
+        _require(x, ty.bf16, 2, "x")
+        _explain(x.device, {}, {"x": (x, ty.bf16, 2), "router_w": (router_w, ty.bf16, 2),
+                                "bias": (bias, ty.f32, 1)})
+        raise ValueError("the shapes of x [T, D], router_w [E, D] and bias [E] do not match")
+    if score == "sigmoid":
+        kind, normalise = SCORE_SIGMOID, 1 if normalise is None else int(normalise)
+    elif score == "softmax":
+        kind, normalise = SCORE_SOFTMAX, 0 if normalise is None else int(normalise)
+    else:
         raise ValueError(f"unknown score {score!r}")
-    sigmoid = score == "sigmoid"
-    if normalise is None:
-        normalise = sigmoid
-    return experts, _pack_routing(router_w.data_ptr(), _ptr(bias), top_k, groups, topk_groups,
-                                  SCORE_SIGMOID if sigmoid else SCORE_SOFTMAX, 1 if normalise else 0,
-                                  route_scale)
+    return dev, experts, _pack_routing(router_w.data_ptr(), 0 if bias is None else bias.data_ptr(), top_k,
+                                       groups, topk_groups, kind, normalise, route_scale)
 
 
 def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_groups=1, normalise=None,
@@ -733,32 +740,39 @@ def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_gro
     int32 [T, top_k], best first). bias fp32 [E] shifts the choice only; groups/topk_groups limit it
     to the best groups of experts; normalise (default: for sigmoid scores) makes a token's weights
     sum to route_scale."""
-    import torch
-    experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
+    dev, experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise,
+                                     route_scale)
     T, D = x.shape
-    weights = x.new_empty((T, top_k), dtype=torch.float32)
-    ids = x.new_empty((T, top_k), dtype=torch.int32)
+    weights = x.new_empty((T, top_k), dtype=_types.f32)
+    ids = x.new_empty((T, top_k), dtype=_types.i32)
     _check("fp8bs_moe_route", (_lib or load()).fp8bs_moe_route(
-        x.data_ptr(), routing, weights.data_ptr(), ids.data_ptr(), T, D, experts,
-        _raw_stream(x.get_device())))
+        x.data_ptr(), routing, weights.data_ptr(), ids.data_ptr(), T, D, experts, _raw_stream(dev)))
     return weights, ids
 
 
 def _expert_shapes(x, w13, s13, w2, s2, weights=None, ids=None):
-    import torch
-    e4m3, f32 = torch.float8_e4m3fn, torch.float32
-    dense = ((x, torch.bfloat16, 2), (w13, e4m3, 3), (s13, f32, 3), (w2, e4m3, 3), (s2, f32, 3),
-             (weights, f32, 2), (ids, torch.int32, 2))
-    dev = _device_index(x)
-    if not _fine(dev, (), dense):
-        _require(x, torch.bfloat16, 2, "x")
-        _explain(x.device, {}, dict(zip(("x", "w13", "s13", "w2", "s2", "weights", "ids"), dense)))
-    T, D = x.shape
-    E, rows, inter = w2.shape
-    if rows != D or w13.shape != (E, 2 * inter, D) or \
-            s13.shape != (E, 2 * inter // BLOCK, D // BLOCK) or \
-            s2.shape != (E, D // BLOCK, inter // BLOCK):
-        raise ValueError("expert weight or scale shapes do not match")
+    """(CUDA device, T, D, I, E), checked."""
+    ty = _types if _types.ready else _types.load()
+    f32, e4m3 = ty.f32, ty.e4m3
+    try:
+        T, D = x.shape
+        E, _, inter = w2.shape
+        dev = x.get_device()
+        kb, ib = D // BLOCK, inter // BLOCK
+        fine = (dev >= 0 and x.dtype is ty.bf16 and x.is_contiguous() and
+                _dense(w13, e4m3, dev, (E, 2 * inter, D)) and _dense(w2, e4m3, dev, (E, D, inter)) and
+                _dense(s13, f32, dev, (E, 2 * inter // BLOCK, kb)) and _dense(s2, f32, dev, (E, kb, ib)) and
+                (ids is None or (_dense(ids, ty.i32, dev, (T, ids.shape[1])) and
+                                 _dense(weights, f32, dev, ids.shape))))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fine = False
+    if not fine:
+        _require(x, ty.bf16, 2, "x")
+        _explain(x.device, {}, {"x": (x, ty.bf16, 2), "w13": (w13, e4m3, 3), "s13": (s13, f32, 3),
+                                "w2": (w2, e4m3, 3), "s2": (s2, f32, 3), "weights": (weights, f32, 2),
+                                "ids": (ids, ty.i32, 2)})
+        raise ValueError("the shapes of x [T, D], w13 [E, 2I, D], s13 [E, 2I/128, D/128], w2 [E, D, I], "
+                         "s2 [E, D/128, I/128] (and weights, ids [T, top_k]) do not match")
     return dev, T, D, inter, E
 
 
@@ -775,8 +789,6 @@ def moe_experts(x, weights, ids, w13, s13, w2, s2, scale_fmt="fp32", out=None):
     and weights fp32 [T, top_k] as moe_route gives them -> y bf16 [T, D]."""
     dev, T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2, weights, ids)
     k = ids.shape[1]
-    if weights.shape != ids.shape or ids.shape[0] != T:
-        raise ValueError("weights and ids must be [T, top_k]")
     y = _new_output(out, (T, D), x)
     stream = _raw_stream(dev)
     lib = _lib or load()
@@ -790,7 +802,8 @@ def moe_experts(x, weights, ids, w13, s13, w2, s2, scale_fmt="fp32", out=None):
 def moe_layer(x, router_w, w13, s13, w2, s2, top_k, bias=None, score="sigmoid", groups=1,
               topk_groups=1, normalise=None, route_scale=1.0, scale_fmt="fp32", out=None):
     """A whole mixture-of-experts layer for x bf16 [T <= 64, D]: moe_route, then moe_experts."""
-    experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale)
+    _, experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise,
+                                   route_scale)
     dev, T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
     if experts != E:
         raise ValueError("router_w must have one row per expert")

@@ -8,9 +8,9 @@
 //                  into TMEM in place of S
 //   O += P V       tcgen05.mma, P from TMEM, V from shared memory as the cache holds it (keys
 //                  outermost: an MN-major operand), O fp32 in TMEM
-// The maximum only moves when it has grown by more than 2^8 (kRescale): O is then scaled in TMEM by
-// its softmax warps; otherwise P is that much larger than 1 at most, which bf16 and fp32 hold without
-// loss, and O is left alone. The row sum is taken from P before its rounding to bf16, so lse is exact
+// The maximum only moves when it has grown by more than 2^8 (kRescale): the tile's probabilities are then
+// computed again and O is scaled in TMEM by its softmax warps; otherwise P is that much larger than 1 at most,
+// which bf16 and fp32 hold without loss, and O is left alone. So no row waits for its maximum. The row sum is taken from P before its rounding to bf16, so lse is exact
 // to binary32; the rounding of P (2^-9 on average per term) is of the size of the output's own.
 //
 // Two forms (AttnCfg): NQ = 2 query tiles per CTA for chunks, whose softmax warps work on one tile
@@ -35,7 +35,6 @@ struct AttnCfg {
     static constexpr int DK = DK_, DV = DV_, NQ = NQ_;
     static constexpr int BN = NQ == 2 ? 128 : 64;                // keys per tile
     static constexpr int ROWS = NQ * 128;
-    static constexpr int PARTS = BN == 128 ? 2 : 1;              // P is handed over in so many parts
     static constexpr int SLOTS = 4;                              // ring of work items
     static constexpr int SBUF = 2;                               // S buffers: per query tile, or 2
     static constexpr int K_TILE = BN * DK * 2, V_TILE = BN * DV * 2, Q_TILE = 128 * DK * 2;
@@ -48,7 +47,7 @@ struct AttnCfg {
     // (two query tiles: a whole third warpgroup beside the softmax's, for the split of registers below)
     static constexpr int THREADS = 32 * (SOFT_WARPS + (NQ == 2 ? 4 : 3));
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
-    static constexpr int BARS = 2 * KST + 2 * VST + (1 + PARTS) * SBUF + 3 * NQ + 2 + 2 * SLOTS;
+    static constexpr int BARS = 2 * KST + 2 * VST + 2 * SBUF + 3 * NQ + 2 + 2 * SLOTS;
     static constexpr int SMEM = 1024 + NQ * Q_TILE + KST * K_TILE + VST * V_TILE + BARS * 8 + 64;
     static_assert(SMEM <= kSmemLimit, "shared memory");
 };
@@ -390,8 +389,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint64_t* v_full = k_empty + Cfg::KST;
     uint64_t* v_empty = v_full + Cfg::VST;
     uint64_t* s_full = v_empty + Cfg::VST;                // [SBUF]
-    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF][PARTS]
-    uint64_t* q_full = p_full + Cfg::PARTS * Cfg::SBUF;   // [NQ] queries of an item
+    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF]
+    uint64_t* q_full = p_full + Cfg::SBUF;   // [NQ] queries of an item
     uint64_t* o_done = q_full + NQ;                       // [NQ] each product with V
     uint64_t* o_last = o_done + NQ;                       // [NQ] the last one of an item
     uint64_t* v_tail = o_last + NQ;                       // an item's last, partly valid value tile
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         for (int i = 0; i < Cfg::SBUF; ++i) {
             mbar_init(&s_full[i], 1);
-            for (int k = 0; k < Cfg::PARTS; ++k) mbar_init(&p_full[Cfg::PARTS * i + k], 4);
+            mbar_init(&p_full[i], 4);
         }
         for (int i = 0; i < NQ; ++i) {
             mbar_init(&q_full[i], 4);
@@ -452,9 +451,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     };
 
     // Two query tiles, registers: 168 x 384 threads at launch; the softmax's row of S needs more, the third
-    // warpgroup less (200 x 256 + 96 x 128 = 63488 of 64512).
+    // warpgroup less (208 x 256 + 80 x 128 = 63488 of 64512).
     if (warp < Cfg::SOFT_WARPS) {
-        if constexpr (NQ == 2) regs_inc<200>();
+        if constexpr (NQ == 2) regs_inc<208>();
         // ---- softmax warps: thread = row of query tile q
         const int q = warp >> 2;
         const int quarter = warp & 3;
@@ -548,78 +547,89 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     tc_fence_after();
                     if (!idle) {
                         const uint32_t s_tmem_row = tmem + lanes + buf * BN;
-                        float s[BN];
-#pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) tmem_ld_32cols(s_tmem_row + 32 * i, s + 32 * i);
-#pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_32(s + 32 * i);
                         const int kb = k0 + j * BN;
-                        if (kb < full_lo || kb + BN > full_hi) {
-                            const int lo = row_lo - kb, hi = row_hi - kb;
+                        const bool masked = kb < full_lo || kb + BN > full_hi;
+                        uint32_t p[BN / 2];
+                        float2 sum[2];
+                        auto load_row = [&](float* s) {
 #pragma unroll
-                            for (int i = 0; i < BN; ++i)
-                                if (i < lo || i >= hi) s[i] = -INFINITY;
-                        }
-                        float mx[4] = {s[0], s[1], s[2], s[3]};
+                            for (int i = 0; i < BN / 32; ++i) tmem_ld_32cols(s_tmem_row + 32 * i, s + 32 * i);
 #pragma unroll
-                        for (int i = 4; i < BN; i += 4) {
-                            mx[0] = fmaxf(mx[0], s[i]);
-                            mx[1] = fmaxf(mx[1], s[i + 1]);
-                            mx[2] = fmaxf(mx[2], s[i + 2]);
-                            mx[3] = fmaxf(mx[3], s[i + 3]);
+                            for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_32(s + 32 * i);
+                            if (masked) {
+                                const int lo = row_lo - kb, hi = row_hi - kb;
+#pragma unroll
+                                for (int i = 0; i < BN; ++i)
+                                    if (i < lo || i >= hi) s[i] = -INFINITY;
+                            }
+                        };
+                        // Probabilities with the maximum in use, and this tile's maximum beside them: it is only
+                        // looked at afterwards, and hardly ever asks for another pass (kRescale). The first tile
+                        // of a row has no maximum yet and looks before; so does the form with one query tile,
+                        // whose softmax waits for the keys (64 ragged sequences: 192 us, 204 the other way; the
+                        // chunk of 4096 with two tiles: 321 and 313).
+                        float top = m;
+                        auto probabilities = [&](const float* s) {
+                            const float mc = m == -INFINITY ? 0.0f : m * c;
+                            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int k = 0; k < BN / 2; ++k) {
+                                mx[k & 3] = fmaxf(mx[k & 3], fmaxf(s[2 * k], s[2 * k + 1]));
+                                float2 y = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), c2, mc2);
+                                y.x = exp2_fast(y.x);
+                                y.y = exp2_fast(y.y);
+                                sum[k & 1] = __fadd2_rn(sum[k & 1], y);
+                                p[k] = pack_bf16x2(y.x, y.y);
+                            }
+                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        };
+                        bool look = NQ == 1 || j == 0 || __any_sync(0xffffffffu, m == -INFINITY);
+                        if (!look) {
+                            float s[BN];
+                            load_row(s);
+                            probabilities(s);
+                            look = __any_sync(0xffffffffu, (top - m) * c > kRescale);
                         }
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
-                        if (__any_sync(0xffffffffu, grow)) {
+                        if (look) {
+                            float s[BN];
+                            load_row(s);
+                            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                            for (int i = 4; i < BN; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                            const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
                             const float keep = grow ? exp2_fast((m - top) * c) : 1.0f;
                             if (grow) m = top;
                             l *= keep;
-                            if (j > 0) {
+                            probabilities(s);
+                            if (j > 0 && __any_sync(0xffffffffu, grow)) {
                                 if (!warp_wait(&o_done[q], (n - 1) & 1)) {
                                     ok = false;
                                     break;
                                 }
                                 tc_fence_after();
 #pragma unroll 1
-                                for (int i = 0; i < DV / 32; ++i) {
-                                    float o[32];
-                                    tmem_ld_32cols(o_tmem + 32 * i, o);
-                                    tmem_wait_ld_32(o);
+                                for (int i = 0; i < DV / 16; ++i) {
+                                    float o[16];
+                                    tmem_ld_16cols(o_tmem + 16 * i, o);
+                                    tmem_wait_ld_16(o);
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k) o[k] *= keep;
-                                    tmem_st_32cols(o_tmem + 32 * i, reinterpret_cast<const uint32_t*>(o));
+                                    for (int k = 0; k < 16; ++k) o[k] *= keep;
+                                    tmem_st_16cols(o_tmem + 16 * i, reinterpret_cast<const uint32_t*>(o));
                                 }
                             }
                         }
-                        const float mc = m == -INFINITY ? 0.0f : m * c;
-                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                        const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
 #pragma unroll
-                        for (int part = 0; part < Cfg::PARTS; ++part) {
-                            constexpr int H = BN / Cfg::PARTS;
-#pragma unroll
-                            for (int i = 0; i < H / 32; ++i) {
-                                uint32_t p[16];
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    const int e = part * H + 32 * i + 2 * k;
-                                    float2 y = __ffma2_rn(make_float2(s[e], s[e + 1]), c2, mc2);
-                                    y.x = exp2_fast(y.x);
-                                    y.y = exp2_fast(y.y);
-                                    sum[k & 1] = __fadd2_rn(sum[k & 1], y);
-                                    p[k] = pack_bf16x2(y.x, y.y);
-                                }
-                                tmem_st_16cols(s_tmem_row + part * (H / 2) + 16 * i, p);
-                            }
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&p_full[Cfg::PARTS * buf + part]);
-                        }
+                        for (int i = 0; i < BN / 32; ++i) tmem_st_16cols(s_tmem_row + 16 * i, p + 16 * i);
                         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[buf]);
                     } else if (lane == 0) {
-                        for (int part = 0; part < Cfg::PARTS; ++part)
-                            mbar_arrive(&p_full[Cfg::PARTS * buf + part]);
+                        mbar_arrive(&p_full[buf]);
                     }
                 }
                 n0 += nt;
@@ -683,7 +693,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
     } else {
-        if constexpr (NQ == 2) regs_dec<96>();
+        if constexpr (NQ == 2) regs_dec<80>();
         if (warp == Cfg::KEY_WARP) {
             // ---- hands out the items and brings their keys
             ItemFinder finder;
@@ -744,8 +754,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 mbar_wait(v_tail, vs.tails & 1, kDrainLimitNs);
             }
         } else if (warp == Cfg::MMA_WARP) {
-            // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j) in the parts that the softmax hands
-            // over, then S of the tile's next keys, which takes P's place (the tensor core works in order).
+            // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j), then S of the tile's next keys, which
+            // takes P's place (the tensor core works in order).
             // With two query tiles one's products run under the other's softmax.
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV) | kIdescBMajorMN;
@@ -804,29 +814,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
                         const int buf = NQ == 2 ? q : n & 1;
-#pragma unroll
-                        for (int part = 0; part < Cfg::PARTS; ++part) {
-                            if (!ok || !warp_wait(&p_full[Cfg::PARTS * buf + part], pph)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int k = part * (BN / 16 / Cfg::PARTS);
-                                     k < (part + 1) * (BN / 16 / Cfg::PARTS); ++k)
-                                    mma_bf16_ta(o_tmem + q * DV, tmem + buf * BN + 8 * k,
-                                                vd + k * (DV / 64 * 2048 / 16), idesc_pv,
-                                                j > 0 || k > 0 ? 1u : 0u);
-                                if (part == Cfg::PARTS - 1) {
-                                    mma_commit(&o_done[q]);
-                                    if (q == NQ - 1) mma_commit(&v_empty[st]);
-                                    if (j == nt - 1) mma_commit(&o_last[q]);
-                                }
-                            }
-                            __syncwarp();
+                        if (!warp_wait(&p_full[buf], pph)) {
+                            ok = false;
+                            break;
                         }
-                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < BN / 16; ++k)
+                                mma_bf16_ta(o_tmem + q * DV, tmem + buf * BN + 8 * k,
+                                            vd + k * (DV / 64 * 2048 / 16), idesc_pv,
+                                            j > 0 || k > 0 ? 1u : 0u);
+                            mma_commit(&o_done[q]);
+                            if (q == NQ - 1) mma_commit(&v_empty[st]);
+                            if (j == nt - 1) mma_commit(&o_last[q]);
+                        }
+                        __syncwarp();
                         const int next = NQ == 2 ? j + 1 : j + 2;
                         if (next < nt) ok = qk(q, n0 + next);
                     }
