@@ -639,13 +639,15 @@ _scratch = {}
 
 
 def _scratch_bytes(dev, stream, nbytes):
-    """Device memory of at least nbytes for one call on `stream`: one buffer per device and stream, kept
-    and grown (calls on one stream follow one another, so they can share it) -> (pointer, bytes)."""
-    import torch
+    """Device memory of at least nbytes for one call on `stream`: one buffer per device and stream (calls on
+    one stream follow one another, so they can share it) -> (pointer, bytes, ...). It grows by doubling, and
+    the smaller ones before it are kept: a captured graph may still use them."""
     buf = _scratch.get((dev, stream))
     if buf is None or buf[1] < nbytes:
-        t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=torch.device("cuda", dev))
-        buf = _scratch[(dev, stream)] = (t.data_ptr(), t.numel(), t)
+        import torch
+        size = max(nbytes, 2 * buf[1] if buf else 1 << 20)
+        t = torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", dev))
+        buf = _scratch[(dev, stream)] = (t.data_ptr(), size, t, buf)
     return buf
 
 

@@ -118,7 +118,7 @@ int check_attention_sizes(const fp8bs_paged_attention_args& a) {
     if (a.B < 0 || a.B >= (1 << 20) || a.T < 0 || a.T >= kMaxDim || a.q_heads < 1 ||
         a.q_heads >= (1 << 16) || a.cache.heads < 1 || a.q_heads % a.cache.heads || a.window < 0 ||
         a.max_q_len < 0 || a.max_q_len > a.T || a.max_kv_len < 0 || a.max_kv_len >= kMaxDim - 1024 ||
-        a.table_stride < 0 || a.T * (a.q_heads / a.cache.heads) >= kMaxDim)
+        a.table_stride < 0 || a.T * (a.q_heads / a.cache.heads) >= kMaxDim - 1024)
         return FP8BS_ERR_INVALID_ARG;
     if (a.T > 0 && (a.B < 1 || a.max_q_len < 1)) return FP8BS_ERR_INVALID_ARG;
     if (a.cache.page_size < 1 ||

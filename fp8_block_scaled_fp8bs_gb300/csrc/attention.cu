@@ -130,7 +130,9 @@ __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_atten
             for (int i = 0; i < 8; ++i) {
                 const int n = f.start[i + 1] - f.start[i];
                 f.units[i] = 0;
-                if (n > 0) {
+                if (n > a.max_q_len || f.kv[i] > a.max_kv_len) {
+                    f.units[i] = 1;      // out of bounds: handed out once, to be reported
+                } else if (n > 0) {
                     const Cut c = cut_of(a, rows, piece_len, n, f.kv[i], group);
                     f.units[i] = c.tiles * c.pieces;
                 }
@@ -275,8 +277,9 @@ struct Stream {
 // The key tiles k0, k0 + BN, ... (nt of them) of an item into the ring of KEYS or values, by TMA in boxes of
 // 2^box_log2 slots. The pages of 32 boxes are looked up at once, one per lane, while those before are in use, and
 // each box is issued by a lane of its own (one lane for all: 64 ragged sequences with pages of 16 slots took 273
-// instead of 204 us, a chunk of 4096 over 8192 keys 364 instead of 335). The last value tile is
-// cleared past the sequence's end before it counts: whatever stands there must not meet a probability of zero.
+// instead of 204 us, a chunk of 4096 over 8192 keys 364 instead of 335). Values of the
+// first and last tile that do not count are cleared before the tile does: whatever stood there must not meet a
+// probability of zero.
 template <class Cfg, bool KEYS>
 __device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, const fp8bs_paged_attention_args& a,
                                             const Item& it, int k0, int nt, int box_log2, int mode, uint8_t* ring,
@@ -290,38 +293,47 @@ __device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, c
     const int boxes = BN >> box_log2;
     const int page_size = static_cast<int>(a.cache.page_size);
     const int heads = static_cast<int>(a.cache.heads);
-    const int head = it.head, kv = it.kv;
+    const int head = it.head, kv = it.kv, key_lo = it.key_lo;
     const int32_t* table = a.page_table + it.seq * a.table_stride;
     auto lookup = [&](int w) {               // boxes 32 w .. 32 w + 31 of the item
         const int64_t key = k0 + (static_cast<int64_t>(w) * 32 + lane) * box;
         int2 at = make_int2(0, 0);
-        if (key < kv) {
+        if (key < kv && key + box > key_lo) {
             const int p = static_cast<int>(key) / page_size;
             at.y = static_cast<int>(key) - p * page_size;
             at.x = table[p];
         }
         return at;
     };
+    int window_at = 0;                       // the 32 boxes that `next` is of
     int2 next = lookup(0);
     for (int j = 0; j < nt; ++j) {
         const int key0 = k0 + j * BN;
+        // boxes [none, live) hold keys that count: those before them are past a window (their pages may have been
+        // given back), those after them past the sequence
         const int live = min(boxes, (kv - key0 + box - 1) >> box_log2);
+        const int none = j == 0 ? (key_lo - k0) >> box_log2 : 0;
         const int st = s.n % STAGES;
         if (!warp_wait(&empty[st], ((s.n / STAGES) & 1) ^ 1)) return false;
-        const bool partial = !KEYS && kv - key0 < BN;
+        const bool partial = !KEYS && (kv - key0 < BN || none > 0);
         uint64_t* bar = partial ? tail : &full[st];
         const uint32_t dst = smem_addr(ring) + st * TILE;
-        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live * box * CH * 128));
-        for (int b = 0; b < live;) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>((live - none) * box * CH * 128));
+        for (int b = none; b < live;) {
             const int first = j * boxes + b;
-            if ((first & 31) == 0) {
+            if ((first & 31) == 0 || (j == 0 && b == none)) {
+                // (the first look may begin inside a window of 32 boxes)
+                while (window_at < first >> 5) {
+                    next = lookup(++window_at);
+                }
                 // a page outside the cache: a coordinate past the end, which reads as zeros
                 if (static_cast<unsigned>(next.x) >= static_cast<unsigned>(a.cache.pages)) {
                     next.x = static_cast<int>(a.cache.pages);
-                    if (KEYS && k0 + (first + lane) * int64_t{1} * box < kv) record_error(FP8BS_DEVERR_INDEX);
+                    const int64_t key = k0 + (static_cast<int64_t>(window_at) * 32 + lane) * box;
+                    if (KEYS && key < kv && key + box > key_lo) record_error(FP8BS_DEVERR_INDEX);
                 }
                 window[lane] = next;
-                next = lookup((first >> 5) + 1);
+                next = lookup(++window_at);
                 __syncwarp();
             }
             const int count = min(32 - (first & 31), live - b);
@@ -344,9 +356,11 @@ __device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, c
         if (partial) {
             if (!warp_wait(tail, s.tails & 1)) return false;
             ++s.tails;
-            const int keep = kv - key0;
-            for (int i = lane; i < (BN - keep) * CH * 8; i += 32) {
-                const int key = keep + i / (CH * 8);
+            const int skip = none << box_log2;
+            const int keep = min(kv - key0, BN);
+            for (int i = lane; i < (BN - keep + skip) * CH * 8; i += 32) {
+                const int k = i / (CH * 8);
+                const int key = k < skip ? k : keep + k - skip;
                 const int c = i / 8 % CH;
                 *reinterpret_cast<uint4*>(ring + st * TILE + (key >> 3) * (CH * 1024) + c * 1024 +
                                           (key & 7) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);

@@ -399,14 +399,15 @@ FP8BS_API int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stre
  *
  * with query head h reading key head h / (q_heads / cache.heads). Scores, softmax sums and o are
  * held in binary32, the probabilities rounded to bf16 for their product with v, o to bf16 at the
- * end. A query with no key gets o = 0, lse = -inf. Keys at and past L and pages past them are
- * never used, whatever they hold (their table entries are not read); values of keys below L have
- * to be finite. A page id outside the cache sets FP8BS_DEVERR_INDEX and reads as zeros.
+ * end. A query with no key gets o = 0, lse = -inf. Keys at and past L, and pages that end before
+ * the window of a sequence's first query, are never used, whatever they hold (their table entries
+ * are not read: the pages may have been given back); the values of the other keys have to be
+ * finite, those outside a query's window too. A page id outside the cache sets FP8BS_DEVERR_INDEX and reads as zeros.
  *
  *   q [T, q_heads, dk] bf16, rows contiguous and 16-byte aligned, strides multiples of 8.
  *   out bf16 [T, q_heads, dv] contiguous, 16-byte aligned. lse fp32 [T, q_heads] or NULL.
- *   page_table int32 [B, table_stride]; q_start int32 [B+1], q_start[0] = 0, q_start[B] = T;
- *   kv_len int32 [B].   (dk, dv): (64, 64), (128, 128) or (192, 128).
+ *   page_table int32 [B, table_stride]; q_start int32 [B+1], q_start[0] = 0, q_start[B] = T (rows
+ *   of out past a smaller q_start[B] are left undefined); kv_len int32 [B].   (dk, dv): (64, 64), (128, 128) or (192, 128).
  *   max_q_len, max_kv_len: bounds on n and L that the caller knows on the host; they steer how
  *       the work is cut (max_kv_len at most 2^31 - 1024). A sequence past them sets
  *       FP8BS_DEVERR_INDEX and leaves its rows of out undefined.

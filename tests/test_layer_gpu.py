@@ -285,6 +285,66 @@ def test_attention_window(window, hq, hk):
     attention_check(paged_case(4, news, lens, hq, hk, 64, 64, 16), news, lens, window=window)
 
 
+@pytest.mark.parametrize("page", [1, 5, 16, 64, 128])
+@pytest.mark.parametrize("T", [1, 20, 200])
+def test_attention_window_over_freed_pages(page, T):
+    # pages that end before the window have been given back: their entries are out of the cache, and their
+    # contents not numbers
+    news, lens, window = [T, 1], [1500, 700], 150
+    c = paged_case(16, news, lens, 4, 2, 128, 128, page)
+    ref = fp8bs.paged_attention(**c, window=window, return_lse=True)
+    for b, (n, L) in enumerate(zip(news, lens)):
+        gone = max(0, L - n - window + 1) // page
+        c["cache"].k[c["page_table"][b, :gone].long()] = float("nan")
+        c["cache"].v[c["page_table"][b, :gone].long()] = float("inf")
+        c["page_table"][b, :gone] = -1
+    out = fp8bs.paged_attention(**c, window=window, return_lse=True)
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+    assert bool(torch.isfinite(out[0].float()).all())
+
+
+def test_attention_reports_bad_lengths():
+    # one sequence past the caller's bounds: reported, and the others as ever
+    news, lens = [1, 1, 3], [100, 60, 40]
+    c = paged_case(17, news, lens, 4, 2, 64, 64, 16)
+    ref = fp8bs.paged_attention(**c)
+    c["kv_len"][1] = 10 ** 6
+    out = fp8bs.paged_attention(**c)
+    assert fp8bs.fp8bs_device_error(clear=True) == fp8bs.DEVERR_INDEX
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[2:], ref[2:])
+
+
+@pytest.mark.parametrize("B", [257, 700])
+def test_attention_many_sequences(B):
+    # more sequences than one look-up chunk holds, of every length, some without queries
+    news = [(b * 7) % 4 for b in range(B)]
+    lens = [max(n, (b * 13) % 90) for b, n in enumerate(news)]
+    attention_check(paged_case(18, news, lens, 2, 1, 64, 64, 16), news, lens)
+
+
+def test_scratch_memory_of_a_captured_graph_outlives_larger_calls():
+    news, lens = [1], [3000]
+    small = paged_case(19, news, lens, 8, 2, 128, 128, 16)
+    large = paged_case(20, [1] * 200, [3000] * 200, 8, 2, 128, 128, 16)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ref = fp8bs.paged_attention(**small)
+        out = torch.empty_like(ref)
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            fp8bs.paged_attention(**small, out=out)
+        big = fp8bs.paged_attention(**large)
+        other = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(40)]
+        s.synchronize()
+        out.zero_()
+        graph.replay()
+        s.synchronize()
+    assert torch.equal(out, ref) and bool(torch.isfinite(big.float()).all())
+    assert all(bool((o == 7).all()) for o in other)
+
+
 @pytest.mark.parametrize("window", [0, 50])
 def test_attention_not_causal(window):
     news, lens = [7, 130, 1], [300, 130, 0]
