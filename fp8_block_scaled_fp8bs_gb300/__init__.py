@@ -34,7 +34,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 from typing import Any, NamedTuple
 
@@ -130,14 +129,14 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                            vp]
         lib.fp8bs_gemm_grouped.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(ctypes.c_int64),
                                            i64, i64, i64, i32, vp]
-        # (argument structures: byref of one, or its bytes)
-        lib.fp8bs_qk_norm_rope.argtypes = [vp, vp]
-        lib.fp8bs_paged_attention.argtypes = [vp, vp]
-        lib.fp8bs_paged_attention_workspace_size.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+        lib.fp8bs_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeArgs), vp]
+        lib.fp8bs_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), vp]
+        lib.fp8bs_paged_attention_workspace_size.argtypes = [ctypes.POINTER(PagedAttentionArgs),
+                                                             ctypes.POINTER(ctypes.c_size_t)]
         lib.fp8bs_moe_workspace_size.argtypes = [i64] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
-        lib.fp8bs_moe_route.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
+        lib.fp8bs_moe_route.argtypes = [vp, ctypes.POINTER(MoeRouting), vp, vp, i64, i64, i64, vp]
         lib.fp8bs_moe_experts.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, ctypes.c_size_t, vp]
-        lib.fp8bs_moe_layer.argtypes = [vp] * 7 + [i64] * 4 + \
+        lib.fp8bs_moe_layer.argtypes = [vp, ctypes.POINTER(MoeRouting)] + [vp] * 5 + [i64] * 4 + \
             [i32, vp, ctypes.c_size_t, vp]
         lib.fp8bs_status_string.argtypes = [i32]
         lib.fp8bs_status_string.restype = ctypes.c_char_p
@@ -476,10 +475,8 @@ def fp8_gemm_grouped(a, a_s, b, b_s, row_offsets, scale_fmt="fp32", out=None):
 
 # ------------------------------------------------------------- around the products of a decoder layer
 #
-# These calls take microseconds on the GPU, so their host side is kept short: one pass over the tensors'
-# attributes decides whether everything is as it should be, and only if it is not do the checks that say what
-# is wrong run (_explain); the C structures are packed in one go (the ctypes structures above, field by field,
-# cost several microseconds a call).
+# These calls take a few microseconds on the GPU, so their host side (checks, outputs, workspaces) is compiled:
+# csrc/host.cpp.
 
 class PagedCache(NamedTuple):
     """Keys [pages, page_size, heads, dk] and values [pages, page_size, heads, dv], bf16 CUDA tensors
@@ -488,82 +485,27 @@ class PagedCache(NamedTuple):
     v: Any
 
 
-_KV_FORMAT = "PP11q"
-_pack_norm_rope = struct.Struct("@PPP6qPPPPPPP" + _KV_FORMAT + "5qif").pack
-_pack_attention = struct.Struct("@Pqq" + _KV_FORMAT + "PqPPPP6qifPN").pack
-_pack_routing = struct.Struct("@PP3qiif4x").pack
-_KV_SIZE, _NORM_ROPE_SIZE, _ATTENTION_SIZE, _ROUTING_SIZE = (
-    struct.calcsize("@" + f) for f in (_KV_FORMAT, "PPP6qPPPPPPP" + _KV_FORMAT + "5qif",
-                                       "Pqq" + _KV_FORMAT + "PqPPPP6qifPN", "PP3qiif4x"))
-assert (_KV_SIZE, _NORM_ROPE_SIZE, _ATTENTION_SIZE, _ROUTING_SIZE) == tuple(
-    ctypes.sizeof(c) for c in (KvCache, QkNormRopeArgs, PagedAttentionArgs, MoeRouting))
+HOST_PATH = os.path.join(_HERE, "_host.so")
+_host = None
 
 
-class _Types:
-    """torch's types, looked up once (the package itself does not import torch)."""
-    ready = False
-
-    def load(self):
-        import torch
-        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
-        self.i64, self.e4m3 = torch.int64, torch.float8_e4m3fn
-        self.empty = torch.empty
-        self.ready = True
-        return self
-
-
-_types = _Types()
-
-
-def _dense(t, dtype, dev, shape):
-    """Whether t is a contiguous tensor of this type and shape on CUDA device `dev`."""
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
-
-
-def _rows(t, ndim, name):
-    """A bf16 CUDA tensor whose last axis is contiguous."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be a {ndim}-D tensor with contiguous rows")
-    return t
-
-
-def _explain(device, rows, dense):
-    """The checks of types, devices and layouts, one by one, with what is wrong. rows: {name: (tensor, ndim)}, dense: {name:
-    (tensor, dtype, ndim)}."""
-    for name, (t, ndim) in rows.items():
-        _rows(t, ndim, name)
-    for name, (t, dtype, ndim) in dense.items():
-        if t is not None:
-            _require(t, dtype, ndim, name)
-    for name, (t, *_) in (*rows.items(), *dense.items()):
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, like the other tensors")
-
-
-_stream_of = None
-
-
-def _raw_stream(dev):
-    """The current stream of device `dev` (by torch's own shortcut where it has one: a Stream object
-    takes microseconds to make)."""
-    global _stream_of
-    if _stream_of is None:
-        import torch
-        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return _stream_of(dev)
-
-
-def _new_output(out, shape, like):
-    """The bf16 output of `shape`: new on the device of `like` (bf16), or the caller's `out`, checked."""
-    if out is None:
-        return _types.empty(shape, dtype=_types.bf16, device=like.device)
-    return _output(out, shape, like.device)
+def _load_host():
+    """The compiled host side, built if it is missing."""
+    global _host
+    load()
+    with _lock:
+        if _host is None:
+            import importlib.util
+            import torch  # noqa: F401  (its libraries have to be there first)
+            if not os.path.exists(HOST_PATH):
+                from . import build as _build
+                _build.build_host()
+            spec = importlib.util.spec_from_file_location("_host", HOST_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.init(LIB_PATH, Fp8bsError)
+            _host = module
+    return _host
 
 
 def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, rot_start=0,
@@ -572,83 +514,8 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     [T, Hk, D] by positions int32 [T]; cos, sin fp32 [max_positions, R/2] rotate the channels
     rot_start .. rot_start+R-1. With a PagedCache, the keys and v bf16 [T, Hk, Dv] go to its slots
     int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k)."""
-    ty = _types if _types.ready else _types.load()
-    bf16 = ty.bf16
-    if cache is None:
-        if v is not None or slots is not None:
-            raise ValueError("v and slots need a cache")
-    elif v is None or slots is None:
-        raise ValueError("a cache needs v and slots")
-    try:
-        T, hq, d = q.shape
-        hk = k.shape[1]
-        max_pos, half = table = cos.shape
-        dev = q.get_device()
-        q0, q1, q2 = q.stride()
-        k0, k1, k2 = k.stride()
-        fine = (dev >= 0 and q.dtype is bf16 and q2 == 1 and k.dtype is bf16 and k2 == 1 and
-                k.shape == (T, hk, d) and k.get_device() == dev and _dense(cos, ty.f32, dev, table) and
-                _dense(sin, ty.f32, dev, table) and _dense(positions, ty.i32, dev, (T,)) and
-                (q_weight is None or _dense(q_weight, bf16, dev, (d,))) and
-                (k_weight is None or _dense(k_weight, bf16, dev, (d,))))
-        if cache is not None:
-            ck, cv = cache
-            pages, page_size, heads, cd = ck.shape
-            dv = cv.shape[3]
-            v0, v1, v2 = v.stride()
-            ck_strides, cv_strides = ck.stride(), cv.stride()
-            fine = (fine and v.dtype is bf16 and v2 == 1 and v.shape == (T, hk, dv) and
-                    v.get_device() == dev and ck.dtype is bf16 and ck_strides[3] == 1 and
-                    heads == hk and cd == d and ck.get_device() == dev and cv.dtype is bf16 and
-                    cv_strides[3] == 1 and cv.shape == (pages, page_size, hk, dv) and
-                    cv.get_device() == dev and _dense(slots, ty.i64, dev, (T,)))
-    except (AttributeError, ValueError, TypeError):
-        fine = False
-    if not fine:
-        _rows(q, 3, "q")
-        _explain(q.device, {"q": (q, 3), "k": (k, 3),
-                            **({} if cache is None else {"v": (v, 3), "cache.k": (cache[0], 4),
-                                                         "cache.v": (cache[1], 4)})},
-                 {"cos": (cos, ty.f32, 2), "sin": (sin, ty.f32, 2), "positions": (positions, ty.i32, 1),
-                  "q_weight": (q_weight, bf16, 1), "k_weight": (k_weight, bf16, 1),
-                  "slots": (slots, ty.i64, 1)})
-        raise ValueError("the shapes of q [T, Hq, D], k [T, Hk, D], v [T, Hk, Dv], cos and sin "
-                         "[max_positions, R/2], positions and slots [T], the weights [D] and the cache "
-                         "[pages, page_size, Hk, D or Dv] do not match")
-    if cache is None:
-        k_out = k.new_empty((T, hk, d))
-        fields = (k_out.data_ptr(), 0, min(T, 1), max(T, 1), hk, d, d, 0, hk * d, d, 0, 0, 0)
-        v_ptr = v0 = v1 = slots_ptr = 0
-    else:
-        fields = (ck.data_ptr(), cv.data_ptr(), pages, page_size, hk, d, dv, *ck_strides[:3],
-                  *cv_strides[:3])
-        v_ptr, slots_ptr = v.data_ptr(), slots.data_ptr()
-    q_out = _new_output(out, (T, hq, d), q)
-    args = _pack_norm_rope(
-        q.data_ptr(), k.data_ptr(), v_ptr, q0, q1, k0, k1, v0, v1,
-        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
-        cos.data_ptr(), sin.data_ptr(), positions.data_ptr(), slots_ptr, q_out.data_ptr(), *fields, T, hq,
-        max_pos, rot_start, 2 * half, 1 if interleaved else 0, eps)
-    status = (_lib or load()).fp8bs_qk_norm_rope(args, _raw_stream(dev))
-    if status:
-        raise Fp8bsError("fp8bs_qk_norm_rope", status)
-    return q_out if cache is not None else (q_out, k_out)
-
-
-_scratch = {}
-
-
-def _scratch_bytes(dev, stream, nbytes):
-    """Device memory of at least nbytes for one call on `stream`: one buffer per device and stream (calls on
-    one stream follow one another, so they can share it) -> (pointer, bytes, ...). It grows by doubling, and
-    the smaller ones before it are kept: a captured graph may still use them."""
-    buf = _scratch.get((dev, stream))
-    if buf is None or buf[1] < nbytes:
-        import torch
-        size = max(nbytes, 2 * buf[1] if buf else 1 << 20)
-        t = torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", dev))
-        buf = _scratch[(dev, stream)] = (t.data_ptr(), size, t, buf)
-    return buf
+    return (_host or _load_host()).qk_norm_rope(q, k, cos, sin, positions, q_weight, k_weight, eps, rot_start,
+                                                interleaved, cache, v, slots, out)
 
 
 def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=True, window=0,
@@ -659,81 +526,8 @@ def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=Tr
     [B+1] and kv_len int32 [B] are on the GPU; max_q_len and max_kv_len bound them for the host
     (default: T, and what the table can hold; tighter is faster). window > 0: each query sees that
     many keys at most, its own the last."""
-    ty = _types if _types.ready else _types.load()
-    bf16, i32 = ty.bf16, ty.i32
-    ck, cv = cache
-    try:
-        T, hq, dk = q.shape
-        pages, page_size, heads, cdk = ck.shape
-        dv = cv.shape[3]
-        B, n = table = page_table.shape
-        dev = q.get_device()
-        q0, q1, q2 = q.stride()
-        ck_strides, cv_strides = ck.stride(), cv.stride()
-        fine = (dev >= 0 and q.dtype is bf16 and q2 == 1 and dk == cdk and hq % heads == 0 and
-                ck.dtype is bf16 and ck_strides[3] == 1 and ck.get_device() == dev and
-                cv.dtype is bf16 and cv_strides[3] == 1 and cv.get_device() == dev and
-                cv.shape == (pages, page_size, heads, dv) and _dense(page_table, i32, dev, table) and
-                _dense(q_start, i32, dev, (B + 1,)) and _dense(kv_len, i32, dev, (B,)))
-    except (AttributeError, ValueError, TypeError, ZeroDivisionError):
-        fine = False
-    if not fine:
-        _rows(q, 3, "q")
-        _explain(q.device, {"q": (q, 3), "cache.k": (ck, 4), "cache.v": (cv, 4)},
-                 {"page_table": (page_table, i32, 2), "q_start": (q_start, i32, 1),
-                  "kv_len": (kv_len, i32, 1)})
-        raise ValueError("the shapes of q [T, Hq, Dk], the cache [pages, page_size, Hk, Dk or Dv] (Hk "
-                         "dividing Hq), page_table [B, n], q_start [B+1] and kv_len [B] do not match")
-    o = _new_output(out, (T, hq, dv), q)
-    lse = ty.empty((T, hq), dtype=ty.f32, device=q.device) if return_lse else None
-    stream = _raw_stream(dev)
-    lib = _lib or load()
-    # The library says whether the workspace at hand is large enough; if not, it is asked how much it takes.
-    ws = _scratch.get((dev, stream)) or (0, 0)
-    while True:
-        args = _pack_attention(
-            q.data_ptr(), q0, q1, ck.data_ptr(), cv.data_ptr(), pages, page_size, heads, dk, dv,
-            *ck_strides[:3], *cv_strides[:3], page_table.data_ptr(), n, q_start.data_ptr(),
-            kv_len.data_ptr(), o.data_ptr(), 0 if lse is None else lse.data_ptr(), B, T, hq, T if max_q_len is None else max_q_len,
-            n * page_size if max_kv_len is None else max_kv_len, window, 1 if causal else 0,
-            dk ** -0.5 if scale is None else scale, ws[0], ws[1])
-        status = lib.fp8bs_paged_attention(args, stream)
-        if status == 0:
-            return (o, lse) if return_lse else o
-        if status == 1:
-            need = ctypes.c_size_t(0)
-            if lib.fp8bs_paged_attention_workspace_size(args, ctypes.byref(need)) == 0 and \
-                    need.value > ws[1]:
-                ws = _scratch_bytes(dev, stream, need.value)
-                continue
-        raise Fp8bsError("fp8bs_paged_attention", status)
-
-
-def _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise, route_scale):
-    """(CUDA device, experts, the packed fp8bs_moe_routing), checked."""
-    ty = _types if _types.ready else _types.load()
-    try:
-        T, D = x.shape
-        experts = router_w.shape[0]
-        dev = x.get_device()
-        fine = (dev >= 0 and x.dtype is ty.bf16 and x.is_contiguous() and
-                _dense(router_w, ty.bf16, dev, (experts, D)) and
-                (bias is None or _dense(bias, ty.f32, dev, (experts,))))
-    except (AttributeError, ValueError, TypeError, IndexError):
-        fine = False
-    if not fine:
-        _require(x, ty.bf16, 2, "x")
-        _explain(x.device, {}, {"x": (x, ty.bf16, 2), "router_w": (router_w, ty.bf16, 2),
-                                "bias": (bias, ty.f32, 1)})
-        raise ValueError("the shapes of x [T, D], router_w [E, D] and bias [E] do not match")
-    if score == "sigmoid":
-        kind, normalise = SCORE_SIGMOID, 1 if normalise is None else int(normalise)
-    elif score == "softmax":
-        kind, normalise = SCORE_SOFTMAX, 0 if normalise is None else int(normalise)
-    else:
-        raise ValueError(f"unknown score {score!r}")
-    return dev, experts, _pack_routing(router_w.data_ptr(), 0 if bias is None else bias.data_ptr(), top_k,
-                                       groups, topk_groups, kind, normalise, route_scale)
+    return (_host or _load_host()).paged_attention(q, cache, page_table, q_start, kv_len, scale, causal, window,
+                                                   max_q_len, max_kv_len, out, return_lse)
 
 
 def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_groups=1, normalise=None,
@@ -742,78 +536,19 @@ def moe_route(x, router_w, top_k, bias=None, score="sigmoid", groups=1, topk_gro
     int32 [T, top_k], best first). bias fp32 [E] shifts the choice only; groups/topk_groups limit it
     to the best groups of experts; normalise (default: for sigmoid scores) makes a token's weights
     sum to route_scale."""
-    dev, experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise,
-                                     route_scale)
-    T, D = x.shape
-    weights = x.new_empty((T, top_k), dtype=_types.f32)
-    ids = x.new_empty((T, top_k), dtype=_types.i32)
-    _check("fp8bs_moe_route", (_lib or load()).fp8bs_moe_route(
-        x.data_ptr(), routing, weights.data_ptr(), ids.data_ptr(), T, D, experts, _raw_stream(dev)))
-    return weights, ids
-
-
-def _expert_shapes(x, w13, s13, w2, s2, weights=None, ids=None):
-    """(CUDA device, T, D, I, E), checked."""
-    ty = _types if _types.ready else _types.load()
-    f32, e4m3 = ty.f32, ty.e4m3
-    try:
-        T, D = x.shape
-        E, _, inter = w2.shape
-        dev = x.get_device()
-        kb, ib = D // BLOCK, inter // BLOCK
-        fine = (dev >= 0 and x.dtype is ty.bf16 and x.is_contiguous() and
-                _dense(w13, e4m3, dev, (E, 2 * inter, D)) and _dense(w2, e4m3, dev, (E, D, inter)) and
-                _dense(s13, f32, dev, (E, 2 * inter // BLOCK, kb)) and _dense(s2, f32, dev, (E, kb, ib)) and
-                (ids is None or (_dense(ids, ty.i32, dev, (T, ids.shape[1])) and
-                                 _dense(weights, f32, dev, ids.shape))))
-    except (AttributeError, ValueError, TypeError, IndexError):
-        fine = False
-    if not fine:
-        _require(x, ty.bf16, 2, "x")
-        _explain(x.device, {}, {"x": (x, ty.bf16, 2), "w13": (w13, e4m3, 3), "s13": (s13, f32, 3),
-                                "w2": (w2, e4m3, 3), "s2": (s2, f32, 3), "weights": (weights, f32, 2),
-                                "ids": (ids, ty.i32, 2)})
-        raise ValueError("the shapes of x [T, D], w13 [E, 2I, D], s13 [E, 2I/128, D/128], w2 [E, D, I], "
-                         "s2 [E, D/128, I/128] (and weights, ids [T, top_k]) do not match")
-    return dev, T, D, inter, E
-
-
-def _expert_workspace(lib, dev, stream, T, D, inter, E, top_k):
-    need = ctypes.c_size_t(0)
-    _check("fp8bs_moe_workspace_size", lib.fp8bs_moe_workspace_size(T, D, inter, E, top_k,
-                                                                    ctypes.byref(need)))
-    return _scratch_bytes(dev, stream, need.value)
+    return (_host or _load_host()).moe_route(x, router_w, top_k, bias, score, groups, topk_groups, normalise,
+                                             route_scale)
 
 
 def moe_experts(x, weights, ids, w13, s13, w2, s2, scale_fmt="fp32", out=None):
     """The experts of a mixture-of-experts layer for x bf16 [T <= 64, D]: w13 e4m3 [E, 2I, D] (gate
     rows, then up rows), w2 e4m3 [E, D, I], scales per 128 x 128 block; ids int32 [T, top_k] (-1: none)
     and weights fp32 [T, top_k] as moe_route gives them -> y bf16 [T, D]."""
-    dev, T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2, weights, ids)
-    k = ids.shape[1]
-    y = _new_output(out, (T, D), x)
-    stream = _raw_stream(dev)
-    lib = _lib or load()
-    ws = _expert_workspace(lib, dev, stream, T, D, inter, E, k)
-    _check("fp8bs_moe_experts", lib.fp8bs_moe_experts(
-        x.data_ptr(), weights.data_ptr(), ids.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
-        s2.data_ptr(), y.data_ptr(), T, D, inter, E, k, _fmt(scale_fmt), ws[0], ws[1], stream))
-    return y
+    return (_host or _load_host()).moe_experts(x, weights, ids, w13, s13, w2, s2, _fmt(scale_fmt), out)
 
 
 def moe_layer(x, router_w, w13, s13, w2, s2, top_k, bias=None, score="sigmoid", groups=1,
               topk_groups=1, normalise=None, route_scale=1.0, scale_fmt="fp32", out=None):
     """A whole mixture-of-experts layer for x bf16 [T <= 64, D]: moe_route, then moe_experts."""
-    _, experts, routing = _routing(x, router_w, bias, top_k, score, groups, topk_groups, normalise,
-                                   route_scale)
-    dev, T, D, inter, E = _expert_shapes(x, w13, s13, w2, s2)
-    if experts != E:
-        raise ValueError("router_w must have one row per expert")
-    y = _new_output(out, (T, D), x)
-    stream = _raw_stream(dev)
-    lib = _lib or load()
-    ws = _expert_workspace(lib, dev, stream, T, D, inter, E, top_k)
-    _check("fp8bs_moe_layer", lib.fp8bs_moe_layer(
-        x.data_ptr(), routing, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), y.data_ptr(),
-        T, D, inter, E, _fmt(scale_fmt), ws[0], ws[1], stream))
-    return y
+    return (_host or _load_host()).moe_layer(x, router_w, top_k, bias, score, groups, topk_groups, normalise,
+                                             route_scale, w13, s13, w2, s2, _fmt(scale_fmt), out)

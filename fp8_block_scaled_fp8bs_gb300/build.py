@@ -1,6 +1,7 @@
-"""Build libfp8bs.so in place: each csrc/*.cu is compiled by nvcc for sm_103a in parallel and
+"""Build libfp8bs.so and _host.so in place: each csrc/*.cu is compiled by nvcc for sm_103a in parallel and
 linked into one shared library with the CUDA runtime linked statically (the library depends on
-no CUDA shared object at load time; it reaches the driver through the runtime).
+no CUDA shared object at load time; it reaches the driver through the runtime). _host.so (csrc/host.cpp) is a
+CPython module over PyTorch's headers: the host side of the calls that take microseconds.
 
     python -m fp8_block_scaled_fp8bs_gb300.build [--verbose-ptxas]
 """
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8bs.so")
+HOST = os.path.join(PKG, "_host.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -43,7 +45,31 @@ def _deps_mtime():
 
 
 def up_to_date() -> bool:
-    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime()
+    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, HOST))
+
+
+def build_host() -> str:
+    """csrc/host.cpp -> _host.so, with the C++ compiler and the headers and libraries of the installed PyTorch."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found")
+    tmp = HOST + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{p}" for p in include_paths()), f"-I{os.path.join(cuda, 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", os.path.join(CSRC, "host.cpp"), "-o", tmp,
+           *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10", "-ldl"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"C++ compiler failed on host.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, HOST)
+    return HOST
 
 
 def _compile(src: str, ptxas_verbose: bool) -> str:
@@ -64,8 +90,10 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        host = ex.submit(build_host)
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
+        host.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
            "-Xlinker", "--no-undefined", "-ldl", "-lpthread", "-lrt"]
