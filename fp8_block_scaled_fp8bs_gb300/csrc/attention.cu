@@ -50,7 +50,7 @@ struct AttnCfg {
     // (two query tiles: a whole third warpgroup beside the softmax's, for the split of registers below)
     static constexpr int THREADS = 32 * (SOFT_WARPS + (NQ == 2 ? 4 : 3));
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
-    static constexpr int BARS = 2 * KST + 2 * VST + 2 * SBUF + 3 * NQ + 2 + 2 * SLOTS;
+    static constexpr int BARS = 2 * KST + 2 * VST + 2 * SBUF + 3 * NQ + 3 + 2 * SLOTS;
     static constexpr int SMEM = 1024 + NQ * Q_TILE + KST * K_TILE + VST * V_TILE + BARS * 8 + 64;
     static_assert(SMEM <= kSmemLimit, "shared memory");
 };
@@ -407,13 +407,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     uint64_t* v_empty = v_full + Cfg::VST;
     uint64_t* s_full = v_empty + Cfg::VST;                // [SBUF]
     uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF]
-    uint64_t* q_full = p_full + Cfg::SBUF;   // [NQ] queries of an item
+    uint64_t* q_full = p_full + Cfg::SBUF;                // [NQ] queries of an item
     uint64_t* o_done = q_full + NQ;                       // [NQ] each product with V
     uint64_t* o_last = o_done + NQ;                       // [NQ] the last one of an item
     uint64_t* v_tail = o_last + NQ;                       // an item's last, partly valid value tile
     uint64_t* i_full = v_tail + 1;                        // [SLOTS]
     uint64_t* i_empty = i_full + Cfg::SLOTS;              // [SLOTS]
     uint64_t* drain = i_empty + Cfg::SLOTS;               // all products, when given up
+    uint64_t* q_first = drain + 1;                        // the first queries, once, for the value warp
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -439,6 +440,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         }
         mbar_init(v_tail, 1);
         mbar_init(drain, 1);
+        mbar_init(q_first, 1);
         for (int i = 0; i < Cfg::SLOTS; ++i) {
             mbar_init(&i_full[i], 1);
             mbar_init(&i_empty[i], Cfg::SOFT_WARPS + 2);
@@ -743,8 +745,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const int nt = key_tiles(it);
                 if (nt == 0) continue;
                 // (the first queries come first: behind a full ring of keys they take several times as long)
-                if (ks.n == 0)
+                if (ks.n == 0) {
                     for (int q = 0; ok && q < NQ; ++q) ok = warp_wait(&q_full[q], 0);
+                    if (ok && lane == 0) mbar_arrive(q_first);
+                }
                 ok = ok && bring_tiles<Cfg, true>(ks, &tmK, a, it, first_tile(it), nt, modes.box_log2, modes.k, sK,
                                                   k_full, k_empty, nullptr, s_window[0], lane);
             }
@@ -761,8 +765,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 if (it.seq < 0) break;
                 const int nt = key_tiles(it);
                 if (nt == 0) continue;
-                if (vs.n == 0)
-                    for (int q = 0; ok && q < NQ; ++q) ok = warp_wait(&q_full[q], 0);
+                if (vs.n == 0) ok = warp_wait(q_first, 0);
                 ok = ok && bring_tiles<Cfg, false>(vs, &tmV, a, it, first_tile(it), nt, modes.box_log2, modes.v,
                                                    sV, v_full, v_empty, v_tail, s_window[1], lane);
             }
@@ -990,8 +993,12 @@ cudaError_t launch_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
 
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
     const bool two = two_tiles(a);
-    const int64_t items = tile_bound(a, two ? 256 : 128) * a.cache.heads;
-    int64_t keys = key_span(a, two ? 256 : 128, a.max_q_len, a.max_kv_len);
+    const int64_t rows = two ? 256 : 128;
+    const int64_t group = a.q_heads / a.cache.heads;
+    // (sequences of one length, as in decoding, are counted exactly)
+    const int64_t items = a.cache.heads * (a.T == a.B * a.max_q_len ? a.B * ((a.max_q_len * group + rows - 1) / rows)
+                                                                    : tile_bound(a, rows));
+    int64_t keys = key_span(a, rows, a.max_q_len, a.max_kv_len);
     if (keys < 1) keys = 1;
     int64_t len = keys;
     if (two) {
@@ -1006,11 +1013,25 @@ AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
                 len = l;
             }
         }
+    } else if (items * keys < int64_t{4096} * num_sms) {
+        // few rows and keys: as above, where a piece costs as much as 128 keys more, and joining p of them as much as
+        // 128 + 32 p. (Cutting by one CTA's share of all keys instead, in 128 keys or more: 43.8 us instead of 30.3
+        // for 14 sequences of 3183 keys, 57 instead of 43 for 5 of 9411, and around 12 instead of 9 where
+        // sequences of 100 to 300 keys need no second kernel.)
+        int64_t best = 0;
+        for (int64_t p = 1; p <= 64 && (p == 1 || keys / p >= 64); ++p) {
+            const int64_t unit = p == 1 ? 64 : 128;
+            const int64_t l = ((keys + p - 1) / p + unit - 1) / unit * unit;
+            const int64_t time = (items * p + num_sms - 1) / num_sms * (l + 128) + (p > 1 ? 128 + 32 * p : 0);
+            if (p == 1 || time < best) {
+                best = time;
+                len = l;
+            }
+        }
     } else if (items < 8 * num_sms) {
-        // few rows: one CTA's share of all keys; many shares' worth in pieces of 1024 at most, so that the
-        // longest sequence of a ragged batch does not finish last on its own
-        const int64_t share = (items * keys + num_sms - 1) / num_sms;
-        len = std::max<int64_t>(share < 4096 ? share : 1024, 128);
+        // many shares' worth of keys: pieces of 1024 at most, so that the longest sequence of a ragged batch does
+        // not finish last on its own
+        len = 1024;
     }
     len = std::min<int64_t>((len + 127) / 128 * 128, int64_t{1} << 30);
     AttentionPlan p;
