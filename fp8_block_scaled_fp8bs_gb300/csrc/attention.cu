@@ -10,11 +10,24 @@
 //                  outermost: an MN-major operand), O fp32 in TMEM
 // The maximum only moves when it has grown by more than 2^8 (kRescale): the tile's probabilities are then
 // computed again and O is scaled in TMEM by its softmax warps; otherwise P is that much larger than 1 at most,
-// which bf16 and fp32 hold without loss, and O is left alone. So no row waits for its maximum. The row sum is taken from P before its rounding to bf16, so lse is exact
-// to binary32; the rounding of P (2^-9 on average per term) is of the size of the output's own.
+// which bf16 and fp32 hold without loss, and O is left alone. So no row waits for its maximum. The row sum is
+// taken from P before its rounding to bf16, so lse is exact to binary32; the rounding of P (2^-9 on average per
+// term) is of the size of the output's own.
 //
 // Two forms (AttnCfg): NQ = 2 query tiles per CTA for chunks, whose softmax warps work on one tile
 // while the tensor core works on the other; NQ = 1 with two S buffers for few rows.
+//
+// Chunks are bound by the tensor core and what feeds it: 4096 new tokens over 8192 keys, 32 query and 8 key heads
+// of 128 channels, 412 GFLOP that count, take 314 us = 1.31 PFLOP/s (0.68 of a library product's rate). The tensor
+// pipe is busy for 61 % of an SM's cycles and waits for the softmax the rest: a row of S is 128 exponentials, and
+// the products with K, whose operands both come from shared memory, run at 80 instead of 64 cycles. The 10 %
+// between the busiest CTA and the average is the unevenness of 1024 causal tiles over 152 SMs. Heads of 192 + 128
+// channels, whose shared memory holds one value tile, run at 0.29 of the rate (2 chunks of 777 over 2500 keys,
+// 16 heads: 59 us).
+// Decoding is bound by HBM: 64 ragged sequences of up to 8192 keys, 64 query and 8 key heads, 1.1 GB of keys and
+// values, take 193 us = 5.7 TB/s (0.86 of a copy's rate); one sequence of 32785 keys takes 32 us for 134 MB, of
+// which launch, first keys and join are 12.
+//
 // Keys and values come through TMA in boxes of as many slots as divide both the page and the tile, all
 // channels of a box at once where the cache's strides allow it.
 // Few rows and long keys: the key axis is cut into pieces (AttentionPlan), each CTA leaves its
@@ -33,7 +46,8 @@ constexpr float kRescale = 8.0f;
 template <int DK_, int DV_, int NQ_>
 struct AttnCfg {
     static constexpr int DK = DK_, DV = DV_, NQ = NQ_;
-    static constexpr int BN = NQ == 2 ? 128 : 64;                // keys per tile
+    // Keys per tile. (192-wide keys: 96, so that two tiles of values fit.)
+    static constexpr int BN = NQ == 1 ? 64 : DK <= 128 ? 128 : 96;
     static constexpr int ROWS = NQ * 128;
     static constexpr int SLOTS = 4;                              // ring of work items
     static constexpr int SBUF = 2;                               // S buffers: per query tile, or 2
@@ -42,7 +56,7 @@ struct AttnCfg {
     // 25 us, decode of 64 sequences of 4096 keys 153 -> 109).
     static constexpr int CTAS = NQ == 1 && DK == 64 ? 2 : 1;
     static constexpr int KST = DK == 64 ? (NQ == 2 ? 4 : 5) : DK == 128 ? (NQ == 2 ? 3 : 6) : (NQ == 2 ? 2 : 4);
-    static constexpr int VST = DK == 64 ? (NQ == 2 ? 4 : 5) : DK == 128 ? (NQ == 2 ? 2 : 5) : (NQ == 2 ? 1 : 4);
+    static constexpr int VST = DK == 64 ? (NQ == 2 ? 4 : 5) : DK == 128 ? (NQ == 2 ? 2 : 5) : (NQ == 2 ? 2 : 4);
     static constexpr int SOFT_WARPS = 4 * NQ;
     static constexpr int KEY_WARP = SOFT_WARPS;                  // brings the keys (and hands out the items)
     static constexpr int VALUE_WARP = SOFT_WARPS + 1;
@@ -1000,13 +1014,14 @@ AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
                                                                     : tile_bound(a, rows));
     int64_t keys = key_span(a, rows, a.max_q_len, a.max_kv_len);
     if (keys < 1) keys = 1;
+    const int64_t unit = two && a.cache.dk > 128 ? 192 : 128;       // whole key tiles
     int64_t len = keys;
     if (two) {
         // chunks that do not fill the GPU: the number of pieces with the lowest time, in keys, of the busiest
         // CTA, where a piece costs as much as 512 keys more (queries, output, its part of the join)
         int64_t best = keys;
         for (int64_t p = 2; items < num_sms && p <= 16 && keys / p >= 256; ++p) {
-            const int64_t l = ((keys + p - 1) / p + 127) / 128 * 128;
+            const int64_t l = ((keys + p - 1) / p + unit - 1) / unit * unit;
             const int64_t time = (items * p + num_sms - 1) / num_sms * (l + 512);
             if (time < best) {
                 best = time;
@@ -1020,8 +1035,8 @@ AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
         // sequences of 100 to 300 keys need no second kernel.)
         int64_t best = 0;
         for (int64_t p = 1; p <= 64 && (p == 1 || keys / p >= 64); ++p) {
-            const int64_t unit = p == 1 ? 64 : 128;
-            const int64_t l = ((keys + p - 1) / p + unit - 1) / unit * unit;
+            const int64_t step = p == 1 ? 64 : 128;
+            const int64_t l = ((keys + p - 1) / p + step - 1) / step * step;
             const int64_t time = (items * p + num_sms - 1) / num_sms * (l + 128) + (p > 1 ? 128 + 32 * p : 0);
             if (p == 1 || time < best) {
                 best = time;
@@ -1033,7 +1048,7 @@ AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
         // not finish last on its own
         len = 1024;
     }
-    len = std::min<int64_t>((len + 127) / 128 * 128, int64_t{1} << 30);
+    len = std::min<int64_t>((len + unit - 1) / unit * unit, int64_t{1} << 30);
     AttentionPlan p;
     p.piece_len = static_cast<int>(len);
     p.pieces = static_cast<int>((keys + len - 1) / len);
@@ -1080,8 +1095,8 @@ AttentionModes attention_modes(const fp8bs_kv_cache& c) {
     AttentionModes m;
     m.k = fetch_mode(c, c.dk, c.k_head_stride, c.k_page_stride);
     m.v = fetch_mode(c, c.dv, c.v_head_stride, c.v_page_stride);
-    // slots per box: the largest power of two that divides the page and the smaller key tile
-    const int most = m.k == 2 || m.v == 2 ? 3 : 6;
+    // slots per box: the largest power of two that divides the page and the key tiles (64 and 128, or 64 and 96)
+    const int most = m.k == 2 || m.v == 2 ? 3 : c.dk > 128 ? 5 : 6;
     m.box_log2 = 0;
     while (m.box_log2 < most && c.page_size % (int64_t{2} << m.box_log2) == 0) ++m.box_log2;
     return m;

@@ -14,6 +14,12 @@
 // token that did not choose the expert, and otherwise the factor (block scale of h) * (weight of the
 // expert), so that the down kernel's accumulators run over all experts without a break: one sum per output,
 // in expert and channel order, the same bits every time.
+//
+// Measured for 32 experts of 2048 channels, D = 7168, 8 chosen per token (1.4 GB of weights when all are met):
+// 64 tokens 265 us for the layer (up 174, down 93, router 13, overlapping), 5.3 TB/s (0.80 of a copy's rate);
+// 7 tokens 186 us for 1.2 GB (0.98); one token 68 us for 353 MB (0.77), where each kernel ends on the SMs with one
+// item more than the others (128 and 112 CTAs of 152). At 64 tokens the promotion of 64 columns per K block and the
+// transposition between kernels are what is left above the weights' time.
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     const int total = static_cast<int>(static_cast<int64_t>(rank + 1) * units / C) - u0;
 
     if (warp == 0) {
-        // One lane for each of a stage's four copies (see the up kernel): the two weight tiles, h, the factors. (The
+        // One lane for each of a stage's four copies: the two weight tiles, h, the factors. (The
         // second tile of the last pair may lie past D: it reads the next expert's rows, or zeros past the last
         // one's, and is not stored.)
         const uint64_t policy = lane < 2 ? l2_policy_evict_first() : l2_policy_evict_last();

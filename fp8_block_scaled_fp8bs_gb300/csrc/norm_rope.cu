@@ -6,6 +6,10 @@
 // channels (16-byte loads and stores). The two chunks are the two halves of the same rotation
 // pairs, so the rotation needs no exchange between lanes, and the norm one reduction over LPR
 // lanes. The token's cosines and sines are read once into registers and serve all its heads.
+//
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 channels, norm and rotation, keys and values into the cache,
+// 34 us for 205 MB = 6.0 TB/s (0.90 of a copy's rate); 1000 tokens of 16 heads of 192 channels 6.7 us; five tokens
+// 2.6 us, a launch and two dependent loads.
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
