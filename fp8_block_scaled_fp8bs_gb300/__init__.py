@@ -2,7 +2,8 @@
 
 A thin ctypes binding over the C ABI in ``include/fp8bs.h`` (``libfp8bs.so``, built in place
 by ``fp8_block_scaled_fp8bs_gb300.build``). Every step of the path runs in the library's CUDA
-kernels; this module only marshals arguments. There is no CPU fallback: if the library is
+kernels; this module only marshals arguments (those of the decoder-layer operators in compiled
+code, ``csrc/host.cpp``: their smallest calls take a few microseconds). There is no CPU fallback: if the library is
 missing or cannot be loaded, importing the binding's functions raises.
 
 Raw entry points (same names and arguments as the C functions; pointers are ints):

@@ -22,8 +22,8 @@
 // pipe is busy for 61 % of an SM's cycles and waits for the softmax the rest: a row of S is 128 exponentials, and
 // the products with K, whose operands both come from shared memory, run at 80 instead of 64 cycles. The 10 %
 // between the busiest CTA and the average is the unevenness of 1024 causal tiles over 152 SMs. Heads of 192 + 128
-// channels, whose shared memory holds one value tile, run at 0.29 of the rate (2 chunks of 777 over 2500 keys,
-// 16 heads: 59 us).
+// channels take tiles of 96 keys (128 would leave room for one tile of values: 59 us instead of 56 for 2 chunks of
+// 777 over 2500 keys, 16 heads).
 // Decoding is bound by HBM: 64 ragged sequences of up to 8192 keys, 64 query and 8 key heads, 1.1 GB of keys and
 // values, take 193 us = 5.7 TB/s (0.86 of a copy's rate); one sequence of 32785 keys takes 32 us for 134 MB, of
 // which launch, first keys and join are 12.
@@ -961,7 +961,10 @@ int64_t tile_bound(const fp8bs_paged_attention_args& a, int rows) {
     return a.T * group / rows + (a.B < a.T ? a.B : a.T);
 }
 
-// Whether the two-tile form is used: its 256 rows have to be filled by the average sequence.
+// Whether the two-tile form is used: where the average sequence has more rows than one tile holds. (32 sequences of
+// 2048 keys, 8 heads of 128 channels, one tile and two: 128 rows 62 and 76 us, 160 rows 122 and 80, 512 rows 268 and
+// 148; heads of 64 35 and 54, 82 and 61; of 192 75 and 94, 148 and 96. 4 sequences of 8192 keys, 4 heads: 128 rows 25
+// and 33, 160 to 256 rows even.)
 bool two_tiles(const fp8bs_paged_attention_args& a) {
     const int64_t group = a.q_heads / a.cache.heads;
     return a.T * group > 128 * a.B;

@@ -17,9 +17,9 @@
 //
 // Measured for 32 experts of 2048 channels, D = 7168, 8 chosen per token (1.4 GB of weights when all are met):
 // 64 tokens 265 us for the layer (up 174, down 93, router 13, overlapping), 5.3 TB/s (0.80 of a copy's rate);
-// 7 tokens 186 us for 1.2 GB (0.98); one token 68 us for 353 MB (0.77), where each kernel ends on the SMs with one
-// item more than the others (128 and 112 CTAs of 152). At 64 tokens the promotion of 64 columns per K block and the
-// transposition between kernels are what is left above the weights' time.
+// 7 tokens 186 us for 1.2 GB (0.98); one token 67 us for 353 MB (0.79): the router comes first,
+// and the grids are 128 and 112 CTAs for 152 SMs. At 64 tokens the down kernel's 112 CTAs have 64 columns to scale
+// per K block, 93 us where its weights take 70.
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
@@ -43,12 +43,19 @@ struct Routing {
     int n;
 };
 
-// All threads of the CTA; ends with a block barrier.
-__device__ __forceinline__ void build_routing(Routing& r, const MoeArgs& a, bool report) {
+// All threads of the CTA: before the ids are there, and when they are (`first`: this thread's own; a block barrier
+// between the two, and one at the end).
+__device__ __forceinline__ void clear_routing(Routing& r, const MoeArgs& a) {
     for (int e = threadIdx.x; e < a.E; e += MOE_THREADS) r.mask[e] = 0;
-    __syncthreads();
+}
+
+__device__ __forceinline__ int first_id(const MoeArgs& a) {
+    return threadIdx.x < a.T * a.top_k ? a.ids[threadIdx.x] : -1;
+}
+
+__device__ __forceinline__ void build_routing(Routing& r, const MoeArgs& a, int first, bool report) {
     for (int s = threadIdx.x; s < a.T * a.top_k; s += MOE_THREADS) {
-        const int e = a.ids[s];
+        const int e = s == threadIdx.x ? first : a.ids[s];
         if (e >= 0 && e < a.E)
             atomicOr(&r.mask[e], 1ull << (s / a.top_k));
         else if (e != -1 && report)
@@ -273,14 +280,17 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         tma_prefetch_desc(&tmX);
     }
     if (warp == 1) tmem_alloc(&s_tmem, Cfg::TMEM_COLS);
+    clear_routing(rt, a);
     tc_fence_before();
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
+    const int first = first_id(a);                           // (on its way while the scales are)
     for (int i = threadIdx.x; i < nkb * MT; i += MOE_THREADS) {
         const int t = i % MT;
         sXs[i] = t < a.T ? xs[(i / MT) * kMoeMaxTokens + t] : 0.0f;
     }
-    build_routing(rt, a, blockIdx.x == 0);
+    build_routing(rt, a, first, blockIdx.x == 0);
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int iblocks = a.I / BK;
@@ -368,14 +378,24 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             const unsigned long long mask = rt.mask[e];
             // the item's columns: its rows of x, or all tokens
             const int cols = GATHER ? __popcll(mask) : a.T;
+            const int tid = threadIdx.x - MOE_PROMOTE_WARP0 * 32;
+            float route_w = 0.0f;              // thread tid: the expert's weight for column tid's token
+            if (tid < cols) {
+                const int t = GATHER ? nth_bit(mask, tid) : tid;
+#pragma unroll 8
+                for (int j = 0; j < a.top_k; ++j) {
+                    const int id = a.ids[t * a.top_k + j];
+                    const float w = a.weights[t * a.top_k + j];
+                    route_w += id == e ? w : 0.0f;
+                }
+            }
             const float* scales = sXs;
             if constexpr (GATHER) {
                 // the scales of the item's rows, side by side (barrier 1: no warp reads the last item's any more)
-                const int x = threadIdx.x - MOE_PROMOTE_WARP0 * 32;
-                const int i = x % MT;
+                const int i = tid % MT;
                 if (i < cols) {
                     const int t = nth_bit(mask, i);
-                    for (int kb = x / MT; kb < nkb; kb += 256 / MT) sGs[kb * MT + i] = sXs[kb * MT + t];
+                    for (int kb = tid / MT; kb < nkb; kb += 256 / MT) sGs[kb * MT + i] = sXs[kb * MT + t];
                 }
                 asm volatile("bar.sync 4, 256;" ::: "memory");
                 scales = sGs;
@@ -399,17 +419,6 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             // h = silu(gate) * up. The gate's warps take the first half of the columns, the up product's warps the
             // others, four at a time (one after another, they are all latency: 41000 cycles for 16 tokens, half as
             // much as the item's weights take); each side hands the other what it needs through shared memory.
-            const int tid = threadIdx.x - MOE_PROMOTE_WARP0 * 32;
-            float route_w = 0.0f;              // thread tid: the expert's weight for column tid's token
-            if (tid < cols) {
-                const int t = GATHER ? nth_bit(mask, tid) : tid;
-#pragma unroll 8
-                for (int j = 0; j < a.top_k; ++j) {
-                    const int id = a.ids[t * a.top_k + j];
-                    const float w = a.weights[t * a.top_k + j];
-                    route_w += id == e ? w : 0.0f;
-                }
-            }
             const int mid = (cols + 7) / 8 * 4;
             auto here = [&](int c) { return (4 * c < mid) == (half == 0); };
 #pragma unroll
@@ -516,10 +525,12 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         tma_prefetch_desc(&tmH);
     }
     if (warp == 1) tmem_alloc(&s_tmem, Cfg::TMEM_COLS);
+    clear_routing(rt, a);
     tc_fence_before();
+    __syncthreads();
     // The ids and weights were complete before the up kernel let this one start (it does so after its own
     // wait), so the experts are known and the weights' ring fills while the up kernel is still running.
-    build_routing(rt, a, false);
+    build_routing(rt, a, first_id(a), false);
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int nkb = a.I / BK;
