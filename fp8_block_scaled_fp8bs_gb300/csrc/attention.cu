@@ -297,11 +297,12 @@ struct Stream {
 // instead of 204 us, a chunk of 4096 over 8192 keys 364 instead of 335). Values of the
 // first and last tile that do not count are cleared before the tile does: whatever stood there must not meet a
 // probability of zero.
-template <class Cfg, bool KEYS>
+// first_wait(): waited for before the first tile, under the first look at the pages.
+template <class Cfg, bool KEYS, typename First>
 __device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, const fp8bs_paged_attention_args& a,
                                             const Item& it, int k0, int nt, int box_log2, int mode, uint8_t* ring,
                                             uint64_t* full, uint64_t* empty, uint64_t* tail, int2* window,
-                                            int lane) {
+                                            int lane, First first_wait) {
     constexpr int STAGES = KEYS ? Cfg::KST : Cfg::VST;
     constexpr int TILE = KEYS ? Cfg::K_TILE : Cfg::V_TILE;
     constexpr int CH = (KEYS ? Cfg::DK : Cfg::DV) / 64;
@@ -324,6 +325,7 @@ __device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, c
     };
     int window_at = 0;                       // the 32 boxes that `next` is of
     int2 next = lookup(0);
+    if (s.n == 0 && !first_wait()) return false;
     for (int j = 0; j < nt; ++j) {
         const int key0 = k0 + j * BN;
         // boxes [none, live) hold keys that count: those before them are past a window (their pages may have been
@@ -759,12 +761,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const int nt = key_tiles(it);
                 if (nt == 0) continue;
                 // (the first queries come first: behind a full ring of keys they take several times as long)
-                if (ks.n == 0) {
-                    for (int q = 0; ok && q < NQ; ++q) ok = warp_wait(&q_full[q], 0);
-                    if (ok && lane == 0) mbar_arrive(q_first);
-                }
-                ok = ok && bring_tiles<Cfg, true>(ks, &tmK, a, it, first_tile(it), nt, modes.box_log2, modes.k, sK,
-                                                  k_full, k_empty, nullptr, s_window[0], lane);
+                ok = bring_tiles<Cfg, true>(ks, &tmK, a, it, first_tile(it), nt, modes.box_log2, modes.k, sK,
+                                            k_full, k_empty, nullptr, s_window[0], lane, [&] {
+                                                for (int q = 0; q < NQ; ++q)
+                                                    if (!warp_wait(&q_full[q], 0)) return false;
+                                                if (lane == 0) mbar_arrive(q_first);
+                                                return true;
+                                            });
             }
             if (!ok && lane == 0) drain_tiles<Cfg::KST>(ks, k_full);
         } else if (warp == Cfg::VALUE_WARP) {
@@ -779,9 +782,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 if (it.seq < 0) break;
                 const int nt = key_tiles(it);
                 if (nt == 0) continue;
-                if (vs.n == 0) ok = warp_wait(q_first, 0);
-                ok = ok && bring_tiles<Cfg, false>(vs, &tmV, a, it, first_tile(it), nt, modes.box_log2, modes.v,
-                                                   sV, v_full, v_empty, v_tail, s_window[1], lane);
+                ok = bring_tiles<Cfg, false>(vs, &tmV, a, it, first_tile(it), nt, modes.box_log2, modes.v, sV,
+                                             v_full, v_empty, v_tail, s_window[1], lane,
+                                             [&] { return warp_wait(q_first, 0); });
             }
             if (!ok && lane == 0) {
                 drain_tiles<Cfg::VST>(vs, v_full);
