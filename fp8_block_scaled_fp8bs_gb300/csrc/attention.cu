@@ -18,10 +18,9 @@
 // while the tensor core works on the other; NQ = 1 with two S buffers for few rows.
 //
 // Chunks are bound by the tensor core and what feeds it: 4096 new tokens over 8192 keys, 32 query and 8 key heads
-// of 128 channels, 412 GFLOP that count, take 314 us = 1.31 PFLOP/s (0.68 of a library product's rate). The tensor
+// of 128 channels, 412 GFLOP that count, take 282 us = 1.46 PFLOP/s (0.75 of a library product's rate). The tensor
 // pipe is busy for 61 % of an SM's cycles and waits for the softmax the rest: a row of S is 128 exponentials, and
-// the products with K, whose operands both come from shared memory, run at 80 instead of 64 cycles. The 10 %
-// between the busiest CTA and the average is the unevenness of 1024 causal tiles over 152 SMs. Heads of 192 + 128
+// the products with K, whose operands both come from shared memory, run at 80 instead of 64 cycles. Heads of 192 + 128
 // channels take tiles of 96 keys (128 would leave room for one tile of values: 59 us instead of 56 for 2 chunks of
 // 777 over 2500 keys, 16 heads).
 // Decoding is bound by HBM: 64 ragged sequences of up to 8192 keys, 64 query and 8 key heads, 1.1 GB of keys and
@@ -126,8 +125,39 @@ __device__ __forceinline__ Cut cut_of(const fp8bs_paged_attention_args& a, int r
     return c;
 }
 
-__device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_attention_args& a, int item,
-                                          int rows, int bn, int piece_len, int lane) {
+__device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_attention_args& a, int rows,
+                                               int piece_len, int lane) {
+    const int group = static_cast<int>(a.q_heads / a.cache.heads);
+    f.sum = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+        const int64_t b = f.base + 8 * lane + i;
+        f.start[i] = a.q_start[b < a.B ? b : a.B];
+        if (i < 8) f.kv[i] = b < a.B ? a.kv_len[b] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int n = f.start[i + 1] - f.start[i];
+        f.units[i] = 0;
+        if (n > a.max_q_len || f.kv[i] > a.max_kv_len) {
+            f.units[i] = 1;      // out of bounds: handed out once, to be reported
+        } else if (n > 0) {
+            const Cut c = cut_of(a, rows, piece_len, n, f.kv[i], group);
+            f.units[i] = c.tiles * c.pieces;
+        }
+        f.sum += f.units[i];
+    }
+    f.incl = f.sum;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, f.incl, m);
+        if (lane >= m) f.incl += o;
+    }
+    f.loaded = true;
+}
+
+__device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_attention_args& a, int item, int rows,
+                                          int bn, int piece_len, int lane) {
     Item it;
     it.seq = -1;
     const int heads = static_cast<int>(a.cache.heads);
@@ -135,34 +165,7 @@ __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_atten
     const int unit = item / heads;
     it.head = item - unit * heads;
     while (f.base < a.B) {
-        if (!f.loaded) {
-            f.sum = 0;
-#pragma unroll
-            for (int i = 0; i < 9; ++i) {
-                const int64_t b = f.base + 8 * lane + i;
-                f.start[i] = a.q_start[b < a.B ? b : a.B];
-                if (i < 8) f.kv[i] = b < a.B ? a.kv_len[b] : 0;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int n = f.start[i + 1] - f.start[i];
-                f.units[i] = 0;
-                if (n > a.max_q_len || f.kv[i] > a.max_kv_len) {
-                    f.units[i] = 1;      // out of bounds: handed out once, to be reported
-                } else if (n > 0) {
-                    const Cut c = cut_of(a, rows, piece_len, n, f.kv[i], group);
-                    f.units[i] = c.tiles * c.pieces;
-                }
-                f.sum += f.units[i];
-            }
-            f.incl = f.sum;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, f.incl, m);
-                if (lane >= m) f.incl += o;
-            }
-            f.loaded = true;
-        }
+        if (!f.loaded) load_sequences(f, a, rows, piece_len, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, f.before + f.incl > unit);
         if (hit) {
             const int src = __ffs(hit) - 1;
@@ -737,10 +740,30 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             bool ok = true;
             Stream ks = {0, 0};
             int x = 0;
-            for (int64_t round = 0; ok; ++round) {
-                // every other round backwards: long items and short ones even out
-                const int64_t at = round * gridDim.x +
-                                   (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            // The items are dealt out in rounds, every other one backwards: long items and short ones even out. Where
+            // the last round is not whole, some CTAs have an item more than the others. Of one sequence, whose
+            // items come longest first, those are dealt the short ones (a chunk of 4096 over 8192 keys: 169 key tiles
+            // for the busiest CTA instead of 182, 282 us instead of 315); in a batch they may be any. (Two query
+            // tiles only: few rows mean pieces of one length, and a batch of 9 us takes 0.3 more with it.)
+            int ctas = gridDim.x, mine = blockIdx.x, start = 0, rounds = INT32_MAX;
+            if (NQ == 2 && __builtin_expect(a.B == 1, 0)) {
+                load_sequences(finder, a, Cfg::ROWS, piece_len, lane);
+                const int items = __shfl_sync(0xffffffffu, finder.incl, 31) * static_cast<int>(a.cache.heads);
+                const int whole = items / ctas, more = items % ctas;
+                if (mine < ctas - more) {
+                    ctas -= more;
+                    rounds = whole;
+                } else {
+                    mine -= ctas - more;
+                    start = (ctas - more) * whole;
+                    ctas = more;
+                    rounds = whole + 1;
+                }
+            }
+            for (int round = 0; ok; ++round) {
+                const int64_t at = round < rounds ? start + static_cast<int64_t>(round) * ctas +
+                                                        (round & 1 ? ctas - 1 - mine : mine)
+                                                  : int64_t{INT32_MAX};
                 const Item it = find_item(finder, a, static_cast<int>(min(at, int64_t{INT32_MAX})), Cfg::ROWS,
                                           BN, piece_len, lane);
                 if (it.seq == -2) {
