@@ -16,7 +16,7 @@
 // in expert and channel order, the same bits every time.
 //
 // Measured for 32 experts of 2048 channels, D = 7168, 8 chosen per token (1.4 GB of weights when all are met):
-// 64 tokens 265 us for the layer (up 174, down 93, router 13, overlapping), 5.3 TB/s (0.80 of a copy's rate);
+// 64 tokens 255 us for the layer (up, down and router overlap), 5.5 TB/s (0.83 of a copy's rate);
 // 7 tokens 186 us for 1.2 GB (0.98); one token 67 us for 353 MB (0.79): the router comes first,
 // and the grids are 128 and 112 CTAs for 152 SMs. At 64 tokens the down kernel's 112 CTAs have 64 columns to scale
 // per K block, 93 us where its weights take 70.
@@ -27,12 +27,15 @@ namespace fp8bs {
 
 namespace {
 
-// Warps of both kernels: 0 brings the stages, 1 and 10 issue the MMAs of the first and second weight tile of a
-// stage, 2..5 promote the first, 6..9 the second (TMEM lanes: warp % 4).
+// Warps of both kernels: 0 brings the stages' weights and 11 their activations, 1 and 10 issue the MMAs of the first and
+// second weight tile of a stage, 2..5 promote the first, 6..9 the second (TMEM lanes: warp % 4). (One warp for weights
+// and activations: issuing a stage's copies one after another took longer than its weights do, 64 tokens 265 us
+// instead of 255; two tokens 14.7 instead of 15.0.)
 constexpr int MOE_PROMOTE_WARP0 = 2;
 constexpr int MOE_PROMOTE_WARPS = 8;
 constexpr int MOE_ISSUER2 = MOE_PROMOTE_WARP0 + MOE_PROMOTE_WARPS;
-constexpr int MOE_THREADS = (MOE_ISSUER2 + 1) * 32;
+constexpr int MOE_LOADER2 = MOE_ISSUER2 + 1;
+constexpr int MOE_THREADS = (MOE_LOADER2 + 1) * 32;
 constexpr int MOE_NBUF = 4;                           // TMEM buffers (K blocks in flight)
 constexpr int kMaxExperts = 512;
 
@@ -299,10 +302,11 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     const int mine = blockIdx.x < items ? (items - 1 - blockIdx.x) / gridDim.x + 1 : 0;
     const int total = mine * nkb;
 
-    if (warp == 0) {
-        // Lanes 0 and 1 bring the weight tiles, lane 2 the activations; GATHER: lane 2 + i rows 4i .. 4i + 3 of those
-        // that chose the expert (a row past them: any).
-        const uint64_t policy = lane < 2 ? l2_policy_evict_first() : l2_policy_evict_last();
+    if (warp == 0 || warp == MOE_LOADER2) {
+        // Lanes 0 and 1 of the first loader bring the weight tiles, lane 0 of the second the activations; GATHER: lane
+        // i rows 4i .. 4i + 3 of those that chose the expert (a row past them: any).
+        const bool weights = warp == 0;
+        const uint64_t policy = weights ? l2_policy_evict_first() : l2_policy_evict_last();
         int n = 0;
         bool ok = true;
         for (int m = 0; ok && m < mine; ++m) {
@@ -315,8 +319,8 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             if constexpr (GATHER) {
                 unsigned long long mask = rt.mask[e];
                 gathers = (__popcll(mask) + 3) / 4;
-                if (lane >= 2 && lane < 2 + gathers) {
-                    for (int i = 0; i < 4 * (lane - 2); ++i) mask &= mask - 1;
+                if (lane < gathers) {
+                    for (int i = 0; i < 4 * lane; ++i) mask &= mask - 1;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         tok[i] = mask ? __ffsll(mask) - 1 : tok[0];
@@ -331,15 +335,18 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
-                __syncwarp();
-                if (lane < 2)
-                    tma_load_2d_hint(sW + (2 * st + lane) * A_TILE, &tmW, &bar.full[st], kb * BK, row, policy);
-                else if (GATHER && lane < 2 + gathers)
-                    tma_gather4(sX + st * Cfg::X_TILE + (lane - 2) * 4 * BK, &tmX, &bar.full[st], kb * BK, tok[0],
-                                tok[1], tok[2], tok[3]);
-                else if (!GATHER && lane == 2)
+                if (weights) {
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], bytes);
+                    __syncwarp();
+                    if (lane < 2)
+                        tma_load_2d_hint(sW + (2 * st + lane) * A_TILE, &tmW, &bar.full[st], kb * BK, row, policy);
+                } else if (GATHER) {
+                    if (lane < gathers)
+                        tma_gather4(sX + st * Cfg::X_TILE + lane * 4 * BK, &tmX, &bar.full[st], kb * BK, tok[0],
+                                    tok[1], tok[2], tok[3]);
+                } else if (lane == 0) {
                     tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmX, &bar.full[st], kb * BK, 0, policy);
+                }
             }
         }
         if (!ok && lane == 0) drain_stages(bar, stages, n);
@@ -538,40 +545,40 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     const int u0 = static_cast<int>(static_cast<int64_t>(rank) * units / C);
     const int total = static_cast<int>(static_cast<int64_t>(rank + 1) * units / C) - u0;
 
-    if (warp == 0) {
-        // One lane for each of a stage's four copies: the two weight tiles, h, the factors. (The
-        // second tile of the last pair may lie past D: it reads the next expert's rows, or zeros past the last
-        // one's, and is not stored.)
-        const uint64_t policy = lane < 2 ? l2_policy_evict_first() : l2_policy_evict_last();
-        auto load = [&](int n, bool weights, bool h) {
+    if (warp == 0 || warp == MOE_LOADER2) {
+        // One lane for each of a stage's four copies: the two weight tiles by the first loader, h and the factors by the
+        // second. (The second tile of the last pair may lie past D: it reads the next expert's rows, or zeros past the
+        // last one's, and is not stored.)
+        const bool weights = warp == 0;
+        const uint64_t policy = weights ? l2_policy_evict_first() : l2_policy_evict_last();
+        auto load = [&](int n) {
             const int st = n % stages;
             const int act = (u0 + n) / nkb;
             const int kb = u0 + n - act * nkb;
             if (weights) {
                 if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], Cfg::STAGE + Cfg::F_BYTES);
                 __syncwarp();
-            }
-            const bool w = lane < 2;
-            if ((w && weights) || (lane == 2 && h))
-                tma_load_2d_hint(w ? sW + (2 * st + lane) * A_TILE : sX + st * Cfg::X_TILE, w ? &tmW : &tmH,
-                                 &bar.full[st], kb * BK,
-                                 w ? rt.active[act] * a.D + (2 * pair + lane) * BM : act * a.T, policy);
-            if (lane == 3 && h)
+                if (lane < 2)
+                    tma_load_2d_hint(sW + (2 * st + lane) * A_TILE, &tmW, &bar.full[st], kb * BK,
+                                     rt.active[act] * a.D + (2 * pair + lane) * BM, policy);
+            } else if (lane == 0) {
+                tma_load_2d_hint(sX + st * Cfg::X_TILE, &tmH, &bar.full[st], kb * BK, act * a.T, policy);
+            } else if (lane == 1) {
                 bulk_load(sF + st * MT, hs + (static_cast<int64_t>(act) * nkb + kb) * kMoeMaxTokens,
                           Cfg::F_BYTES, &bar.full[st]);
+            }
         };
-        const int ahead = min(stages, total);
-        for (int n = 0; n < ahead; ++n) load(n, true, false);
-        grid_dependency_wait();
+        if (!weights) grid_dependency_wait();
+        int n = 0;
+        for (; n < min(stages, total); ++n) load(n);
+        if (weights) grid_dependency_wait();
         grid_launch_dependents();
-        for (int n = 0; n < ahead; ++n) load(n, false, true);
-        int n = ahead;
         for (; n < total; ++n) {
             if (!warp_wait(&bar.empty[n % stages], ((n / stages) & 1) ^ 1)) {
                 if (lane == 0) drain_stages(bar, stages, n);
                 break;
             }
-            load(n, true, true);
+            load(n);
         }
     } else if (warp == 1 || warp == MOE_ISSUER2) {
         grid_dependency_wait();
