@@ -245,10 +245,14 @@ __device__ __forceinline__ void promote_block(float* acc, uint32_t t0, const flo
     promote<MT>(acc, v, xs, s);
 }
 
-template <int MT>
+// SPLIT: with few items (experts and blocks of 128 channels) for the SMs, clusters of 2^log2s CTAs share an item's channels
+// of x: each computes its part of the K blocks, rank 0 adds the sums in rank order and goes on with them. (One token of
+// 6400 channels, 4 experts of 256: 33 -> 21 us for the layer. A form of its own: with the split decided at run time the
+// others took 0.5 to 0.9 us more.)
+template <int MT, bool SPLIT>
 __global__ void __launch_bounds__(MOE_THREADS, 1)
     moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                  const MoeArgs a, const float* xs, uint8_t* h8, float* hs, const int stages) {
+                  const MoeArgs a, const float* xs, uint8_t* h8, float* hs, const int stages, const int log2s) {
     using Cfg = MoeCfg<MT>;
     constexpr bool GATHER = Cfg::GATHER;
     extern __shared__ uint8_t smem_raw[];
@@ -298,9 +302,14 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     const uint32_t tmem = s_tmem;
     const int iblocks = a.I / BK;
     const int items = rt.n * iblocks;
-    // this CTA's items: blockIdx.x, + gridDim.x, ...; K blocks counted on through them
-    const int mine = blockIdx.x < items ? (items - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    const int total = mine * nkb;
+    // this cluster's items: first, first + clusters, ...; K blocks [k0, k0 + nk) of each, counted on through them
+    const int first_item = SPLIT ? blockIdx.x >> log2s : blockIdx.x;
+    const int clusters = SPLIT ? gridDim.x >> log2s : gridDim.x;
+    const int rank = SPLIT ? blockIdx.x & ((1 << log2s) - 1) : 0;
+    const int k0 = SPLIT ? rank * nkb >> log2s : 0;
+    const int nk = SPLIT ? ((rank + 1) * nkb >> log2s) - k0 : nkb;
+    const int mine = first_item < items ? (items - 1 - first_item) / clusters + 1 : 0;
+    const int total = mine * nk;
 
     if (warp == 0 || warp == MOE_LOADER2) {
         // Lanes 0 and 1 of the first loader bring the weight tiles, lane 0 of the second the activations; GATHER: lane
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         int n = 0;
         bool ok = true;
         for (int m = 0; ok && m < mine; ++m) {
-            const int item = blockIdx.x + m * gridDim.x;
+            const int item = first_item + m * clusters;
             const int act = item / iblocks;
             const int e = rt.active[act];
             const int row = e * 2 * a.I + (item - act * iblocks) * BM + (lane == 1 ? a.I : 0);
@@ -329,7 +338,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                 }
             }
             const uint32_t bytes = 2 * A_TILE + (GATHER ? gathers * 4 * BK : Cfg::X_TILE);
-            for (int kb = 0; kb < nkb; ++kb, ++n) {
+            for (int kb = k0; kb < k0 + nk; ++kb, ++n) {
                 const int st = n % stages;
                 if (!warp_wait(&bar.empty[st], ((n / stages) & 1) ^ 1)) {
                     ok = false;
@@ -352,9 +361,9 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         if (!ok && lane == 0) drain_stages(bar, stages, n);
     } else if (warp == 1 || warp == MOE_ISSUER2) {
         if (lane == 0)
-            issue_half<MT>(warp == 1 ? 0 : 1, total, nkb, stages, sW, sX, tmem, bar, [&](int m) {
+            issue_half<MT>(warp == 1 ? 0 : 1, total, nk, stages, sW, sX, tmem, bar, [&](int m) {
                 if (!GATHER) return MT;
-                const int act = (static_cast<int>(blockIdx.x) + m * static_cast<int>(gridDim.x)) / iblocks;
+                const int act = (first_item + m * clusters) / iblocks;
                 return (__popcll(rt.mask[rt.active[act]]) + 15) / 16 * 16;
             });
     } else {
@@ -364,12 +373,12 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * MT);
         auto scale_of = [&](int n) {
             if (n >= total) return 0.0f;
-            const int m = n / nkb;
-            const int item = blockIdx.x + m * gridDim.x;
+            const int m = n / nk;
+            const int item = first_item + m * clusters;
             const int act = item / iblocks;
             const int64_t block = static_cast<int64_t>(rt.active[act]) * 2 * iblocks + half * iblocks +
                                   (item - act * iblocks);
-            return __ldg(a.s13 + block * nkb + (n - m * nkb));
+            return __ldg(a.s13 + block * nkb + k0 + (n - m * nk));
         };
         ScaleStream<decltype(scale_of)> ws(lane, scale_of);
         bool ok = true;
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             float g[MT];
 #pragma unroll
             for (int i = 0; i < MT; ++i) g[i] = 0.0f;
-            const int item = blockIdx.x + m * gridDim.x;
+            const int item = first_item + m * clusters;
             const int act = item / iblocks;
             const int ib = item - act * iblocks;
             const int e = rt.active[act];
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                 asm volatile("bar.sync 4, 256;" ::: "memory");
                 scales = sGs;
             }
-            for (int kb = 0; ok && kb < nkb; ++kb, ++n) {
+            for (int kb = k0; ok && kb < k0 + nk; ++kb, ++n) {
                 const float s = ws.at(n, lane, scale_of);
                 const int buf = n % MOE_NBUF;
                 if (!warp_wait(&bar.tfull[buf], (n / MOE_NBUF) & 1)) {
@@ -426,6 +435,24 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             // h = silu(gate) * up. The gate's warps take the first half of the columns, the up product's warps the
             // others, four at a time (one after another, they are all latency: 41000 cycles for 16 tokens, half as
             // much as the item's weights take); each side hands the other what it needs through shared memory.
+            if constexpr (SPLIT) {
+                // [rank - 1][column][256 rows], where rank 0's stages were
+                cluster_sync();                                  // every CTA is done with its stages
+                if (rank > 0) {
+                    const uint32_t recv = mapa_shared(smem_addr(smem), 0) +
+                                          static_cast<uint32_t>(((rank - 1) * MT * 2 * BM + half * BM + r) * 4);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        if (i < cols) st_shared_cluster_f32(recv + static_cast<uint32_t>(i * 2 * BM * 4), g[i]);
+                }
+                cluster_sync();
+                if (rank > 0) break;
+                const float* got = reinterpret_cast<const float*>(smem) + half * BM + r;
+                for (int q = 0; q < (1 << log2s) - 1; ++q)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        if (i < cols) g[i] += got[(q * MT + i) * 2 * BM];
+            }
             const int mid = (cols + 7) / 8 * 4;
             auto here = [&](int c) { return (4 * c < mid) == (half == 0); };
 #pragma unroll
@@ -489,7 +516,15 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
                     }
                 }
         }
+        if (SPLIT && mine == 0) {
+            cluster_sync();
+            cluster_sync();
+        }
         if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
+    }
+    if (SPLIT && !(warp >= MOE_PROMOTE_WARP0 && warp < MOE_PROMOTE_WARP0 + MOE_PROMOTE_WARPS)) {
+        cluster_sync();
+        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
@@ -674,16 +709,26 @@ cudaError_t launch_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspac
     if (up_stages < 2 || down_stages < 2) return cudaErrorInvalidValue;
     const int up_smem = Cfg::up_fixed(nkb) + up_stages * Cfg::STAGE;
     const int down_smem = Cfg::down_fixed() + down_stages * Cfg::STAGE;
-    cudaError_t e = set_smem(moe_up_kernel<MT>, up_smem);
+    cudaError_t e = set_smem(moe_up_kernel<MT, false>, up_smem);
+    if (e == cudaSuccess) e = set_smem(moe_up_kernel<MT, true>, up_smem);
     if (e == cudaSuccess) e = set_smem(moe_down_kernel<MT>, down_smem);
     if (e != cudaSuccess) return e;
     const int most_active = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
     const int64_t items = static_cast<int64_t>(most_active) * (a.I / BK);
-    const int grid = static_cast<int>(items < num_sms ? items : num_sms);
+    // Few items: clusters of as many CTAs as fit the GPU at once, 4 K blocks or more each.
+    int log2s = 3;
+    static_assert(kMaxSplit == 8, "log2s");
+    while (log2s > 0 &&
+           (items << log2s > num_sms || nkb < 4 << log2s ||
+            ((1 << log2s) - 1) * MT * 2 * BM * 4 > up_stages * Cfg::STAGE ||
+            max_active_clusters(reinterpret_cast<const void*>(moe_up_kernel<MT, true>), MOE_THREADS, up_smem,
+                                1 << log2s) < items))
+        --log2s;
+    const int grid = static_cast<int>(items << log2s < num_sms ? items << log2s : num_sms);
     const float* xs = reinterpret_cast<const float*>(a.ws + w.xs);
     float* hs = reinterpret_cast<float*>(a.ws + w.hs);
-    e = launch_pdl(moe_up_kernel<MT>, grid, MOE_THREADS, up_smem, stream, m.w13, m.x8, a, xs, a.ws + w.h8, hs,
-                   up_stages);
+    e = launch_pdl_cluster(log2s ? moe_up_kernel<MT, true> : moe_up_kernel<MT, false>, dim3(grid), MOE_THREADS, up_smem,
+                           stream, 1 << log2s, false, m.w13, m.x8, a, xs, a.ws + w.h8, hs, up_stages, log2s);
     if (e != cudaSuccess) return e;
     // The most CTAs per pair of slabs that leave every cluster of the grid its own SMs and each CTA work.
     const int pairs = (a.D / BM + 1) / 2;

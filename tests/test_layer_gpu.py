@@ -523,6 +523,25 @@ def test_moe_experts(T, D, I, E, k, fmt):
     assert torch.equal(y, again)
 
 
+@pytest.mark.parametrize("T,D,I,E,k", [
+    (1, 1024, 128, 4, 1), (3, 4480, 512, 8, 1), (5, 4736, 128, 24, 4), (20, 1536, 128, 8, 2), (64, 2176, 128, 4, 2),
+    (64, 4096, 256, 2, 2),
+])
+@pytest.mark.parametrize("same", [False, True])
+def test_moe_few_items_for_the_gpu(T, D, I, E, k, same):
+    # `same`: all tokens choose the same experts, so that fewer are met than there could be
+    g = gen(T + D + I)
+    x = rand(g, T, D)
+    w13, s13 = moe_weights(g, E, 2 * I, D, False)
+    w2, s2 = moe_weights(g, E, D, I, False)
+    ids = torch.stack([torch.arange(k, device="cuda") if same else
+                       torch.randperm(E, generator=g, device="cuda")[:k] for _ in range(T)]).int()
+    weights = torch.rand(T, k, generator=g, device="cuda")
+    y = fp8bs.moe_experts(x, weights, ids, w13, s13, w2, s2)
+    moe_close(y, moe_ref(x, weights, ids, w13, s13, w2, s2, False))
+    assert torch.equal(y, fp8bs.moe_experts(x, weights, ids, w13, s13, w2, s2))
+
+
 def test_moe_experts_absent_repeated_and_bad_ids():
     g = gen(5)
     T, D, I, E, k = 6, 256, 256, 4, 3
