@@ -19,7 +19,7 @@
 // 64 tokens 255 us for the layer (up, down and router overlap), 5.5 TB/s (0.83 of a copy's rate);
 // 7 tokens 186 us for 1.2 GB (0.98); one token 67 us for 353 MB (0.79): the router comes first,
 // and the grids are 128 and 112 CTAs for 152 SMs. At 64 tokens the down kernel's 112 CTAs have 64 columns to scale
-// per K block, 93 us where its weights take 70.
+// per K block, 87 us where its weights take 70.
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 

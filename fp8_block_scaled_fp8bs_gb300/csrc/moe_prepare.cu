@@ -7,7 +7,7 @@
 // L2 after their first reader) are spread over 8 SMs even for a single token. The partial logits meet
 // in CTA 0 through distributed shared memory, are added in rank order (the same bits every time) and
 // one warp per token makes the choice. Bound by latency: a single token's 32 x 7168 router is
-// 0.46 MB, 5 us in front of the experts' first weights; 64 tokens 13 us (16 clusters, 128 CTAs).
+// 0.46 MB: 4.2 us for the choice alone, 7.7 for 64 tokens (16 clusters, 128 CTAs).
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
