@@ -369,6 +369,22 @@ def test_attention_long_chunk():
     attention_check(paged_case(8, [700], [1700], 8, 2, 128, 128, 64), [700], [1700])
 
 
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("n,L,hq,hk,window,causal", [
+    (1999, 2300, 24, 8, 0, True),      # 192 tiles of rows: one whole round of CTAs and a part of one
+    (2500, 2500, 32, 8, 0, True),      # 320: two and a part
+    (1230, 3001, 32, 16, 500, True),   # 160, a window
+    (1230, 1300, 16, 8, 0, False),     # 80: less than a round
+])
+def test_attention_rounds_of_one_sequence(dk, dv, n, L, hq, hk, window, causal):
+    attention_check(paged_case(17, [n], [L], hq, hk, dk, dv, 32), [n], [L], window=window, causal=causal)
+
+
+def test_attention_rounds_of_a_batch():
+    news, lens = [700, 1, 1100, 300], [700, 900, 1500, 2001]
+    attention_check(paged_case(18, news, lens, 32, 16, 128, 128, 16), news, lens)
+
+
 @pytest.mark.parametrize("scale", [0.0, 1.0, 3.0])
 def test_attention_scales(scale):
     # flat, and almost one key only: large scores, whose maximum moves a lot between tiles. Scores grow
