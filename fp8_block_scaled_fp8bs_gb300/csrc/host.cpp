@@ -8,6 +8,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -17,7 +18,6 @@
 #include <map>
 #include <string>
 #include <utility>
-#include <vector>
 
 #include "../../include/fp8bs.h"
 
@@ -165,25 +165,20 @@ Cache cache_of(PyObject* o, int dev) {
 
 // ------------------------------------------------------------------------------ workspaces
 
-// Device memory for one call on a stream: one buffer per device and stream, which its calls, one after another,
-// share. It grows by doubling; smaller ones before it are kept, since a captured graph may still use them.
-struct Scratch {
-    std::vector<at::Tensor> held;
-    void* ptr = nullptr;
-    size_t bytes = 0;
-};
-
-Scratch& scratch(int dev, void* stream) {
-    static std::map<std::pair<int, void*>, Scratch>* all = new std::map<std::pair<int, void*>, Scratch>;
-    return (*all)[{dev, stream}];
-}
-
-void grow(Scratch& s, size_t bytes, const at::Tensor& like) {
-    if (s.bytes >= bytes) return;
-    const size_t size = std::max(bytes, s.bytes ? 2 * s.bytes : size_t{1} << 20);
-    s.held.push_back(at::empty({static_cast<int64_t>(size)}, like.options().dtype(at::kByte)));
-    s.ptr = s.held.back().data_ptr();
-    s.bytes = size;
+// Device memory for one call. Calls on a stream run one after another and share one buffer per device and stream, which
+// grows by doubling (the outgrown one goes back to the allocator, which hands it out again in the stream's order). A
+// call that is being captured gets memory of its own from the allocator, as an output would: the graph keeps the
+// address and may be replayed on any stream, beside graphs that were captured on the same one and beside eager calls.
+at::Tensor scratch(int dev, void* stream, size_t bytes, const at::Tensor& like) {
+    const auto make = [&](size_t size) {
+        return at::empty({static_cast<int64_t>(size)}, like.options().dtype(at::kByte));
+    };
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return make(bytes);
+    static auto* all = new std::map<std::pair<int, void*>, at::Tensor>;
+    at::Tensor& held = (*all)[{dev, stream}];
+    const size_t have = held.defined() ? held.nbytes() : 0;
+    if (have < bytes) held = make(std::max(bytes, have ? 2 * have : size_t{1} << 20));
+    return held;
 }
 
 void* current_stream(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
@@ -298,11 +293,11 @@ PyObject* paged_attention(PyObject* const* x) {
     void* stream = current_stream(dev);
     size_t need = 0;
     check_status("fp8bs_paged_attention", p_paged_attention_workspace_size(&a, &need));
+    at::Tensor work;                   // (held until the call is queued)
     if (need > 0) {
-        Scratch& s = scratch(dev, stream);
-        grow(s, need, q);
-        a.workspace = s.ptr;
-        a.workspace_bytes = s.bytes;
+        work = scratch(dev, stream, need, q);
+        a.workspace = work.data_ptr();
+        a.workspace_bytes = work.nbytes();
     }
     check_status("fp8bs_paged_attention", p_paged_attention(&a, stream));
     if (!lse.defined()) return THPVariable_Wrap(std::move(out));
@@ -380,12 +375,10 @@ Experts experts_of(const at::Tensor& t, int dev, PyObject* const* x) {
     return e;
 }
 
-Scratch& expert_scratch(const Experts& e, int64_t top_k, int dev, void* stream, const at::Tensor& like) {
+at::Tensor expert_scratch(const Experts& e, int64_t top_k, int dev, void* stream, const at::Tensor& like) {
     size_t need = 0;
     check_status("fp8bs_moe_workspace_size", p_moe_workspace_size(e.T, e.D, e.I, e.E, top_k, &need));
-    Scratch& s = scratch(dev, stream);
-    grow(s, need, like);
-    return s;
+    return scratch(dev, stream, need, like);
 }
 
 // x, weights, ids, w13, s13, w2, s2, scale_fmt (0 or 1), out
@@ -400,11 +393,11 @@ PyObject* moe_experts(PyObject* const* x) {
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     at::Tensor y = output(x[8], {e.T, e.D}, t);
     void* stream = current_stream(dev);
-    Scratch& s = expert_scratch(e, ids.size(1), dev, stream, t);
+    const at::Tensor work = expert_scratch(e, ids.size(1), dev, stream, t);
     check_status("fp8bs_moe_experts",
                  p_moe_experts(t.data_ptr(), weights.data_ptr<float>(), ids.data_ptr<int32_t>(), e.w13, e.s13, e.w2,
                                e.s2, y.data_ptr(), e.T, e.D, e.I, e.E, ids.size(1), static_cast<int>(integer(x[7])),
-                               s.ptr, s.bytes, stream));
+                               work.data_ptr(), work.nbytes(), stream));
     return THPVariable_Wrap(std::move(y));
 }
 
@@ -419,10 +412,10 @@ PyObject* moe_layer(PyObject* const* x) {
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     at::Tensor y = output(x[14], {e.T, e.D}, t);
     void* stream = current_stream(dev);
-    Scratch& s = expert_scratch(e, r.top_k, dev, stream, t);
+    const at::Tensor work = expert_scratch(e, r.top_k, dev, stream, t);
     check_status("fp8bs_moe_layer",
                  p_moe_layer(t.data_ptr(), &r, e.w13, e.s13, e.w2, e.s2, y.data_ptr(), e.T, e.D, e.I, e.E,
-                             static_cast<int>(integer(x[13])), s.ptr, s.bytes, stream));
+                             static_cast<int>(integer(x[13])), work.data_ptr(), work.nbytes(), stream));
     return THPVariable_Wrap(std::move(y));
 }
 
