@@ -127,6 +127,14 @@ int check_attention_sizes(const fp8bs_paged_attention_args& a) {
     return FP8BS_OK;
 }
 
+// A window as long as the longest sequence leaves nothing out: none, so that sums with what remains stay far below
+// 2^63 (callers without a window may pass the largest integer).
+fp8bs_paged_attention_args without_idle_window(const fp8bs_paged_attention_args& args) {
+    fp8bs_paged_attention_args a = args;
+    if (a.window >= a.max_kv_len) a.window = 0;
+    return a;
+}
+
 }  // namespace
 
 extern "C" int fp8bs_paged_attention_workspace_size(const fp8bs_paged_attention_args* args,
@@ -137,15 +145,16 @@ extern "C" int fp8bs_paged_attention_workspace_size(const fp8bs_paged_attention_
     int sms = 0;
     const int dev = check_device(&sms);
     if (dev != FP8BS_OK) return dev;
-    *bytes = args->T == 0 ? 0 : fp8bs::attention_workspace(*args, fp8bs::attention_plan(*args, sms));
+    const fp8bs_paged_attention_args a = without_idle_window(*args);
+    *bytes = a.T == 0 ? 0 : fp8bs::attention_workspace(a, fp8bs::attention_plan(a, sms));
     return FP8BS_OK;
 }
 
 extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, void* stream) {
     if (!args) return FP8BS_ERR_INVALID_ARG;
-    const fp8bs_paged_attention_args& a = *args;
-    int rc = check_attention_sizes(a);
+    int rc = check_attention_sizes(*args);
     if (rc != FP8BS_OK) return rc;
+    const fp8bs_paged_attention_args a = without_idle_window(*args);
     if (!stride_ok(a.q_token_stride) || !stride_ok(a.q_head_stride)) return FP8BS_ERR_INVALID_ARG;
     rc = check_cache(a.cache, true);
     if (rc == FP8BS_ERR_INVALID_ARG || a.cache.pages < 1) return FP8BS_ERR_INVALID_ARG;

@@ -66,3 +66,15 @@ def test_graphs_of_one_capture_stream_in_flight_at_once(call):
                 eager.append(calls[1]())
         torch.cuda.synchronize()
         assert torch.equal(outs[0], refs[0]) and all(torch.equal(o, refs[1]) for o in eager)
+
+
+# --------------------------------------------------------------------------------------- windows
+
+@pytest.mark.parametrize("window", [2 ** 63 - 1, 2 ** 63 - 200, 2 ** 62, 2 ** 32 + 100, 2 ** 31, 5000])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("news,lens", [([1, 1], [5000, 3]), ([200, 1, 30], [300, 900, 10]), ([300], [4000])])
+def test_window_longer_than_any_sequence(window, causal, news, lens):
+    c = paged_case(51, news, lens, 8, 2, 128, 128, 16)
+    ref = fp8bs.paged_attention(**c, causal=causal, max_kv_len=max(lens), return_lse=True)
+    out = fp8bs.paged_attention(**c, causal=causal, max_kv_len=max(lens), window=window, return_lse=True)
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
