@@ -13,6 +13,8 @@
 // which bf16 and fp32 hold without loss, and O is left alone. So no row waits for its maximum. The row sum is
 // taken from P before its rounding to bf16, so lse is exact to binary32; the rounding of P (2^-9 on average per
 // term) is of the size of the output's own.
+// A row without keys is one whose sum is zero. A score that is not a number, or +infinite, makes the sum NaN (the
+// maximum passes over NaN), and with it the row, in one piece or in many.
 //
 // Two forms (AttnCfg): NQ = 2 query tiles per CTA for chunks, whose softmax warps work on one tile
 // while the tensor core works on the other; NQ = 1 with two S buffers for few rows.
@@ -284,7 +286,7 @@ constexpr uint32_t kIdescBMajorMN = 1u << 16;
 
 struct AttnParts {
     float* o;      // [piece][T * q_heads][DV], unnormalised
-    float2* ml;    // [piece][T * q_heads]: (maximum in log2 units, sum)
+    float2* ml;    // [piece][T * q_heads]: (maximum in log2 units, sum); a sum of zero: no keys, o not written
     int64_t rows;  // T * q_heads
 };
 
@@ -498,8 +500,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const int r = q * 128 + quarter * 32 + lane;          // row of the item's tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
-        // (a scale of zero: any tiny factor keeps -inf apart from the finite scores)
-        const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        // (a scale of zero: any tiny factor keeps -inf apart from the finite scores; one that is NaN stays so)
+        const float c_scale = fabsf(a.scale) * 1.4426950408889634f;
+        const float c = c_scale < 1e-30f ? 1e-30f : c_scale;
         // Queries of query tile q into shared memory (K-major, 128-byte swizzle), valid rows only (what the
         // others hold is of no consequence: rows do not meet). A negative scale turns their signs, so that
         // the row maximum is always that of the largest S.
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             if (ok && !idle) {
                 const int64_t row = live ? out_row(it, r) : 0;
                 const float mc = m == -INFINITY ? -INFINITY : m * c;
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;       // (NaN stays NaN)
                 if (pieces > 1) {
                     float* dst = parts.o + (it.piece * parts.rows + row) * DV;
                     if (nt > 0)
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                     pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
                     }
                     if (live && a.lse)
-                        a.lse[row] = l > 0.0f ? (mc + log2_fast(l)) * 0.6931471805599453f : -INFINITY;
+                        a.lse[row] = l == 0.0f ? -INFINITY : (mc + log2_fast(l)) * 0.6931471805599453f;
                 }
             }
             tc_fence_before();
@@ -936,7 +939,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnParts par
         float w = 0.0f;
         if (mine < pieces) {
             const float2 ml = parts.ml[mine * parts.rows + row];
-            if (ml.x > -INFINITY) {
+            if (ml.y != 0.0f) {                      // (a sum that is NaN makes the row's NaN, whatever w is)
                 w = exp2_fast(ml.x - top);
                 l = fmaf(w, ml.y, l);
             }
@@ -945,7 +948,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnParts par
 #pragma unroll 8
         for (int i = 0; i < count; ++i) {
             const float wi = __shfl_sync(0xffffffffu, w, i);
-            if (wi > 0.0f) {                     // (an empty piece's O has not been written)
+            if (wi != 0.0f) {                    // (an empty piece's O has not been written)
                 const float* src = parts.o + ((base + WPR * i + warp) * parts.rows + row) * DV + PER * lane;
 #pragma unroll
                 for (int k = 0; k < PER; k += 2) {
@@ -972,12 +975,12 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnParts par
             for (int k = 0; k < PER; ++k) o[k] += s_o[w][PER * lane + k];
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint32_t* dst = reinterpret_cast<uint32_t*>(out + row * DV) + PER / 2 * lane;
 #pragma unroll
     for (int i = 0; i < PER / 2; ++i) dst[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
     if (lse && lane == 0)
-        lse[row] = l > 0.0f ? (top + log2_fast(l)) * 0.6931471805599453f : -INFINITY;
+        lse[row] = l == 0.0f ? -INFINITY : (top + log2_fast(l)) * 0.6931471805599453f;
 }
 
 int64_t tile_bound(const fp8bs_paged_attention_args& a, int rows) {

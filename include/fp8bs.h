@@ -399,7 +399,8 @@ FP8BS_API int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stre
  *
  * with query head h reading key head h / (q_heads / cache.heads). Scores, softmax sums and o are
  * held in binary32, the probabilities rounded to bf16 for their product with v, o to bf16 at the
- * end. A query with no key gets o = 0, lse = -inf. Keys at and past L, and pages that end before
+ * end. A query with no key (or whose scores are all -infinity) gets o = 0, lse = -inf; one with a score that is NaN or
+ * +infinity gets NaN for both. Keys at and past L, and pages that end before
  * the window of a sequence's first query, are never used, whatever they hold (their table entries
  * are not read: the pages may have been given back); the values of the other keys have to be
  * finite, those outside a query's window too. A page id outside the cache sets FP8BS_DEVERR_INDEX and reads as zeros.

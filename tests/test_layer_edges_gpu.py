@@ -78,3 +78,61 @@ def test_window_longer_than_any_sequence(window, causal, news, lens):
     ref = fp8bs.paged_attention(**c, causal=causal, max_kv_len=max(lens), return_lse=True)
     out = fp8bs.paged_attention(**c, causal=causal, max_kv_len=max(lens), window=window, return_lse=True)
     assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
+# --------------------------------------------------------------------------- scores that are not finite
+
+def not_finite_case(dk, dv, n, L):
+    c = paged_case(61, [n], [L], 8, 2, dk, dv, 16)
+    q, k = c["q"], c["cache"].k
+
+    def key(j, head):
+        return k[int(c["page_table"][0, j // 16]), j % 16, head]
+
+    pages = c["page_table"][0, :-(-L // 16)].long()
+    k[pages, :, 1, 9] = k[pages, :, 1, 9].abs() + 0.125
+    q[0, 0] = float("nan")                                   # a query: all its scores are NaN
+    q[0, 1, 5] = float("inf")                                # scores of both infinities, then
+    key(2, 1)[7] = float("inf")                              # one key: +-infinity by the query's sign
+    key(L - 1, 0)[3] = float("nan")                          # one key of the last query alone
+    q[0, 6] = 0
+    q[0, 6, 9], q[0, 6, 7] = -float("inf"), -1               # all scores -infinity
+    return c
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("n,L", [(1, 40), (1, 20000), (5, 3000), (300, 400), (300, 6000)])
+def test_scores_that_are_not_finite(dk, dv, n, L):
+    # one tile of queries and two, in one piece of the keys and in many
+    c = not_finite_case(dk, dv, n, L)
+    out, lse = fp8bs.paged_attention(**c, return_lse=True)
+    j = torch.arange(L, device="cuda")
+    pg = c["page_table"][0].long()[j // 16]
+    k = c["cache"].k[pg, j % 16].double().repeat_interleave(4, 1)
+    v = c["cache"].v[pg, j % 16].double().repeat_interleave(4, 1)
+    s = torch.einsum("nhd,khd->nhk", c["q"].double(), k) * dk ** -0.5
+    s[0, 6] = -float("inf")                 # (in the sum above its zeros meet the infinity of one key's channel)
+    seen = (j <= L - n + torch.arange(n, device="cuda")[:, None])[:, None]
+    bad = ((torch.isnan(s) | (s == float("inf"))) & seen).any(-1)
+    s = s.masked_fill(~seen, -float("inf"))
+    none = ~bad & torch.isinf(s).all(-1)
+    assert bool(bad[0, :2].all()) and bool(none[0, 6]) and int(none.sum()) == 1 and not bool(bad[:, 4:].all())
+    assert bool(torch.isnan(out[bad].float()).all()) and bool(torch.isnan(lse[bad]).all())
+    assert bool((out[none] == 0).all()) and bool((lse[none] == -float("inf")).all())
+    good = ~bad & ~none
+    l = torch.logsumexp(s, -1)
+    p = torch.exp(s - l[..., None])
+    p[~good] = 0
+    o = torch.einsum("nhk,khd->nhd", p, v)
+    mag = torch.einsum("nhk,khd->nhd", p, v.abs())
+    # as in attention_check: probabilities and output rounded to bf16, binary32 scores and sums
+    err = (out.double() - o).abs()
+    assert bool((err <= (2.0 ** -7 + 2.0 ** -12) * mag + 1e-30)[good].all())
+    assert bool(((lse.double() - l)[good].abs() <= 1e-4).all())
+
+
+@pytest.mark.parametrize("n,L", [(1, 40), (1, 20000), (300, 400)])
+def test_a_scale_that_is_not_a_number(n, L):
+    c = paged_case(62, [n], [L], 8, 2, 128, 128, 16)
+    out, lse = fp8bs.paged_attention(**c, scale=float("nan"), return_lse=True)
+    assert bool(torch.isnan(out.float()).all()) and bool(torch.isnan(lse).all())
