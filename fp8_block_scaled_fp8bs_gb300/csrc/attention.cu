@@ -1037,6 +1037,17 @@ cudaError_t launch_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
 
 }  // namespace
 
+namespace {
+
+// Bytes that one piece of the keys leaves for the join: every row's O, maximum and sum.
+int64_t part_bytes(const fp8bs_paged_attention_args& a) { return a.T * a.q_heads * (a.cache.dv * 4 + 8); }
+
+// Most bytes that all pieces leave (a single one leaves none). 64 sequences of 64 heads of 128 channels: 245 pieces,
+// so that a table of 250,000 keys still gives the pieces of 1024 that ragged batches want.
+constexpr int64_t kMaxPartBytes = int64_t{1} << 29;
+
+}  // namespace
+
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
     const bool two = two_tiles(a);
     const int64_t rows = two ? 256 : 128;
@@ -1080,6 +1091,9 @@ AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
         // not finish last on its own
         len = 1024;
     }
+    // The bounds may be far above the sequences (a page table's whole width): no more pieces than kMaxPartBytes hold.
+    const int64_t most = std::max<int64_t>(1, kMaxPartBytes / std::max<int64_t>(1, part_bytes(a)));
+    if (len * most < keys) len = (keys + most - 1) / most;
     len = std::min<int64_t>((len + unit - 1) / unit * unit, int64_t{1} << 30);
     AttentionPlan p;
     p.piece_len = static_cast<int>(len);
@@ -1089,8 +1103,7 @@ AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
 
 size_t attention_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan) {
     if (plan.pieces == 1) return 0;
-    return static_cast<size_t>(plan.pieces) * static_cast<size_t>(a.T * a.q_heads) *
-           (static_cast<size_t>(a.cache.dv) * 4 + 8);
+    return static_cast<size_t>(plan.pieces) * static_cast<size_t>(part_bytes(a));
 }
 
 cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,

@@ -412,7 +412,8 @@ FP8BS_API int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stre
  *   max_q_len, max_kv_len: bounds on n and L that the caller knows on the host; they steer how
  *       the work is cut (max_kv_len at most 2^31 - 1024). A sequence past them sets
  *       FP8BS_DEVERR_INDEX and leaves its rows of out undefined.
- *   workspace: fp8bs_paged_attention_workspace_size(args) bytes, 16-byte aligned (0 bytes: NULL).
+ *   workspace: fp8bs_paged_attention_workspace_size(args) bytes, 16-byte aligned (0 bytes: NULL); at most 2^29 where
+ *       max_kv_len is up to 2^30.
  *       Its contents need not be kept between calls; calls that may overlap need their own.
  *
  * The key axis is cut into pieces of equal length when the rows alone would not fill the GPU; the

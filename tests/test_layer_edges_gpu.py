@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_layer_gpu import gen, moe_weights, no_device_error, paged_case, rand  # noqa: F401
+from test_layer_gpu import attention_check, gen, moe_weights, no_device_error, paged_case, rand  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,32 @@ def test_a_scale_that_is_not_a_number(n, L):
     c = paged_case(62, [n], [L], 8, 2, 128, 128, 16)
     out, lse = fp8bs.paged_attention(**c, scale=float("nan"), return_lse=True)
     assert bool(torch.isnan(out.float()).all()) and bool(torch.isnan(lse).all())
+
+
+# ------------------------------------------------------------------------- bounds far above the lengths
+
+@pytest.mark.parametrize("B,n,hq,hk,dk,dv,kv", [
+    (150, 16, 64, 8, 128, 128, 131072),       # a page table for long conversations, short chunks
+    (64, 1, 64, 8, 128, 128, 1 << 20),
+    (1, 1, 32, 8, 128, 128, 1 << 30),
+    (128, 1, 128, 8, 192, 128, 65536),
+    (64, 1, 16, 16, 64, 64, 1 << 24),
+    (1, 8192, 64, 1, 128, 128, 1 << 20),      # one chunk: two query tiles
+    (4, 1, 16, 4, 128, 128, 33000),
+])
+def test_workspace_is_bounded(B, n, hq, hk, dk, dv, kv):
+    torch.cuda.init()
+    a = fp8bs.PagedAttentionArgs(
+        cache=fp8bs.KvCache(pages=1, page_size=16, heads=hk, dk=dk, dv=dv), table_stride=-(-kv // 16), B=B, T=B * n,
+        q_heads=hq, max_q_len=n, max_kv_len=kv, causal=1, scale=1.0)
+    assert fp8bs.fp8bs_paged_attention_workspace_size(a) <= 1 << 29
+
+
+@pytest.mark.parametrize("news,lens", [([1] * 30, [10 * b + 1 for b in range(30)]), ([16] * 30, [300] * 30),
+                                       ([500, 1], [500, 3000])])
+def test_tables_far_wider_than_the_sequences(news, lens):
+    c = paged_case(71, news, lens, 64, 8, 64, 64, 16)
+    wide = torch.full((len(lens), 1 << 20), -7, dtype=torch.int32, device="cuda")
+    wide[:, :c["page_table"].shape[1]] = c["page_table"]
+    c["page_table"] = wide
+    attention_check(c, news, lens)
