@@ -230,6 +230,13 @@ __device__ __forceinline__ float log2_fast(float x) {
     return y;
 }
 
+// The larger one, or NaN if either is. (The same by comparison and selection cost the chunk of 4096 1.3 %.)
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(
@@ -501,8 +508,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
         // (a scale of zero: any tiny factor keeps -inf apart from the finite scores; one that is NaN stays so)
-        const float c_scale = fabsf(a.scale) * 1.4426950408889634f;
-        const float c = c_scale < 1e-30f ? 1e-30f : c_scale;
+        const float c = max_nan(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
         // Queries of query tile q into shared memory (K-major, 128-byte swizzle), valid rows only (what the
         // others hold is of no consequence: rows do not meet). A negative scale turns their signs, so that
         // the row maximum is always that of the largest S.
