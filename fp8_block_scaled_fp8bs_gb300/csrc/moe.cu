@@ -46,6 +46,10 @@ struct Routing {
     int n;
 };
 
+// Dynamic shared memory of both kernels, at most: what Routing and the TMEM address leave.
+constexpr int kMoeSmem = kSmemLimit - 6144;
+static_assert(sizeof(Routing) + 64 <= 6144, "static shared memory");
+
 // All threads of the CTA: before the ids are there, and when they are (`first`: this thread's own; a block barrier
 // between the two, and one at the end).
 __device__ __forceinline__ void clear_routing(Routing& r, const MoeArgs& a) {
@@ -171,7 +175,7 @@ struct MoeCfg {
     }
     static constexpr int down_fixed() { return 1024 + kMaxStages * F_BYTES + moe_bar_bytes(kMaxStages); }
     static int stages(int fixed) {
-        const int s = (kSmemLimit - 6144 - fixed) / STAGE;   // (Routing is static)
+        const int s = (kMoeSmem - fixed) / STAGE;
         return s < kMaxStages ? s : kMaxStages;
     }
 };
@@ -709,9 +713,10 @@ cudaError_t launch_experts(const MoeMaps& m, const MoeArgs& a, const MoeWorkspac
     if (up_stages < 2 || down_stages < 2) return cudaErrorInvalidValue;
     const int up_smem = Cfg::up_fixed(nkb) + up_stages * Cfg::STAGE;
     const int down_smem = Cfg::down_fixed() + down_stages * Cfg::STAGE;
-    cudaError_t e = set_smem(moe_up_kernel<MT, false>, up_smem);
-    if (e == cudaSuccess) e = set_smem(moe_up_kernel<MT, true>, up_smem);
-    if (e == cudaSuccess) e = set_smem(moe_down_kernel<MT>, down_smem);
+    // (The limit belongs to the kernel, for all threads of the process: it is the same whatever D is.)
+    cudaError_t e = set_smem(moe_up_kernel<MT, false>, kMoeSmem);
+    if (e == cudaSuccess) e = set_smem(moe_up_kernel<MT, true>, kMoeSmem);
+    if (e == cudaSuccess) e = set_smem(moe_down_kernel<MT>, kMoeSmem);
     if (e != cudaSuccess) return e;
     const int most_active = a.E < a.T * a.top_k ? a.E : a.T * a.top_k;
     const int64_t items = static_cast<int64_t>(most_active) * (a.I / BK);

@@ -21,6 +21,13 @@ constexpr int PREP_THREADS = 256;
 constexpr int PREP_EXPERTS = 4;     // experts a warp computes at once
 constexpr int PREP_AHEAD = 4;       // 16-byte pieces of each of their rows a lane has in flight
 constexpr int kMaxExperts = 512;
+constexpr int kMaxChannels = 16384;
+
+// Dynamic shared memory: x of a CTA's blocks of channels, and with a router the partial logits and the choices.
+constexpr int64_t prep_smem_bytes(int64_t D, int64_t E, bool router) {
+    const int64_t blocks = (D / BK + PREP_CLUSTER - 1) / PREP_CLUSTER;
+    return PREP_TOKENS * blocks * BK * 2 + (router ? (PREP_CLUSTER + 1) * PREP_TOKENS * E * 4 : 0);
+}
 
 struct PrepArgs {
     const uint4* x;
@@ -310,10 +317,9 @@ cudaError_t launch_moe_prepare(const void* x, const fp8bs_moe_routing* routing, 
         a.normalise = routing->normalise;
         a.route_scale = routing->route_scale;
     }
-    const int64_t nb_max = (D / BK + PREP_CLUSTER - 1) / PREP_CLUSTER;
-    int64_t smem = PREP_TOKENS * nb_max * BK * 2;
-    if (routing) smem += (PREP_CLUSTER + 1) * PREP_TOKENS * E * 4;
-    cudaError_t e = set_smem(moe_prepare_kernel, static_cast<int>(smem));
+    const int64_t smem = prep_smem_bytes(D, E, routing != nullptr);
+    // (The limit belongs to the kernel, for all threads of the process: it is the same whatever D and E are.)
+    cudaError_t e = set_smem(moe_prepare_kernel, static_cast<int>(prep_smem_bytes(kMaxChannels, kMaxExperts, true)));
     if (e != cudaSuccess) return e;
     const int64_t clusters = (T + PREP_TOKENS - 1) / PREP_TOKENS;
     return launch_pdl_cluster(moe_prepare_kernel, dim3(static_cast<unsigned>(clusters * PREP_CLUSTER)),

@@ -1,4 +1,6 @@
 """The operators around the FP8 products of a decoder layer at the edges of what they accept."""
+import threading
+
 import pytest
 import torch
 
@@ -165,3 +167,63 @@ def test_tables_far_wider_than_the_sequences(news, lens):
     wide[:, :c["page_table"].shape[1]] = c["page_table"]
     c["page_table"] = wide
     attention_check(c, news, lens)
+
+
+# -------------------------------------------------------------------------------- several host threads
+
+def test_host_threads_with_layers_of_different_sizes():
+    # what one thread's calls set for a kernel must suit the other's: the shared memory of both kernels depends
+    # on the sizes. (The raw calls: they let other threads run.)
+    g = gen(81)
+    fp8bs.load()
+
+    def case(D, E, I, T):
+        x, router = rand(g, T, D), rand(g, E, D, scale=0.02)
+        w13, s13 = moe_weights(g, 2, 2 * I, D)
+        w2, s2 = moe_weights(g, 2, D, I)
+        ids = torch.randint(0, 2, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+        one = torch.ones(T, 1, device="cuda")
+        routing = fp8bs.MoeRouting(router_w=router.data_ptr(), top_k=2, groups=1, topk_groups=1, score=0, normalise=1,
+                                   route_scale=1.0)
+        size = fp8bs.fp8bs_moe_workspace_size(T, D, I, 2, 1)
+        work = torch.empty(size, dtype=torch.uint8, device="cuda")
+        weights = torch.empty(T, 2, device="cuda")
+        chosen = torch.empty(T, 2, dtype=torch.int32, device="cuda")
+        y = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+
+        def call(stream):
+            fp8bs.fp8bs_moe_route(x.data_ptr(), routing, weights.data_ptr(), chosen.data_ptr(), T, D, E, stream)
+            fp8bs.fp8bs_moe_experts(x.data_ptr(), one.data_ptr(), ids.data_ptr(), w13.data_ptr(), s13.data_ptr(),
+                                    w2.data_ptr(), s2.data_ptr(), y.data_ptr(), T, D, I, 2, 1, workspace=work.data_ptr(),
+                                    workspace_bytes=size, stream=stream)
+        keep = (x, router, w13, s13, w2, s2, ids, one, work, routing)
+        return call, lambda: (weights.clone(), chosen.clone(), y.clone()), keep
+
+    cases = [case(16384, 512, 128, 3), case(128, 8, 128, 3)]
+    refs = []
+    for call, results, _ in cases:
+        call(0)
+        torch.cuda.synchronize()
+        refs.append(results())
+    failed = []
+
+    def run(call):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            for i in range(2000):
+                call(stream.cuda_stream)
+                if i % 100 == 99:
+                    stream.synchronize()
+            stream.synchronize()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(call,)) for call, _, _ in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for (_, results, _), ref in zip(cases, refs):
+        assert all(torch.equal(a, b) for a, b in zip(results(), ref))
