@@ -491,15 +491,15 @@ _host = None
 
 
 def _load_host():
-    """The compiled host side, built if it is missing."""
+    """The compiled host side, built if it is missing or was made for another PyTorch."""
     global _host
     load()
     with _lock:
         if _host is None:
             import importlib.util
             import torch  # noqa: F401  (its libraries have to be there first)
-            if not os.path.exists(HOST_PATH):
-                from . import build as _build
+            from . import build as _build
+            if not _build.host_fits():
                 _build.build_host()
             spec = importlib.util.spec_from_file_location("_host", HOST_PATH)
             module = importlib.util.module_from_spec(spec)

@@ -1,9 +1,10 @@
 """Build libfp8bs.so and _host.so in place: each csrc/*.cu is compiled by nvcc for sm_103a in parallel and
 linked into one shared library with the CUDA runtime linked statically (the library depends on
-no CUDA shared object at load time; it reaches the driver through the runtime). _host.so (csrc/host.cpp) is a
-CPython module over PyTorch's headers: the host side of the calls that take microseconds.
+no CUDA shared object at load time; it reaches the driver through the runtime). It needs nvcc and nothing else.
+_host.so (csrc/host.cpp) is a CPython module over PyTorch's headers, the host side of the calls that take microseconds:
+a step of its own, for the installed PyTorch, and again for another one.
 
-    python -m fp8_block_scaled_fp8bs_gb300.build [--verbose-ptxas]
+    python -m fp8_block_scaled_fp8bs_gb300.build [--verbose-ptxas] [--library-only]
 """
 from __future__ import annotations
 
@@ -37,15 +38,33 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps_mtime():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "fp8bs.h"))
-    files.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(f) for f in files)
+def _newest(files):
+    return max(os.path.getmtime(f) for f in (*files, os.path.join(ROOT, "include", "fp8bs.h"), os.path.abspath(__file__)))
 
 
 def up_to_date() -> bool:
-    return all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, HOST))
+    """Of the library alone."""
+    sources_ = (os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp"))
+    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest(sources_)
+
+
+def _torch_tag() -> str:
+    """What _host.so is bound to: PyTorch's C++ interface and the interpreter's."""
+    import torch
+    return f"torch {torch.__version__} {sys.implementation.cache_tag}\n"
+
+
+def host_fits() -> bool:
+    """Whether there is a _host.so, made for the PyTorch and Python at hand."""
+    try:
+        with open(HOST + ".txt") as f:
+            return os.path.exists(HOST) and f.read() == _torch_tag()
+    except OSError:
+        return False
+
+
+def host_up_to_date() -> bool:
+    return host_fits() and os.path.getmtime(HOST) >= _newest([os.path.join(CSRC, "host.cpp")])
 
 
 def build_host() -> str:
@@ -69,6 +88,9 @@ def build_host() -> str:
     if res.returncode != 0:
         raise RuntimeError(f"C++ compiler failed on host.cpp:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, HOST)
+    with open(tmp, "w") as f:
+        f.write(_torch_tag())
+    os.replace(tmp, HOST + ".txt")
     return HOST
 
 
@@ -86,14 +108,13 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
+    """The library."""
     if not force and not ptxas_verbose and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        host = ex.submit(build_host)
+    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
-        host.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs,
            "-Xlinker", "--no-undefined", "-ldl", "-lpthread", "-lrt"]
@@ -104,9 +125,19 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     return LIB
 
 
+def build_all(force: bool = False, ptxas_verbose: bool = False) -> str:
+    """The library and, beside it, the host module; the library is there even if the host module fails."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        host = ex.submit(lambda: build_host() if force or not host_up_to_date() else HOST)
+        lib = build(force, ptxas_verbose)
+        host.result()
+    return lib
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--verbose-ptxas", action="store_true")
     ap.add_argument("--force", action="store_true")
+    ap.add_argument("--library-only", action="store_true", help="libfp8bs.so alone: needs no PyTorch")
     a = ap.parse_args()
-    print(build(force=a.force, ptxas_verbose=a.verbose_ptxas))
+    print((build if a.library_only else build_all)(force=a.force, ptxas_verbose=a.verbose_ptxas))
