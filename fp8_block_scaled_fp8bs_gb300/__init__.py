@@ -493,7 +493,7 @@ _host = None
 def _load_host():
     """The compiled host side, built if it is missing or was made for another PyTorch."""
     global _host
-    load()
+    lib = load()
     with _lock:
         if _host is None:
             import importlib.util
@@ -504,7 +504,7 @@ def _load_host():
             spec = importlib.util.spec_from_file_location("_host", HOST_PATH)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
-            module.init(LIB_PATH, Fp8bsError)
+            module.init(lib._handle, Fp8bsError)
             _host = module
     return _host
 

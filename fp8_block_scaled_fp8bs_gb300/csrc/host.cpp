@@ -439,14 +439,13 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
 }
 
-// init(path of libfp8bs.so, Fp8bsError)
+// init(handle of the loaded library, Fp8bsError)
 PyObject* init(PyObject*, PyObject* args) {
-    const char* path = nullptr;
-    PyObject* error = nullptr;
-    if (!PyArg_ParseTuple(args, "sO", &path, &error)) return nullptr;
-    void* lib = dlopen(path, RTLD_NOW | RTLD_LOCAL);
+    PyObject *handle = nullptr, *error = nullptr;
+    if (!PyArg_ParseTuple(args, "OO", &handle, &error)) return nullptr;
+    void* lib = PyLong_AsVoidPtr(handle);
     if (!lib) {
-        PyErr_SetString(PyExc_OSError, dlerror());
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_OSError, "libfp8bs.so is not loaded");
         return nullptr;
     }
 #define FP8BS_LOOKUP(name)                                                                  \
