@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_layer_gpu import attention_check, gen, moe_weights, no_device_error, paged_case, rand  # noqa: F401
+from test_layer_gpu import (attention_check, gen, moe_close, moe_ref, moe_weights, no_device_error,  # noqa: F401
+                            norm_rope_close, norm_rope_ref, paged_case, rand)
 
 pytestmark = pytest.mark.gpu
 
@@ -227,3 +228,72 @@ def test_host_threads_with_layers_of_different_sizes():
     assert not failed
     for (_, results, _), ref in zip(cases, refs):
         assert all(torch.equal(a, b) for a, b in zip(results(), ref))
+
+
+# ------------------------------------------------------------------------- far ends of what is accepted
+
+@pytest.mark.parametrize("d,rot_start,rot,interleaved", [(64, 0, 64, False), (64, 16, 32, True), (128, 0, 128, True),
+                                                         (128, 0, 128, False), (192, 128, 64, True), (256, 0, 256, False)])
+@pytest.mark.parametrize("T,hq,hk", [(2048, 7, 3), (2500, 1, 1), (5001, 3, 2)])
+def test_norm_rope_of_many_tokens(d, rot_start, rot, interleaved, T, hq, hk):
+    # the form for long chunks, with rows of q, k and v beside one another and a cache of odd pages
+    g = gen(T + d)
+    qkv = rand(g, T, (hq + 2 * hk) * d)
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([hq * d, hk * d, hk * d], 1))
+    pages = T // 7 + 2
+    ck, cv = rand(g, pages, 7, hk, d), rand(g, pages, 7, hk, d)
+    before_k, before_v = ck.clone(), cv.clone()
+    ang = torch.rand(99, rot // 2, generator=g, device="cuda") * 6.28
+    pos = torch.randint(0, 99, (T,), generator=g, device="cuda", dtype=torch.int32)
+    slots = torch.randperm(pages * 7, generator=g, device="cuda")[:T].contiguous()
+    slots[T // 2] = -1
+    w = rand(g, d)
+    qo = fp8bs.qk_norm_rope(q, k, ang.cos(), ang.sin(), pos, q_weight=w, k_weight=w, rot_start=rot_start,
+                            interleaved=interleaved, cache=fp8bs.PagedCache(ck, cv), v=v, slots=slots)
+    ref = norm_rope_ref(q, w, ang.cos(), ang.sin(), pos, rot_start, interleaved, 1e-6)
+    norm_rope_close(qo, ref, float(ref.abs().max()) * 1.5)
+    ref = norm_rope_ref(k, w, ang.cos(), ang.sin(), pos, rot_start, interleaved, 1e-6)
+    there = slots >= 0
+    norm_rope_close(ck.view(-1, hk, d)[slots[there]], ref[there], float(ref.abs().max()) * 1.5)
+    assert torch.equal(cv.view(-1, hk, d)[slots[there]], v[there])
+    rest = torch.ones(pages * 7, dtype=torch.bool, device="cuda")
+    rest[slots[there]] = False
+    rest = rest.view(pages, 7)
+    assert torch.equal(ck[rest], before_k[rest]) and torch.equal(cv[rest], before_v[rest])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("hq,hk", [(20, 1), (128, 1), (130, 1), (600, 2)])
+@pytest.mark.parametrize("news,lens", [([1, 1], [700, 33]), ([1], [9000]), ([5, 1, 3], [5, 300, 1000])])
+def test_attention_of_many_query_heads_to_a_key_head(dk, dv, hq, hk, news, lens):
+    attention_check(paged_case(91, news, lens, hq, hk, dk, dv, 16), news, lens)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (192, 128)])
+@pytest.mark.parametrize("news,lens", [([1, 1], [700, 12000]), ([150, 1], [150, 300])])
+def test_attention_negative_scale(dk, dv, news, lens):
+    attention_check(paged_case(92, news, lens, 8, 2, dk, dv, 16), news, lens, scale=-0.125)
+
+
+@pytest.mark.parametrize("T,D,I,E,k", [
+    (1, 16384, 128, 4, 2), (5, 16384, 256, 4, 2), (20, 16384, 128, 4, 2), (64, 16384, 256, 3, 2),
+    (1, 128, 16384, 3, 1), (9, 256, 16384, 3, 2), (64, 128, 16384, 2, 2),
+    (2, 512, 256, 16, 4), (7, 2048, 1024, 8, 2), (33, 1024, 512, 12, 3), (64, 512, 1024, 16, 8),
+])
+@pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
+def test_moe_experts_as_a_whole(T, D, I, E, k, fmt):
+    # Beside the bound of each output, which allows each a code on the other side of a rounding boundary, the size of all
+    # errors together. y's rounding to bf16 is at most 2^-8 of its size. A code goes the other way where h is within its
+    # binary32 error (2^-16 of it, say) of a boundary; these are 2^-4 of it apart, so one code in 2^11 does, and moves its
+    # term by 2^-3 at most: 2^-3 / sqrt(2^11) < 2^-8 of the size. A lost block of 128 of the k * I terms would be
+    # sqrt(128 / (k I)), 2^-4 or more here.
+    g = gen(T * 17 + D + I)
+    x = rand(g, T, D)
+    w13, s13 = moe_weights(g, E, 2 * I, D, fmt == "ue8m0")
+    w2, s2 = moe_weights(g, E, D, I, fmt == "ue8m0")
+    ids = torch.stack([torch.randperm(E, generator=g, device="cuda")[:k] for _ in range(T)]).int()
+    weights = torch.rand(T, k, generator=g, device="cuda") + 0.5
+    y = fp8bs.moe_experts(x, weights, ids, w13, s13, w2, s2, scale_fmt=fmt)
+    ref = moe_ref(x, weights, ids, w13, s13, w2, s2, fmt == "ue8m0")
+    moe_close(y, ref)
+    assert float((y.double() - ref[0]).norm() / ref[0].norm()) <= 2.0 ** -7
