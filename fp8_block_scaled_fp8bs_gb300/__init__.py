@@ -526,7 +526,8 @@ def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=Tr
     pages page_table[b] (int32 [B, n]) -> out bf16 [T, Hq, Dv] (and lse fp32 [T, Hq]). q_start int32
     [B+1] and kv_len int32 [B] are on the GPU; max_q_len and max_kv_len bound them for the host
     (default: T, and what the table can hold; tighter is faster). window > 0: each query sees that
-    many keys at most, its own the last."""
+    many keys at most, its own the last. A query without keys gets 0 (lse -inf), one with a score
+    that is NaN or +inf gets NaN."""
     return (_host or _load_host()).paged_attention(q, cache, page_table, q_start, kv_len, scale, causal, window,
                                                    max_q_len, max_kv_len, out, return_lse)
 

@@ -399,21 +399,24 @@ FP8BS_API int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stre
  *
  * with query head h reading key head h / (q_heads / cache.heads). Scores, softmax sums and o are
  * held in binary32, the probabilities rounded to bf16 for their product with v, o to bf16 at the
- * end. A query with no key (or whose scores are all -infinity) gets o = 0, lse = -inf; one with a score that is NaN or
- * +infinity gets NaN for both. Keys at and past L, and pages that end before
+ * end. A query with no key (or whose scores are all -infinity) gets o = 0, lse = -inf; one with a
+ * score that is NaN or +infinity gets NaN for both. Keys at and past L, and pages that end before
  * the window of a sequence's first query, are never used, whatever they hold (their table entries
  * are not read: the pages may have been given back); the values of the other keys have to be
- * finite, those outside a query's window too. A page id outside the cache sets FP8BS_DEVERR_INDEX and reads as zeros.
+ * finite, those outside a query's window too. A page id outside the cache sets FP8BS_DEVERR_INDEX
+ * and reads as zeros.
  *
  *   q [T, q_heads, dk] bf16, rows contiguous and 16-byte aligned, strides multiples of 8.
  *   out bf16 [T, q_heads, dv] contiguous, 16-byte aligned. lse fp32 [T, q_heads] or NULL.
  *   page_table int32 [B, table_stride]; q_start int32 [B+1], q_start[0] = 0, q_start[B] = T (rows
- *   of out past a smaller q_start[B] are left undefined); kv_len int32 [B].   (dk, dv): (64, 64), (128, 128) or (192, 128).
+ *   of out past a smaller q_start[B] are left undefined); kv_len int32 [B].
+ *   (dk, dv): (64, 64), (128, 128) or (192, 128).   window: any size; of max_kv_len or more, it
+ *   leaves nothing out.
  *   max_q_len, max_kv_len: bounds on n and L that the caller knows on the host; they steer how
  *       the work is cut (max_kv_len at most 2^31 - 1024). A sequence past them sets
  *       FP8BS_DEVERR_INDEX and leaves its rows of out undefined.
- *   workspace: fp8bs_paged_attention_workspace_size(args) bytes, 16-byte aligned (0 bytes: NULL); at most 2^29 where
- *       max_kv_len is up to 2^30.
+ *   workspace: fp8bs_paged_attention_workspace_size(args) bytes, 16-byte aligned (0 bytes: NULL),
+ *       at most 2^29 for a max_kv_len up to 2^30.
  *       Its contents need not be kept between calls; calls that may overlap need their own.
  *
  * The key axis is cut into pieces of equal length when the rows alone would not fill the GPU; the
@@ -477,7 +480,9 @@ FP8BS_API int fp8bs_moe_route(const void* x, const fp8bs_moe_routing* routing, f
  * block of activations and 128 x 128 block of weights, accumulated in binary32. Nothing between the
  * codes of x and y is rounded to bf16: the gate, the sum over experts and the weights stay in
  * binary32, y is rounded once. An id of -1 chooses nothing; another id outside [0, experts) sets
- * FP8BS_DEVERR_INDEX and chooses nothing. A token without experts gets y = 0.
+ * FP8BS_DEVERR_INDEX and chooses nothing. A token without experts gets y = 0. A token's x may be
+ * anything, that is seen in its own y alone; w2 and s2 of the chosen experts have to be finite (a
+ * code that is NaN reaches every token of the call).
  *
  *   x bf16 [T, D]; ids int32 [T, top_k]; weights fp32 [T, top_k]; y bf16 [T, D].
  *   w13 e4m3 [experts, 2 I, D]: the I gate rows, then the I up rows; s13 fp32 [experts, 2I/128, D/128].
