@@ -386,11 +386,28 @@ def gemm_workspace(device=None, stream=None):
     return ws
 
 
+def _auto_workspace(device, M, N, K, fmt):
+    """The workspace of a call that leaves it to us: gemm_workspace's, or in a call that is being
+    captured one of its own from the graph's memory, with the counters zeroed by the graph (they
+    stand first; the partials behind them are written before they are read). A graph may be
+    replayed beside others that were captured on the same stream, and a cached workspace must not
+    wait for a replay for its zeros. None where the call would not use one."""
+    import torch
+    if not torch.cuda.is_current_stream_capturing():
+        return gemm_workspace(device)
+    if 0 in (M, N, K) or K % BLOCK or not fp8bs_gemm_plan(M, N, K, fmt, True)["stream_k"]:
+        return None
+    ws = torch.empty(fp8bs_gemm_workspace_size(), dtype=torch.uint8, device=device)
+    ws[:4096].zero_()
+    return ws
+
+
 def fp8_gemm(a, a_s, b, b_s, scale_fmt="fp32", out=None, weights_constant=False,
              workspace="auto"):
     """C[M,N] bf16 = A[M,K] . B[N,K]^T with per-128-K-block scales a_s [M,K/128] and
-    b_s [ceil(N/128), K/128]. workspace: "auto" (a cached one per device and stream), None (no
-    split K loops) or a zero-filled uint8 CUDA tensor of fp8bs_gemm_workspace_size() bytes."""
+    b_s [ceil(N/128), K/128]. workspace: "auto" (a cached one per device and stream; the
+    graph's own in a call that is being captured), None (no split K loops) or a zero-filled uint8
+    CUDA tensor of fp8bs_gemm_workspace_size() bytes."""
     import torch
     _require(a, torch.float8_e4m3fn, 2, "a")
     _require(b, torch.float8_e4m3fn, 2, "b")
@@ -403,7 +420,7 @@ def fp8_gemm(a, a_s, b, b_s, scale_fmt="fp32", out=None, weights_constant=False,
         raise ValueError("operand or scale shapes do not match")
     c = _output(out, (M, N), a.device)
     if isinstance(workspace, str) and workspace == "auto":
-        workspace = gemm_workspace(a.device)
+        workspace = _auto_workspace(a.device, M, N, K, _fmt(scale_fmt))
     ws_ptr, ws_bytes = _workspace_args(workspace)
     fp8bs_gemm_ws(a.data_ptr(), a_s.data_ptr(), b.data_ptr(), b_s.data_ptr(), c.data_ptr(),
                   M, N, K, _fmt(scale_fmt), GEMM_WEIGHTS_CONSTANT if weights_constant else 0,
@@ -428,7 +445,7 @@ def act_quant_gemm(x, b, b_s, scale_fmt="fp32", weights_constant=False, workspac
     s = torch.empty((M, K // BLOCK), dtype=torch.float32, device=b.device)
     c = _output(out, (M, N), b.device)
     if isinstance(workspace, str) and workspace == "auto":
-        workspace = gemm_workspace(b.device)
+        workspace = _auto_workspace(b.device, M, N, K, _fmt(scale_fmt))
     ws_ptr, ws_bytes = _workspace_args(workspace)
     flags = (GEMM_WEIGHTS_CONSTANT if weights_constant else 0) | \
         (GEMM_QUANT_IN_KERNEL if quant_in_kernel else 0)
