@@ -20,8 +20,8 @@
 // while the tensor core works on the other; NQ = 1 with two S buffers for few rows.
 //
 // Chunks are bound by the tensor core and what feeds it: 4096 new tokens over 8192 keys, 32 query and 8 key heads
-// of 128 channels, 412 GFLOP that count, take 282 us = 1.46 PFLOP/s (0.75 of a library product's rate). The tensor
-// pipe is busy for 61 % of an SM's cycles and waits for the softmax the rest: a row of S is 128 exponentials, and
+// of 128 channels, 412 GFLOP that count, take 282 us = 1.46 PFLOP/s (0.75 of a library product's rate; 298 us where the
+// inputs come from HBM in every call). The tensor pipe is busy for 61 % of an SM's cycles and waits for the softmax the rest: a row of S is 128 exponentials, and
 // the products with K, whose operands both come from shared memory, run at 80 instead of 64 cycles. Heads of 192 + 128
 // channels take tiles of 96 keys (128 would leave room for one tile of values: 59 us instead of 56 for 2 chunks of
 // 777 over 2500 keys, 16 heads).

@@ -8,8 +8,8 @@
 // lanes. The token's cosines and sines are read once into registers and serve all its heads.
 //
 // Measured: 8192 tokens of 32 + 8 + 8 heads of 128 channels, norm and rotation, keys and values into the cache,
-// 34 us for 205 MB = 6.0 TB/s (0.90 of a copy's rate); 1000 tokens of 16 heads of 192 channels 6.7 us; five tokens
-// 2.6 us, a launch and two dependent loads.
+// 34 us for 205 MB = 6.0 TB/s (0.90 of a copy's rate), 37 us on inputs that change from call to call; 1000 tokens of 16
+// heads of 192 channels 6.7 us, 9.1 where they come from HBM; five tokens 2.7 us, a launch and two dependent loads.
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
