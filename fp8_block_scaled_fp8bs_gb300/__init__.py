@@ -18,14 +18,18 @@ Raw entry points (same names and arguments as the C functions; pointers are ints
     fp8bs_device_error(clear=True, stream=0) -> int
     fp8bs_probe_wait_timeout(timeout_ns, stream)
     fp8bs_qk_norm_rope(args, stream), fp8bs_paged_attention(args, stream),
+    fp8bs_qk_norm_rope_fp8(args, k_scale, v_scale, stream),
+    fp8bs_paged_attention_fp8(args, k_scale, v_scale, stream), fp8bs_rms_norm(args, stream),
     fp8bs_moe_route / _experts / _layer: argument structures QkNormRopeArgs, PagedAttentionArgs,
-        MoeRouting with the C structures' fields
+        RmsNormArgs, MoeRouting with the C structures' fields
 Tensor conveniences (PyTorch CUDA tensors; outputs allocated with torch):
     act_quant(x, scale_fmt="fp32") -> (y, s)      ("DeepSeek-V3 Administrator & Developer
     weight_dequant(w, s) -> y                        Guide", §8.5.1, §8.5.2, §8.5.3)
     fp8_gemm(a, a_s, b, b_s, scale_fmt="fp32") -> c
     fp8_gemm_grouped(a, a_s, b, b_s, row_offsets, scale_fmt="fp32") -> c
-    qk_norm_rope(q, k, cos, sin, positions, ...) -> q (and k, or the keys and values in a PagedCache)
+    rms_norm(x, weight, ...) -> NormOut(y, s, n, h)
+    qk_norm_rope(q, k, cos, sin, positions, ...) -> q (and k, or the keys and values in a PagedCache or
+        PagedCacheFp8)
     paged_attention(q, cache, page_table, q_start, kv_len, ...) -> out (and lse)
     moe_route(x, router_w, ...) -> (weights, ids)      ("DeepSeek-V3 Administrator & Developer
     moe_experts(x, weights, ids, w13, s13, w2, s2) -> y    Guide", §6.4)
@@ -60,6 +64,8 @@ EXPORTS = ("fp8bs_act_quant", "fp8bs_weight_dequant", "fp8bs_gemm", "fp8bs_gemm_
            "fp8bs_act_quant_gemm", "fp8bs_linear_bf16",
            "fp8bs_gemm_grouped",
            "fp8bs_qk_norm_rope", "fp8bs_paged_attention", "fp8bs_paged_attention_workspace_size",
+           "fp8bs_qk_norm_rope_fp8", "fp8bs_paged_attention_fp8",
+           "fp8bs_paged_attention_fp8_workspace_size", "fp8bs_rms_norm",
            "fp8bs_moe_route", "fp8bs_moe_experts", "fp8bs_moe_layer", "fp8bs_moe_workspace_size",
            "fp8bs_status_string", "fp8bs_device_error", "fp8bs_probe_wait_timeout",
            "fp8bs_probe_occupy")
@@ -89,6 +95,10 @@ PagedAttentionArgs = _structure(
     q_head_stride=_i64, cache=KvCache, page_table=_vp, table_stride=_i64, q_start=_vp, kv_len=_vp,
     out=_vp, lse=_vp, B=_i64, T=_i64, q_heads=_i64, max_q_len=_i64, max_kv_len=_i64, window=_i64,
     causal=ctypes.c_int, scale=ctypes.c_float, workspace=_vp, workspace_bytes=ctypes.c_size_t)
+RmsNormArgs = _structure(
+    "RmsNormArgs", "fp8bs_rms_norm_args", x=_vp, residual=_vp, weight=_vp, residual_out=_vp,
+    norm_out=_vp, y=_vp, s=_vp, x_stride=_i64, residual_stride=_i64, T=_i64, D=_i64,
+    scale_fmt=ctypes.c_int, eps=ctypes.c_float)
 MoeRouting = _structure(
     "MoeRouting", "fp8bs_moe_routing", router_w=_vp, bias=_vp, top_k=_i64, groups=_i64,
     topk_groups=_i64, score=ctypes.c_int, normalise=ctypes.c_int, route_scale=ctypes.c_float)
@@ -134,6 +144,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.fp8bs_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), vp]
         lib.fp8bs_paged_attention_workspace_size.argtypes = [ctypes.POINTER(PagedAttentionArgs),
                                                              ctypes.POINTER(ctypes.c_size_t)]
+        lib.fp8bs_qk_norm_rope_fp8.argtypes = [ctypes.POINTER(QkNormRopeArgs), vp, vp, vp]
+        lib.fp8bs_paged_attention_fp8.argtypes = [ctypes.POINTER(PagedAttentionArgs), vp, vp, vp]
+        lib.fp8bs_paged_attention_fp8_workspace_size.argtypes = [ctypes.POINTER(PagedAttentionArgs),
+                                                                 ctypes.POINTER(ctypes.c_size_t)]
+        lib.fp8bs_rms_norm.argtypes = [ctypes.POINTER(RmsNormArgs), vp]
         lib.fp8bs_moe_workspace_size.argtypes = [i64] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
         lib.fp8bs_moe_route.argtypes = [vp, ctypes.POINTER(MoeRouting), vp, vp, i64, i64, i64, vp]
         lib.fp8bs_moe_experts.argtypes = [vp] * 8 + [i64] * 5 + [i32, vp, ctypes.c_size_t, vp]
@@ -242,6 +257,27 @@ def fp8bs_paged_attention_workspace_size(args: PagedAttentionArgs) -> int:
     _check("fp8bs_paged_attention_workspace_size",
            load().fp8bs_paged_attention_workspace_size(ctypes.byref(args), ctypes.byref(out)))
     return out.value
+
+
+def fp8bs_qk_norm_rope_fp8(args: QkNormRopeArgs, k_scale, v_scale, stream=0) -> None:
+    _check("fp8bs_qk_norm_rope_fp8",
+           load().fp8bs_qk_norm_rope_fp8(ctypes.byref(args), k_scale, v_scale, stream))
+
+
+def fp8bs_paged_attention_fp8(args: PagedAttentionArgs, k_scale, v_scale, stream=0) -> None:
+    _check("fp8bs_paged_attention_fp8",
+           load().fp8bs_paged_attention_fp8(ctypes.byref(args), k_scale, v_scale, stream))
+
+
+def fp8bs_paged_attention_fp8_workspace_size(args: PagedAttentionArgs) -> int:
+    out = ctypes.c_size_t(0)
+    _check("fp8bs_paged_attention_fp8_workspace_size",
+           load().fp8bs_paged_attention_fp8_workspace_size(ctypes.byref(args), ctypes.byref(out)))
+    return out.value
+
+
+def fp8bs_rms_norm(args: RmsNormArgs, stream=0) -> None:
+    _check("fp8bs_rms_norm", load().fp8bs_rms_norm(ctypes.byref(args), stream))
 
 
 def fp8bs_moe_workspace_size(T, D, I, experts, top_k) -> int:
@@ -503,6 +539,25 @@ class PagedCache(NamedTuple):
     v: Any
 
 
+class PagedCacheFp8(NamedTuple):
+    """The same in 8 bits: e4m3 codes k [pages, page_size, heads, dk] and v [pages, page_size, heads, dv]
+    (page_size and the strides multiples of 16), each page and head with one scale, fp32 [pages, heads]:
+    a code stands for code * scale. The scales are powers of two that qk_norm_rope writes and lets grow
+    with the page; zeros say that a page holds nothing yet."""
+    k: Any
+    v: Any
+    k_scale: Any
+    v_scale: Any
+
+
+class NormOut(NamedTuple):
+    """What rms_norm gives; None in the place of what was not asked for."""
+    y: Any      # e4m3 [T, D]
+    s: Any      # fp32 [T, D/128]
+    n: Any      # bf16 [T, D]
+    h: Any      # bf16 [T, D], x + residual
+
+
 HOST_PATH = os.path.join(_HERE, "_host.so")
 _host = None
 
@@ -526,12 +581,25 @@ def _load_host():
     return _host
 
 
+def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, norm=None, residual_out=None):
+    """RMS norm of x bf16 [T, D] (D a multiple of 128; rows may be strided) with weight bf16 [D], and what
+    stands around it between two products, in one pass -> NormOut(y, s, n, h):
+    h = x + residual (bf16 [T, D]; into residual_out, which may be x or the residual itself), which then is
+    what is normalised; n, the norm in bf16, where no codes are asked for or norm is true; y and s, with
+    quant "fp32" or "ue8m0", the norm's e4m3 codes and scales as act_quant's, from unrounded n."""
+    if quant is not None:
+        quant = _fmt(quant)
+    return NormOut(*(_host or _load_host()).rms_norm(x, weight, eps, residual, quant, norm, residual_out))
+
+
 def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, rot_start=0,
                  interleaved=False, cache=None, v=None, slots=None, out=None):
     """RMS norm per head (where a weight is given) and rotation of q bf16 [T, Hq, D] and k bf16
     [T, Hk, D] by positions int32 [T]; cos, sin fp32 [max_positions, R/2] rotate the channels
     rot_start .. rot_start+R-1. With a PagedCache, the keys and v bf16 [T, Hk, Dv] go to its slots
-    int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k)."""
+    int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k). With a
+    PagedCacheFp8 they are held as codes; the tokens that go to one page stand next to one another, in
+    rising slots, and a token in a page's slot 0 begins it anew."""
     return (_host or _load_host()).qk_norm_rope(q, k, cos, sin, positions, q_weight, k_weight, eps, rot_start,
                                                 interleaved, cache, v, slots, out)
 
@@ -539,7 +607,7 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
 def paged_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=True, window=0,
                     max_q_len=None, max_kv_len=None, out=None, return_lse=False):
     """Attention of the new tokens q bf16 [T, Hq, Dk] of B sequences (sequence b: rows q_start[b] ..
-    q_start[b+1]-1) over a PagedCache that holds their kv_len[b] keys, their own included, in the
+    q_start[b+1]-1) over a PagedCache or PagedCacheFp8 that holds their kv_len[b] keys, their own included, in the
     pages page_table[b] (int32 [B, n]) -> out bf16 [T, Hq, Dv] (and lse fp32 [T, Hq]). q_start int32
     [B+1] and kv_len int32 [B] are on the GPU; max_q_len and max_kv_len bound them for the host
     (default: T, and what the table can hold; tighter is faster). window > 0: each query sees that

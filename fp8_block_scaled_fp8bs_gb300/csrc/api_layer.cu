@@ -12,25 +12,25 @@ bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0
 
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 
-// A stride that keeps rows on 16-byte boundaries.
-bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+// A stride that keeps rows on 16-byte boundaries, `unit` elements of them.
+bool stride_ok(int64_t s, int64_t unit = 8) { return s >= 0 && s % unit == 0; }
 
-// Sizes and strides of a cache; pointers of k (and, with values, v).
-int check_cache(const fp8bs_kv_cache& c, bool values) {
+// Sizes and strides of a cache; pointers of k (and, with values, v). unit: elements in 16 bytes.
+int check_cache(const fp8bs_kv_cache& c, bool values, int64_t unit = 8) {
     if (c.pages < 0 || c.page_size < 1 || c.heads < 1 || c.heads >= (1 << 16) ||
         c.page_size >= kMaxDim || c.pages >= kMaxDim)
         return FP8BS_ERR_INVALID_ARG;
-    if (!stride_ok(c.k_page_stride) || !stride_ok(c.k_slot_stride) || !stride_ok(c.k_head_stride))
+    if (!stride_ok(c.k_page_stride, unit) || !stride_ok(c.k_slot_stride, unit) || !stride_ok(c.k_head_stride, unit))
         return FP8BS_ERR_INVALID_ARG;
     if (values &&
-        (!stride_ok(c.v_page_stride) || !stride_ok(c.v_slot_stride) || !stride_ok(c.v_head_stride)))
+        (!stride_ok(c.v_page_stride, unit) || !stride_ok(c.v_slot_stride, unit) || !stride_ok(c.v_head_stride, unit)))
         return FP8BS_ERR_INVALID_ARG;
     // rows must not lie on one another
-    if ((c.pages > 1 && c.k_page_stride < 8) || (c.page_size > 1 && c.k_slot_stride < 8) ||
-        (c.heads > 1 && c.k_head_stride < 8))
+    if ((c.pages > 1 && c.k_page_stride < unit) || (c.page_size > 1 && c.k_slot_stride < unit) ||
+        (c.heads > 1 && c.k_head_stride < unit))
         return FP8BS_ERR_INVALID_ARG;
-    if (values && ((c.pages > 1 && c.v_page_stride < 8) || (c.page_size > 1 && c.v_slot_stride < 8) ||
-                   (c.heads > 1 && c.v_head_stride < 8)))
+    if (values && ((c.pages > 1 && c.v_page_stride < unit) || (c.page_size > 1 && c.v_slot_stride < unit) ||
+                   (c.heads > 1 && c.v_head_stride < unit)))
         return FP8BS_ERR_INVALID_ARG;
     if (c.pages > 0 && (!c.k || (values && !c.v))) return FP8BS_ERR_INVALID_ARG;
     if (!aligned16(c.k) || (values && !aligned16(c.v))) return FP8BS_ERR_MISALIGNED;
@@ -39,9 +39,18 @@ int check_cache(const fp8bs_kv_cache& c, bool values) {
 
 }  // namespace
 
-extern "C" int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stream) {
-    if (!args) return FP8BS_ERR_INVALID_ARG;
-    fp8bs_qk_norm_rope_args a = *args;
+namespace {
+
+// A cache of codes: its sizes, strides and pages of whole boxes.
+int check_cache_fp8(const fp8bs_kv_cache& c) {
+    const int rc = check_cache(c, true, 16);
+    if (rc != FP8BS_ERR_INVALID_ARG && c.page_size % 16) return FP8BS_ERR_INVALID_ARG;
+    return rc;
+}
+
+// fp8bs_qk_norm_rope and, with scales, fp8bs_qk_norm_rope_fp8.
+int qk_norm_rope(const fp8bs_qk_norm_rope_args& args, bool fp8, float* k_scale, float* v_scale, void* stream) {
+    fp8bs_qk_norm_rope_args a = args;
     if (!a.v) a.cache.dv = a.cache.dk;
     const int64_t dk = a.cache.dk, dv = a.cache.dv;
     if (a.T < 0 || a.T >= kMaxDim || a.q_heads < 0 || a.q_heads >= (1 << 16))
@@ -54,21 +63,61 @@ extern "C" int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* str
     if (!stride_ok(a.q_token_stride) || !stride_ok(a.q_head_stride) || !stride_ok(a.k_token_stride) ||
         !stride_ok(a.k_head_stride) || (a.v && (!stride_ok(a.v_token_stride) || !stride_ok(a.v_head_stride))))
         return FP8BS_ERR_INVALID_ARG;
-    const int rc = check_cache(a.cache, a.v != nullptr);
+    const int rc = fp8 ? check_cache_fp8(a.cache) : check_cache(a.cache, a.v != nullptr);
     if (rc == FP8BS_ERR_INVALID_ARG) return rc;
+    // (a block per token, and one per head and token that may begin a page)
+    if (fp8 && a.T * (a.cache.heads + 1) >= kMaxDim) return FP8BS_ERR_INVALID_ARG;
     if (a.T == 0) return FP8BS_OK;
+    if (fp8 && (!a.v || !a.slots || !k_scale || !v_scale)) return FP8BS_ERR_INVALID_ARG;
     if (!a.k || !a.positions || (a.q_heads > 0 && (!a.q || !a.q_out)) ||
         (a.rot_dim > 0 && (!a.cos || !a.sin)))
         return FP8BS_ERR_INVALID_ARG;
     if (rc != FP8BS_OK) return rc;
     if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_out) ||
         !aligned16(a.q_weight) || !aligned16(a.k_weight) || !aligned4(a.cos) || !aligned4(a.sin) ||
-        !aligned4(a.positions) || !aligned8(a.slots))
+        !aligned4(a.positions) || !aligned8(a.slots) || !aligned4(k_scale) || !aligned4(v_scale))
         return FP8BS_ERR_MISALIGNED;
     int sms = 0;
     const int dev = check_device(&sms);
     if (dev != FP8BS_OK) return dev;
-    return status_of(fp8bs::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+    return status_of(fp8 ? fp8bs::launch_qk_norm_rope_fp8(a, k_scale, v_scale, static_cast<cudaStream_t>(stream))
+                         : fp8bs::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" int fp8bs_qk_norm_rope(const fp8bs_qk_norm_rope_args* args, void* stream) {
+    if (!args) return FP8BS_ERR_INVALID_ARG;
+    return qk_norm_rope(*args, false, nullptr, nullptr, stream);
+}
+
+extern "C" int fp8bs_qk_norm_rope_fp8(const fp8bs_qk_norm_rope_args* args, float* k_scale, float* v_scale,
+                                      void* stream) {
+    if (!args) return FP8BS_ERR_INVALID_ARG;
+    return qk_norm_rope(*args, true, k_scale, v_scale, stream);
+}
+
+extern "C" int fp8bs_rms_norm(const fp8bs_rms_norm_args* args, void* stream) {
+    if (!args) return FP8BS_ERR_INVALID_ARG;
+    const fp8bs_rms_norm_args& a = *args;
+    if (a.T < 0 || a.T >= kMaxDim || a.D < FP8BS_BLOCK || a.D > 16384 || a.D % FP8BS_BLOCK)
+        return FP8BS_ERR_INVALID_ARG;
+    if (!stride_ok(a.x_stride) || (a.residual && !stride_ok(a.residual_stride))) return FP8BS_ERR_INVALID_ARG;
+    if (a.scale_fmt != FP8BS_SCALE_FP32 && a.scale_fmt != FP8BS_SCALE_UE8M0) return FP8BS_ERR_INVALID_ARG;
+    if (a.T == 0) return FP8BS_OK;
+    if (!a.x || !a.weight || !a.residual != !a.residual_out || !a.y != !a.s || (!a.norm_out && !a.y))
+        return FP8BS_ERR_INVALID_ARG;
+    // in place: rows over themselves alone
+    if (a.residual && ((a.residual_out == a.x && a.x_stride != a.D) ||
+                       (a.residual_out == a.residual && a.residual_stride != a.D)))
+        return FP8BS_ERR_INVALID_ARG;
+    if (!aligned16(a.x) || !aligned16(a.residual) || !aligned16(a.weight) || !aligned16(a.residual_out) ||
+        !aligned16(a.norm_out) || !aligned16(a.y) || !aligned4(a.s))
+        return FP8BS_ERR_MISALIGNED;
+    int sms = 0;
+    const int dev = check_device(&sms);
+    if (dev != FP8BS_OK) return dev;
+    return status_of(fp8bs::launch_rms_norm(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -150,6 +199,21 @@ extern "C" int fp8bs_paged_attention_workspace_size(const fp8bs_paged_attention_
     return FP8BS_OK;
 }
 
+namespace {
+
+// What a paged_attention call must not have, after its sizes; `cache`: what its cache's check said. T > 0.
+int check_attention_pointers(const fp8bs_paged_attention_args& a, int cache) {
+    if (!a.q || !a.q_start || !a.kv_len || !a.out || (a.max_kv_len > 0 && !a.page_table))
+        return FP8BS_ERR_INVALID_ARG;
+    if (cache != FP8BS_OK) return cache;
+    if (!aligned16(a.q) || !aligned16(a.out) || !aligned4(a.lse) || !aligned4(a.page_table) ||
+        !aligned4(a.q_start) || !aligned4(a.kv_len) || !aligned16(a.workspace))
+        return FP8BS_ERR_MISALIGNED;
+    return FP8BS_OK;
+}
+
+}  // namespace
+
 extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, void* stream) {
     if (!args) return FP8BS_ERR_INVALID_ARG;
     int rc = check_attention_sizes(*args);
@@ -159,12 +223,8 @@ extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, voi
     rc = check_cache(a.cache, true);
     if (rc == FP8BS_ERR_INVALID_ARG || a.cache.pages < 1) return FP8BS_ERR_INVALID_ARG;
     if (a.T == 0) return FP8BS_OK;
-    if (!a.q || !a.q_start || !a.kv_len || !a.out || (a.max_kv_len > 0 && !a.page_table))
-        return FP8BS_ERR_INVALID_ARG;
+    rc = check_attention_pointers(a, rc);
     if (rc != FP8BS_OK) return rc;
-    if (!aligned16(a.q) || !aligned16(a.out) || !aligned4(a.lse) || !aligned4(a.page_table) ||
-        !aligned4(a.q_start) || !aligned4(a.kv_len) || !aligned16(a.workspace))
-        return FP8BS_ERR_MISALIGNED;
     int sms = 0;
     rc = check_device(&sms);
     if (rc != FP8BS_OK) return rc;
@@ -181,6 +241,37 @@ extern "C" int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, voi
         return FP8BS_ERR_CUDA;
     return status_of(fp8bs::launch_paged_attention(tmK, tmV, a, modes, plan, sms,
                                                    static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fp8bs_paged_attention_fp8_workspace_size(const fp8bs_paged_attention_args* args, size_t* bytes) {
+    if (!args || !bytes) return FP8BS_ERR_INVALID_ARG;
+    const int rc = check_attention_sizes(*args);
+    if (rc != FP8BS_OK) return rc;
+    int sms = 0;
+    const int dev = check_device(&sms);
+    if (dev != FP8BS_OK) return dev;
+    *bytes = 0;
+    return FP8BS_OK;
+}
+
+extern "C" int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args, const float* k_scale,
+                                         const float* v_scale, void* stream) {
+    if (!args) return FP8BS_ERR_INVALID_ARG;
+    int rc = check_attention_sizes(*args);
+    if (rc != FP8BS_OK) return rc;
+    const fp8bs_paged_attention_args a = without_idle_window(*args);
+    if (!stride_ok(a.q_token_stride) || !stride_ok(a.q_head_stride)) return FP8BS_ERR_INVALID_ARG;
+    rc = check_cache_fp8(a.cache);
+    if (rc == FP8BS_ERR_INVALID_ARG || a.cache.pages < 1) return FP8BS_ERR_INVALID_ARG;
+    if (a.T == 0) return FP8BS_OK;
+    if (!k_scale || !v_scale) return FP8BS_ERR_INVALID_ARG;
+    rc = check_attention_pointers(a, rc);
+    if (rc != FP8BS_OK) return rc;
+    if (!aligned4(k_scale) || !aligned4(v_scale)) return FP8BS_ERR_MISALIGNED;
+    int sms = 0;
+    rc = check_device(&sms);
+    if (rc != FP8BS_OK) return rc;
+    return status_of(fp8bs::launch_paged_attention_fp8(a, k_scale, v_scale, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

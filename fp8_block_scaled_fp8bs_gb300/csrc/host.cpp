@@ -37,13 +37,17 @@ struct Raised {};      // a Python exception is set already
 
 PyObject* g_error_class = nullptr;      // Fp8bsError(function, status)
 
-#define FP8BS_FUNCTIONS(X)            \
-    X(qk_norm_rope)                   \
-    X(paged_attention)                \
-    X(paged_attention_workspace_size) \
-    X(moe_route)                      \
-    X(moe_experts)                    \
-    X(moe_layer)                      \
+#define FP8BS_FUNCTIONS(X)                \
+    X(rms_norm)                           \
+    X(qk_norm_rope)                       \
+    X(qk_norm_rope_fp8)                   \
+    X(paged_attention)                    \
+    X(paged_attention_workspace_size)     \
+    X(paged_attention_fp8)                \
+    X(paged_attention_fp8_workspace_size) \
+    X(moe_route)                          \
+    X(moe_experts)                        \
+    X(moe_layer)                          \
     X(moe_workspace_size)
 #define FP8BS_POINTER(name) decltype(&fp8bs_##name) p_##name = nullptr;
 FP8BS_FUNCTIONS(FP8BS_POINTER)
@@ -87,9 +91,10 @@ void check_tensor(const at::Tensor& t, at::ScalarType type, int64_t ndim, const 
         value_error(std::string(name) + " must be on cuda:" + std::to_string(dev) + ", like the other tensors");
 }
 
-const at::Tensor& rows(PyObject* o, int64_t ndim, const char* name, int dev = -1) {
+const at::Tensor& rows(PyObject* o, int64_t ndim, const char* name, int dev = -1,
+                       at::ScalarType type = at::kBFloat16) {
     const at::Tensor& t = tensor(o, name);
-    check_tensor(t, at::kBFloat16, ndim, name, dev);
+    check_tensor(t, type, ndim, name, dev);
     if (t.size(ndim - 1) > 1 && t.stride(ndim - 1) != 1)
         value_error(std::string(name) + " must have contiguous rows");
     return t;
@@ -128,39 +133,55 @@ bool truth(PyObject* o) {
 }
 
 // The output: new, or the caller's, a contiguous bf16 tensor of exactly this shape, on the GPU or pinned.
-at::Tensor output(PyObject* out, at::IntArrayRef shape, const at::Tensor& like) {
+at::Tensor output(PyObject* out, at::IntArrayRef shape, const at::Tensor& like, const char* name = "out") {
     if (none(out)) return at::empty(shape, like.options().dtype(at::kBFloat16));
-    const at::Tensor& t = tensor(out, "out");
-    if (!t.is_cuda() && !t.is_pinned()) type_error("out must be a CUDA tensor or a pinned host tensor");
-    if (t.scalar_type() != at::kBFloat16) type_error("out must be torch.bfloat16, got " + type_name(t.scalar_type()));
+    const at::Tensor& t = tensor(out, name);
+    if (!t.is_cuda() && !t.is_pinned())
+        type_error(std::string(name) + " must be a CUDA tensor or a pinned host tensor");
+    if (t.scalar_type() != at::kBFloat16)
+        type_error(std::string(name) + " must be torch.bfloat16, got " + type_name(t.scalar_type()));
     if (!t.is_contiguous() || t.sizes() != shape) {
         std::string want;
         for (int64_t n : shape) want += (want.empty() ? "" : ", ") + std::to_string(n);
-        value_error("out must be contiguous, of shape (" + want + ")");
+        value_error(std::string(name) + " must be contiguous, of shape (" + want + ")");
     }
-    if (t.is_cuda() && t.get_device() != like.get_device()) value_error("out must be on the device of the inputs");
+    if (t.is_cuda() && t.get_device() != like.get_device())
+        value_error(std::string(name) + " must be on the device of the inputs");
     return t;
 }
 
 struct Cache {
     fp8bs_kv_cache c;
+    bool fp8 = false;                                  // codes, with scales
+    float *k_scale = nullptr, *v_scale = nullptr;
 };
 
-// A PagedCache (k, v).
+// A PagedCache (k, v) or PagedCacheFp8 (k, v, k_scale, v_scale).
 Cache cache_of(PyObject* o, int dev) {
-    PyObject* items = PySequence_Fast(o, "cache must be a PagedCache");
+    PyObject* items = PySequence_Fast(o, "cache must be a PagedCache or a PagedCacheFp8");
     if (!items) throw Raised{};
     struct Hold {
         PyObject* p;
         ~Hold() { Py_DECREF(p); }
     } hold{items};
-    if (PySequence_Fast_GET_SIZE(items) != 2) type_error("cache must be a PagedCache");
-    const at::Tensor& k = rows(PySequence_Fast_GET_ITEM(items, 0), 4, "cache.k", dev);
-    const at::Tensor& v = rows(PySequence_Fast_GET_ITEM(items, 1), 4, "cache.v", dev);
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(items);
+    if (n != 2 && n != 4) type_error("cache must be a PagedCache or a PagedCacheFp8");
+    const at::ScalarType type = n == 4 ? at::kFloat8_e4m3fn : at::kBFloat16;
+    const at::Tensor& k = rows(PySequence_Fast_GET_ITEM(items, 0), 4, "cache.k", dev, type);
+    const at::Tensor& v = rows(PySequence_Fast_GET_ITEM(items, 1), 4, "cache.v", dev, type);
     if (k.size(0) != v.size(0) || k.size(1) != v.size(1) || k.size(2) != v.size(2))
         value_error("cache.k and cache.v must have the same pages, page size and heads");
-    return Cache{{k.data_ptr(), v.data_ptr(), k.size(0), k.size(1), k.size(2), k.size(3), v.size(3), k.stride(0),
-                  k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2)}};
+    Cache cache{{k.data_ptr(), v.data_ptr(), k.size(0), k.size(1), k.size(2), k.size(3), v.size(3), k.stride(0),
+                 k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2)}};
+    cache.fp8 = n == 4;
+    if (cache.fp8)
+        for (int i = 0; i < 2; ++i) {
+            const char* name = i == 0 ? "cache.k_scale" : "cache.v_scale";
+            const at::Tensor& s = dense(PySequence_Fast_GET_ITEM(items, 2 + i), at::kFloat, 2, name, dev);
+            check_shape(s, {k.size(0), k.size(2)}, name, "[pages, heads]");
+            (i == 0 ? cache.k_scale : cache.v_scale) = s.data_ptr<float>();
+        }
+    return cache;
 }
 
 // ------------------------------------------------------------------------------ workspaces
@@ -185,6 +206,58 @@ void* current_stream(int dev) { return c10::cuda::getCurrentCUDAStream(static_ca
 
 // ------------------------------------------------------------------------------ the operators
 
+// x, weight, eps, residual, quant (None, 0 or 1), norm (None or a truth value), residual_out
+//   -> (y, s, n, h), None in the place of what was not asked for
+PyObject* rms_norm(PyObject* const* x) {
+    const at::Tensor& t = rows(x[0], 2, "x");
+    const int dev = t.get_device();
+    fp8bs_rms_norm_args a = {};
+    a.x = t.data_ptr();
+    a.x_stride = t.stride(0);
+    a.T = t.size(0);
+    a.D = t.size(1);
+    const at::Tensor& w = dense(x[1], at::kBFloat16, 1, "weight", dev);
+    check_shape(w, {a.D}, "weight", "[D]");
+    a.weight = w.data_ptr();
+    a.eps = static_cast<float>(real(x[2]));
+    if (a.D % FP8BS_BLOCK) value_error("x must have a multiple of 128 channels");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+    at::Tensor out[4];                 // y, s, n, h
+    if (!none(x[3])) {
+        const at::Tensor& r = rows(x[3], 2, "residual", dev);
+        check_shape(r, {a.T, a.D}, "residual", "[T, D] of x");
+        a.residual = r.data_ptr();
+        a.residual_stride = r.stride(0);
+        out[3] = output(x[6], {a.T, a.D}, t, "residual_out");
+        if (!out[3].is_cuda()) type_error("residual_out must be a CUDA tensor");
+        a.residual_out = out[3].data_ptr();
+    } else if (!none(x[6])) {
+        value_error("residual_out needs a residual");
+    }
+    const bool quant = !none(x[4]);
+    if (quant) {
+        a.scale_fmt = static_cast<int>(integer(x[4]));
+        out[0] = at::empty({a.T, a.D}, t.options().dtype(at::kFloat8_e4m3fn));
+        out[1] = at::empty({a.T, a.D / FP8BS_BLOCK}, t.options().dtype(at::kFloat));
+        a.y = out[0].data_ptr();
+        a.s = out[1].data_ptr<float>();
+    }
+    if (none(x[5]) ? !quant : truth(x[5])) {
+        out[2] = at::empty({a.T, a.D}, t.options());
+        a.norm_out = out[2].data_ptr();
+    } else if (!quant) {
+        value_error("nothing is asked for: quant or norm");
+    }
+    check_status("fp8bs_rms_norm", p_rms_norm(&a, current_stream(dev)));
+    PyObject* four = PyTuple_New(4);
+    if (!four) throw Raised{};
+    for (int i = 0; i < 4; ++i) {
+        if (!out[i].defined()) Py_INCREF(Py_None);
+        PyTuple_SET_ITEM(four, i, out[i].defined() ? THPVariable_Wrap(std::move(out[i])) : Py_None);
+    }
+    return four;
+}
+
 // q, k, cos, sin, positions, q_weight, k_weight, eps, rot_start, interleaved, cache, v, slots, out
 PyObject* qk_norm_rope(PyObject* const* x) {
     const at::Tensor& q = rows(x[0], 3, "q");
@@ -208,6 +281,7 @@ PyObject* qk_norm_rope(PyObject* const* x) {
     }
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
     at::Tensor k_out;
+    Cache cache{};
     if (none(x[10])) {
         if (!none(x[11]) || !none(x[12])) value_error("v and slots need a cache");
         k_out = at::empty({T, hk, d}, k.options());
@@ -215,7 +289,8 @@ PyObject* qk_norm_rope(PyObject* const* x) {
                    0, 0, 0};
     } else {
         if (none(x[11]) || none(x[12])) value_error("a cache needs v and slots");
-        a.cache = cache_of(x[10], dev).c;
+        cache = cache_of(x[10], dev);
+        a.cache = cache.c;
         const at::Tensor& v = rows(x[11], 3, "v", dev);
         if (a.cache.heads != hk || a.cache.dk != d) value_error("k does not match the cache's heads and channels");
         check_shape(v, {T, hk, a.cache.dv}, "v", "[T, heads, Dv] of k and the cache");
@@ -244,7 +319,11 @@ PyObject* qk_norm_rope(PyObject* const* x) {
     a.rot_dim = 2 * cos.size(1);
     a.interleaved = truth(x[9]) ? 1 : 0;
     a.eps = static_cast<float>(real(x[7]));
-    check_status("fp8bs_qk_norm_rope", p_qk_norm_rope(&a, current_stream(dev)));
+    if (cache.fp8)
+        check_status("fp8bs_qk_norm_rope_fp8",
+                     p_qk_norm_rope_fp8(&a, cache.k_scale, cache.v_scale, current_stream(dev)));
+    else
+        check_status("fp8bs_qk_norm_rope", p_qk_norm_rope(&a, current_stream(dev)));
     if (!k_out.defined()) return THPVariable_Wrap(std::move(out));
     PyObject* two = PyTuple_New(2);
     if (!two) throw Raised{};
@@ -258,7 +337,8 @@ PyObject* paged_attention(PyObject* const* x) {
     const at::Tensor& q = rows(x[0], 3, "q");
     const int dev = q.get_device();
     fp8bs_paged_attention_args a = {};
-    a.cache = cache_of(x[1], dev).c;
+    const Cache cache = cache_of(x[1], dev);
+    a.cache = cache.c;
     a.T = q.size(0);
     a.q_heads = q.size(1);
     if (q.size(2) != a.cache.dk || a.cache.heads < 1 || a.q_heads % a.cache.heads)
@@ -292,14 +372,17 @@ PyObject* paged_attention(PyObject* const* x) {
     a.max_kv_len = none(x[9]) ? a.table_stride * a.cache.page_size : integer(x[9]);
     void* stream = current_stream(dev);
     size_t need = 0;
-    check_status("fp8bs_paged_attention", p_paged_attention_workspace_size(&a, &need));
+    const bool fp8 = cache.fp8;
+    const char* function = fp8 ? "fp8bs_paged_attention_fp8" : "fp8bs_paged_attention";
+    check_status(function, (fp8 ? p_paged_attention_fp8_workspace_size : p_paged_attention_workspace_size)(&a, &need));
     at::Tensor work;                   // (held until the call is queued)
     if (need > 0) {
         work = scratch(dev, stream, need, q);
         a.workspace = work.data_ptr();
         a.workspace_bytes = work.nbytes();
     }
-    check_status("fp8bs_paged_attention", p_paged_attention(&a, stream));
+    check_status(function, fp8 ? p_paged_attention_fp8(&a, cache.k_scale, cache.v_scale, stream)
+                               : p_paged_attention(&a, stream));
     if (!lse.defined()) return THPVariable_Wrap(std::move(out));
     PyObject* two = PyTuple_New(2);
     if (!two) throw Raised{};
@@ -466,6 +549,7 @@ PyObject* init(PyObject*, PyObject* args) {
     {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<name, n>)), METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
+                         ENTRY(rms_norm, 7),
                          ENTRY(qk_norm_rope, 14),
                          ENTRY(paged_attention, 12),
                          ENTRY(moe_route, 9),

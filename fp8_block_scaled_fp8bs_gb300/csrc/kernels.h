@@ -186,6 +186,13 @@ cudaError_t launch_linear_bf16_swap(const CUtensorMap& tmW, const CUtensorMap& t
 // Query/key norm, rotation and cache write (fp8bs_qk_norm_rope); T >= 1.
 cudaError_t launch_qk_norm_rope(const fp8bs_qk_norm_rope_args& a, cudaStream_t stream);
 
+// The same into a cache of e4m3 codes (fp8bs_qk_norm_rope_fp8); T >= 1.
+cudaError_t launch_qk_norm_rope_fp8(const fp8bs_qk_norm_rope_args& a, float* k_scale, float* v_scale,
+                                    cudaStream_t stream);
+
+// Residual, RMS norm and codes (fp8bs_rms_norm); T >= 1.
+cudaError_t launch_rms_norm(const fp8bs_rms_norm_args& a, int num_sms, cudaStream_t stream);
+
 // Attention over a paged cache (fp8bs_paged_attention). attention_plan cuts the work from the
 // sizes in `a` alone; attention_workspace gives the bytes that the plan needs.
 struct AttentionPlan {
@@ -207,6 +214,10 @@ AttentionModes attention_modes(const fp8bs_kv_cache& c);
 cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                    const fp8bs_paged_attention_args& a, const AttentionModes& modes,
                                    const AttentionPlan& plan, int num_sms, cudaStream_t stream);
+
+// Attention over a paged cache of e4m3 codes (fp8bs_paged_attention_fp8).
+cudaError_t launch_paged_attention_fp8(const fp8bs_paged_attention_args& a, const float* k_scale, const float* v_scale,
+                                       cudaStream_t stream);
 
 // Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
 constexpr int kMoeMaxTokens = 64;
@@ -258,6 +269,8 @@ cudaError_t read_error_swapab(unsigned int* out, bool clear, cudaStream_t stream
 cudaError_t read_error_linear(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_norm_rope(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_attention(unsigned int* out, bool clear, cudaStream_t stream);
+cudaError_t read_error_norm_rope_fp8(unsigned int* out, bool clear, cudaStream_t stream);
+cudaError_t read_error_attention_fp8(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_moe(unsigned int* out, bool clear, cudaStream_t stream);
 
 }  // namespace fp8bs

@@ -10,82 +10,13 @@
 // Measured: 8192 tokens of 32 + 8 + 8 heads of 128 channels, norm and rotation, keys and values into the cache,
 // 34 us for 205 MB = 6.0 TB/s (0.90 of a copy's rate), 37 us on inputs that change from call to call; 1000 tokens of 16
 // heads of 192 channels 6.7 us, 9.1 where they come from HBM; five tokens 2.7 us, a launch and two dependent loads.
-#include "gemm_common.cuh"
-#include "quant_math.cuh"
+#include "norm_rows.cuh"
 
 namespace fp8bs {
 
 namespace {
 
 constexpr int NR_BATCH = 2;      // query rows a lane group loads before it computes either
-
-// A lane's 16 channels of a row as 8 pairs (the rotation's partners lie 8 apart: pair i of the first chunk with
-// pair i of the second).
-struct Chunk16 {
-    uint4 a, b;
-};
-
-__device__ __forceinline__ Chunk16 zero16() {
-    return Chunk16{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-}
-
-__device__ __forceinline__ void unpack16(const Chunk16& v, float2* f) {
-    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
-}
-
-__device__ __forceinline__ Chunk16 pack16(const float2* f) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[i].x, f[i].y);
-    return Chunk16{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
-}
-
-// What the rows of a token share.
-template <int LPR, bool INTERLEAVED>
-struct TokenRows {
-    float2 cs[4], sn[4];       // cosines and sines of the lane's 8 pairs
-    bool rotates, has;         // rotated chunks; any chunk of a q or k row
-    float eps, inv_d;
-
-    // Norm (w: the lane's weights, or null) and rotation of one row's chunks; every lane of the warp calls it.
-    __device__ __forceinline__ Chunk16 row(const Chunk16& x, const float2* w, bool norm) const {
-        float2 f[8];
-        unpack16(x, f);
-        if (norm) {
-            float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s2 = __ffma2_rn(f[i], f[i], s2);
-            float ss = s2.x + s2.y;
-#pragma unroll
-            for (int m = LPR / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            const float inv = rsqrtf(fmaf(ss, inv_d, eps));
-            const float2 i2 = make_float2(inv, inv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], i2), w[i]);
-        }
-        if (rotates) {
-            if constexpr (INTERLEAVED) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float c = i & 1 ? cs[i / 2].y : cs[i / 2].x;
-                    const float s = i & 1 ? sn[i / 2].y : sn[i / 2].x;
-                    f[i] = make_float2(f[i].x * c - f[i].y * s, f[i].x * s + f[i].y * c);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 u = f[i], y = f[4 + i];
-                    const float2 ns = make_float2(-sn[i].x, -sn[i].y);
-                    f[i] = __ffma2_rn(y, ns, __fmul2_rn(u, cs[i]));
-                    f[4 + i] = __ffma2_rn(u, sn[i], __fmul2_rn(y, cs[i]));
-                }
-            }
-        }
-        return pack16(f);
-    }
-};
 
 // MANY tokens (more than stay in L2 on their way to the attention): two warps per token, and the stream is marked
 // as not to be kept; else four warps, for the latency of the single token.
@@ -102,21 +33,12 @@ __global__ void __launch_bounds__(MANY ? 64 : 128, (INTERLEAVED ? 5 : 6) * (MANY
     const int hk = static_cast<int>(a.cache.heads);
     const int kv_rows = hk + (a.v ? hk : 0);
 
-    // This lane's chunks of a q or k row: rotated chunks come as pairs (the chunk, the one half the rotated range
-    // further on), the others in order.
     const int r0 = static_cast<int>(a.rot_start) / 8;
     const int nr = static_cast<int>(a.rot_dim) / 8;
     TokenRows<LPR, INTERLEAVED> rows;
     rows.rotates = p < nr / 2;
     int c0, c1;
-    if (rows.rotates) {
-        c0 = r0 + p;
-        c1 = c0 + nr / 2;
-    } else {
-        const int i = 2 * (p - nr / 2);
-        c0 = i < r0 ? i : i + nr;
-        c1 = i + 1 < r0 ? i + 1 : i + 1 + nr;
-    }
+    lane_chunks(p, r0, nr, &c0, &c1);
     rows.has = p < dk / 16;
     rows.eps = a.eps;
     rows.inv_d = 1.0f / static_cast<float>(dk);
@@ -157,20 +79,7 @@ __global__ void __launch_bounds__(MANY ? 64 : 128, (INTERLEAVED ? 5 : 6) * (MANY
     const bool store_kv = pos_ok && slot >= 0 && !slot_past;
     if (!store_kv) slot = 0;
     rows.rotates = rows.rotates && pos_ok;
-    if (rows.rotates) {
-        // pair 8p + i (halves), or the 4 pairs of each of the two chunks (interleaved)
-        const float* ct = a.cos + static_cast<int64_t>(pos) * (a.rot_dim / 2);
-        const float* st = a.sin + static_cast<int64_t>(pos) * (a.rot_dim / 2);
-        const int i0 = INTERLEAVED ? 4 * p : 8 * p;
-        const int i1 = INTERLEAVED ? 4 * (p + nr / 2) : 8 * p + 4;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            rows.cs[i] = make_float2(__ldg(ct + i0 + 2 * i), __ldg(ct + i0 + 2 * i + 1));
-            rows.sn[i] = make_float2(__ldg(st + i0 + 2 * i), __ldg(st + i0 + 2 * i + 1));
-            rows.cs[2 + i] = make_float2(__ldg(ct + i1 + 2 * i), __ldg(ct + i1 + 2 * i + 1));
-            rows.sn[2 + i] = make_float2(__ldg(st + i1 + 2 * i), __ldg(st + i1 + 2 * i + 1));
-        }
-    }
+    if (rows.rotates) rows.load_turn(a, pos, p, nr);
     float2 w[8];
     auto load_weight = [&](const void* from) {
         Chunk16 v16 = zero16();

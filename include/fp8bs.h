@@ -444,6 +444,68 @@ FP8BS_API int fp8bs_paged_attention_workspace_size(const fp8bs_paged_attention_a
 FP8BS_API int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, void* stream);
 
 /*
+ * A cache in 8 bits: the codes (e4m3) of keys and values stand as fp8bs_kv_cache says, with strides counted in codes
+ * and multiples of 16, in pages of a multiple of 16 slots. Each page and head has one scale for its keys and one for
+ * its values, k_scale and v_scale, fp32 [pages, heads]: a code stands for code * scale. The scales are powers of two,
+ * as fp8bs_qk_norm_rope_fp8 writes them; one that is not a positive number says that the page holds nothing yet (a
+ * cache may begin as zeros).
+ *
+ * fp8bs_qk_norm_rope_fp8 -- fp8bs_qk_norm_rope into such a cache (args->cache holds the codes). Keys and values are
+ * rounded once, from binary32 (keys) and bf16 (values) to codes. The tokens of the call that go to one page form a run:
+ * they stand next to one another in rising slots, and no page gets two runs in one call (its contents are undefined
+ * then). For each head, with need = max(amax of the run, 1e-4) / 448 rounded up to a power of two:
+ *
+ *   run from the page's slot 0     scale = need                      (the page begins anew)
+ *   run from a later slot          scale = max(scale, need)          and, where that is larger than it was, every other
+ *                                  code of the page and head is rounded again by the ratio of the scales
+ *
+ * A value that is NaN is kept as such, an infinite one saturates.
+ *
+ *   args: as in fp8bs_qk_norm_rope; v and slots may not be NULL; T * cache.heads below 2^31.
+ *   k_scale, v_scale: fp32 [cache.pages, cache.heads], 4-byte aligned, read and written.
+ */
+FP8BS_API int fp8bs_qk_norm_rope_fp8(const fp8bs_qk_norm_rope_args* args, float* k_scale, float* v_scale,
+                                     void* stream);
+
+/*
+ * fp8bs_paged_attention_fp8 -- fp8bs_paged_attention over a cache in 8 bits (args->cache holds the codes), its keys
+ * and values taken as code * scale. Scores, softmax sums and o are held in binary32. A query that is not finite gets
+ * NaN. The scales of the pages that hold keys have to be positive powers of two. Everything else, the workspace too
+ * (its size from fp8bs_paged_attention_fp8_workspace_size), is as in fp8bs_paged_attention.
+ */
+FP8BS_API int fp8bs_paged_attention_fp8_workspace_size(const fp8bs_paged_attention_args* args, size_t* bytes);
+FP8BS_API int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args, const float* k_scale,
+                                        const float* v_scale, void* stream);
+
+/*
+ * fp8bs_rms_norm -- what stands between two products of a decoder layer, in one pass:
+ *
+ *   h = x + residual                       rounded to bf16 (h = x without a residual)
+ *   n = h * rsqrt(mean(h^2) + eps) * weight
+ *   y = e4m3(n / s), s as in fp8bs_act_quant (per 1 x 128 block, scale_fmt), of n in binary32
+ *
+ * n is not rounded on its way to y: where norm_out is asked for too, y may differ from fp8bs_act_quant's codes of it.
+ *
+ *   x, residual: bf16 [T, D], rows contiguous, strides multiples of 8; residual may be NULL.
+ *   weight: bf16 [D].
+ *   residual_out: bf16 [T, D] contiguous, h; NULL without a residual, else required. It may be x or the residual
+ *       itself (the same pointer, and D its stride).
+ *   norm_out: bf16 [T, D] contiguous, n rounded once, or NULL.
+ *   y: e4m3 [T, D] contiguous, s: fp32 [T, D/128]; both or neither. One of norm_out and y at least.
+ *   D: a multiple of 128 up to 16384. All pointers 16-byte aligned, s 4-byte.
+ */
+typedef struct {
+    const void *x, *residual, *weight;
+    void *residual_out, *norm_out, *y;
+    float* s;
+    int64_t x_stride, residual_stride, T, D;
+    int scale_fmt;         /* fp8bs_scale_fmt */
+    float eps;
+} fp8bs_rms_norm_args;
+
+FP8BS_API int fp8bs_rms_norm(const fp8bs_rms_norm_args* args, void* stream);
+
+/*
  * Expert choice of a mixture-of-experts layer ("DeepSeek-V3 Administrator & Developer Guide", §6.4
  * MoE expert routing): logits = x . router_w^T in binary32, score = sigmoid(logits) or
  * softmax(logits); for the choice (not the weight) bias is added to the scores. With groups > 1 the
