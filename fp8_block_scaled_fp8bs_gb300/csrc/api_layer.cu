@@ -159,6 +159,25 @@ bool make_cache_map(CUtensorMap* map, const void* base, const fp8bs_kv_cache& c,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A cache's codes as fp8bs::AttentionMapsFp8 says: boxes of `chunk` codes of box_slots slots, swizzled by as many
+// bytes. Pages past the end read as zero.
+bool make_codes_map(CUtensorMap* map, const void* base, const fp8bs_kv_cache& c, int64_t d, int64_t head_stride,
+                    int64_t slot_stride, int64_t page_stride, int chunk, int box_slots) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    auto bytes = [&](int64_t stride, int64_t n) { return static_cast<cuuint64_t>(n > 1 ? stride : d); };
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.heads),
+                                static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[3] = {bytes(head_stride, c.heads), bytes(slot_stride, c.page_size),
+                                   bytes(page_stride, c.pages)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(chunk), 1u, static_cast<cuuint32_t>(box_slots), 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               chunk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Everything but the pointers of a paged_attention call.
 int check_attention_sizes(const fp8bs_paged_attention_args& a) {
     const int64_t dk = a.cache.dk, dv = a.cache.dv;
@@ -250,7 +269,8 @@ extern "C" int fp8bs_paged_attention_fp8_workspace_size(const fp8bs_paged_attent
     int sms = 0;
     const int dev = check_device(&sms);
     if (dev != FP8BS_OK) return dev;
-    *bytes = 0;
+    const fp8bs_paged_attention_args a = without_idle_window(*args);
+    *bytes = a.T == 0 ? 0 : fp8bs::attention_fp8_workspace(a, fp8bs::attention_fp8_plan(a, sms));
     return FP8BS_OK;
 }
 
@@ -271,7 +291,19 @@ extern "C" int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args,
     int sms = 0;
     rc = check_device(&sms);
     if (rc != FP8BS_OK) return rc;
-    return status_of(fp8bs::launch_paged_attention_fp8(a, k_scale, v_scale, static_cast<cudaStream_t>(stream)));
+    const fp8bs::AttentionPlan plan = fp8bs::attention_fp8_plan(a, sms);
+    const size_t need = fp8bs::attention_fp8_workspace(a, plan);
+    if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return FP8BS_ERR_INVALID_ARG;
+    const fp8bs_kv_cache& c = a.cache;
+    fp8bs::AttentionMapsFp8 maps;
+    maps.box_log2 = fp8bs::attention_fp8_box_log2(c);
+    if (!make_codes_map(&maps.k, c.k, c, c.dk, c.k_head_stride, c.k_slot_stride, c.k_page_stride,
+                        fp8bs::attention_fp8_key_chunk(c.dk), 1 << maps.box_log2) ||
+        !make_codes_map(&maps.v, c.v, c, c.dv, c.v_head_stride, c.v_slot_stride, c.v_page_stride,
+                        static_cast<int>(c.dv), 1 << maps.box_log2))
+        return FP8BS_ERR_CUDA;
+    return status_of(fp8bs::launch_paged_attention_fp8(maps, a, k_scale, v_scale, plan, sms,
+                                                       static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

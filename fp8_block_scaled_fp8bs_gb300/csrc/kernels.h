@@ -215,9 +215,20 @@ cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tm
                                    const fp8bs_paged_attention_args& a, const AttentionModes& modes,
                                    const AttentionPlan& plan, int num_sms, cudaStream_t stream);
 
-// Attention over a paged cache of e4m3 codes (fp8bs_paged_attention_fp8).
-cudaError_t launch_paged_attention_fp8(const fp8bs_paged_attention_args& a, const float* k_scale, const float* v_scale,
-                                       cudaStream_t stream);
+// Attention over a paged cache of e4m3 codes (fp8bs_paged_attention_fp8); plan and workspace as above. The maps are
+// 4-D, {d codes, heads, slots, pages}, with boxes of 2^box_log2 slots of one head, swizzled by the box's row: `key
+// chunk` codes of a key, all of a value.
+struct AttentionMapsFp8 {
+    CUtensorMap k, v;
+    int box_log2;
+};
+int attention_fp8_box_log2(const fp8bs_kv_cache& c);
+int attention_fp8_key_chunk(int64_t dk);
+AttentionPlan attention_fp8_plan(const fp8bs_paged_attention_args& a, int num_sms);
+size_t attention_fp8_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan);
+cudaError_t launch_paged_attention_fp8(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a,
+                                       const float* k_scale, const float* v_scale, const AttentionPlan& plan,
+                                       int num_sms, cudaStream_t stream);
 
 // Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
 constexpr int kMoeMaxTokens = 64;
