@@ -270,7 +270,7 @@ extern "C" int fp8bs_paged_attention_fp8_workspace_size(const fp8bs_paged_attent
     const int dev = check_device(&sms);
     if (dev != FP8BS_OK) return dev;
     const fp8bs_paged_attention_args a = without_idle_window(*args);
-    *bytes = a.T == 0 ? 0 : fp8bs::attention_fp8_workspace(a, fp8bs::attention_fp8_plan(a, sms));
+    *bytes = a.T == 0 ? 0 : fp8bs::attention_fp8_workspace(a, sms);
     return FP8BS_OK;
 }
 
@@ -291,8 +291,7 @@ extern "C" int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args,
     int sms = 0;
     rc = check_device(&sms);
     if (rc != FP8BS_OK) return rc;
-    const fp8bs::AttentionPlan plan = fp8bs::attention_fp8_plan(a, sms);
-    const size_t need = fp8bs::attention_fp8_workspace(a, plan);
+    const size_t need = fp8bs::attention_fp8_workspace(a, sms);
     if (need > 0 && (!a.workspace || a.workspace_bytes < need)) return FP8BS_ERR_INVALID_ARG;
     const fp8bs_kv_cache& c = a.cache;
     fp8bs::AttentionMapsFp8 maps;
@@ -302,7 +301,7 @@ extern "C" int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args,
         !make_codes_map(&maps.v, c.v, c, c.dv, c.v_head_stride, c.v_slot_stride, c.v_page_stride,
                         static_cast<int>(c.dv), 1 << maps.box_log2))
         return FP8BS_ERR_CUDA;
-    return status_of(fp8bs::launch_paged_attention_fp8(maps, a, k_scale, v_scale, plan, sms,
+    return status_of(fp8bs::launch_paged_attention_fp8(maps, a, k_scale, v_scale, sms,
                                                        static_cast<cudaStream_t>(stream)));
 }
 

@@ -33,674 +33,11 @@
 // channels of a box at once where the cache's strides allow it.
 // Few rows and long keys: the key axis is cut into pieces (AttentionPlan), each CTA leaves its
 // unnormalised O, maximum and sum, and a second kernel joins them in key order.
-#include "attention.cuh"
+#include "attention_tiles.cuh"
 
 namespace fp8bs {
 
 namespace {
-
-constexpr float kRescale = 8.0f;
-
-template <int DK_, int DV_, int NQ_>
-struct AttnCfg {
-    static constexpr int DK = DK_, DV = DV_, NQ = NQ_;
-    // Keys per tile. (192-wide keys: 96, so that two tiles of values fit.)
-    static constexpr int BN = NQ == 1 ? 64 : DK <= 128 ? 128 : 96;
-    static constexpr int ROWS = NQ * 128;
-    static constexpr int SLOTS = 4;                              // ring of work items
-    static constexpr int SBUF = 2;                               // S buffers: per query tile, or 2
-    static constexpr int K_TILE = BN * DK * 2, V_TILE = BN * DV * 2, Q_TILE = 128 * DK * 2;
-    // One query tile of 64 channels: two CTAs per SM, one's softmax under the other's (a windowed mixed batch 32 ->
-    // 25 us, decode of 64 sequences of 4096 keys 153 -> 109).
-    static constexpr int CTAS = NQ == 1 && DK == 64 ? 2 : 1;
-    static constexpr int KST = DK == 64 ? (NQ == 2 ? 4 : 5) : DK == 128 ? (NQ == 2 ? 3 : 6) : (NQ == 2 ? 2 : 4);
-    static constexpr int VST = DK == 64 ? (NQ == 2 ? 4 : 5) : DK == 128 ? (NQ == 2 ? 2 : 5) : (NQ == 2 ? 2 : 4);
-    static constexpr int SOFT_WARPS = 4 * NQ;
-    static constexpr int KEY_WARP = SOFT_WARPS;                  // brings the keys (and hands out the items)
-    static constexpr int VALUE_WARP = SOFT_WARPS + 1;
-    static constexpr int MMA_WARP = SOFT_WARPS + 2;
-    // (two query tiles: a whole third warpgroup beside the softmax's, for the split of registers below)
-    static constexpr int THREADS = 32 * (SOFT_WARPS + (NQ == 2 ? 4 : 3));
-    static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
-    static constexpr int BARS = 2 * KST + 2 * VST + 2 * SBUF + 3 * NQ + 3 + 2 * SLOTS;
-    static constexpr int SMEM = 1024 + NQ * Q_TILE + KST * K_TILE + VST * V_TILE + BARS * 8 + 64;
-    static_assert(SMEM <= kSmemLimit, "shared memory");
-};
-
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16.
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Keys and values lie in shared memory as [8 keys][64 channels]: one key per 128-byte row, 128-byte swizzle, the
-// blocks of 1024 bytes of the same 8 keys one after another, 8-key groups `group` bytes apart. The keys' product
-// reads them K-major, the values' product MN-major (its leading offset is the step to the next 64 channels).
-__device__ __forceinline__ uint64_t smem_desc_groups(uint32_t addr, uint32_t group) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(1024 >> 4) << 16;
-    d |= static_cast<uint64_t>(group >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
-}
-
-constexpr uint32_t kIdescBMajorMN = 1u << 16;
-
-// The key tiles k0, k0 + BN, ... (nt of them) of an item into the ring of KEYS or values, by TMA in boxes of
-// 2^box_log2 slots. The pages of 32 boxes are looked up at once, one per lane, while those before are in use, and
-// each box is issued by a lane of its own (one lane for all: 64 ragged sequences with pages of 16 slots took 273
-// instead of 204 us, a chunk of 4096 over 8192 keys 364 instead of 335). Values of the
-// first and last tile that do not count are cleared before the tile does: whatever stood there must not meet a
-// probability of zero.
-// first_wait(): waited for before the first tile, under the first look at the pages.
-template <class Cfg, bool KEYS, typename First>
-__device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, const fp8bs_paged_attention_args& a,
-                                            const Item& it, int k0, int nt, int box_log2, int mode, uint8_t* ring,
-                                            uint64_t* full, uint64_t* empty, uint64_t* tail, int2* window,
-                                            int lane, First first_wait) {
-    constexpr int STAGES = KEYS ? Cfg::KST : Cfg::VST;
-    constexpr int TILE = KEYS ? Cfg::K_TILE : Cfg::V_TILE;
-    constexpr int CH = (KEYS ? Cfg::DK : Cfg::DV) / 64;
-    constexpr int BN = Cfg::BN;
-    const int box = 1 << box_log2;
-    const int boxes = BN >> box_log2;
-    const int page_size = static_cast<int>(a.cache.page_size);
-    const int heads = static_cast<int>(a.cache.heads);
-    const int head = it.head, kv = it.kv, key_lo = it.key_lo;
-    const int32_t* table = a.page_table + it.seq * a.table_stride;
-    auto lookup = [&](int w) {               // boxes 32 w .. 32 w + 31 of the item
-        const int64_t key = k0 + (static_cast<int64_t>(w) * 32 + lane) * box;
-        int2 at = make_int2(0, 0);
-        if (key < kv && key + box > key_lo) {
-            const int p = static_cast<int>(key) / page_size;
-            at.y = static_cast<int>(key) - p * page_size;
-            at.x = table[p];
-        }
-        return at;
-    };
-    int window_at = 0;                       // the 32 boxes that `next` is of
-    int2 next = lookup(0);
-    if (s.n == 0 && !first_wait()) return false;
-    for (int j = 0; j < nt; ++j) {
-        const int key0 = k0 + j * BN;
-        // boxes [none, live) hold keys that count: those before them are past a window (their pages may have been
-        // given back), those after them past the sequence
-        const int live = min(boxes, (kv - key0 + box - 1) >> box_log2);
-        const int none = j == 0 ? (key_lo - k0) >> box_log2 : 0;
-        const int st = s.n % STAGES;
-        if (!warp_wait(&empty[st], ((s.n / STAGES) & 1) ^ 1)) return false;
-        const bool partial = !KEYS && (kv - key0 < BN || none > 0);
-        uint64_t* bar = partial ? tail : &full[st];
-        const uint32_t dst = smem_addr(ring) + st * TILE;
-        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>((live - none) * box * CH * 128));
-        for (int b = none; b < live;) {
-            const int first = j * boxes + b;
-            if ((first & 31) == 0 || (j == 0 && b == none)) {
-                // (the first look may begin inside a window of 32 boxes)
-                while (window_at < first >> 5) {
-                    next = lookup(++window_at);
-                }
-                // a page outside the cache: a coordinate past the end, which reads as zeros
-                if (static_cast<unsigned>(next.x) >= static_cast<unsigned>(a.cache.pages)) {
-                    next.x = static_cast<int>(a.cache.pages);
-                    const int64_t key = k0 + (static_cast<int64_t>(window_at) * 32 + lane) * box;
-                    if (KEYS && key < kv && key + box > key_lo) record_error(FP8BS_DEVERR_INDEX);
-                }
-                window[lane] = next;
-                next = lookup(++window_at);
-                __syncwarp();
-            }
-            const int count = min(32 - (first & 31), live - b);
-            __syncwarp();
-            if (lane < count) {
-                const int2 at = window[(first + lane) & 31];
-                const int key = (b + lane) << box_log2;           // of the tile
-                if (mode == 0)
-                    tma_load_5d(dst + key * (CH * 128), map, bar, 0, 0, head * CH, at.y >> 3, at.x);
-                else if (mode == 1)
-                    tma_load_5d(dst + key * (CH * 128), map, bar, 0, 0, 0, at.y >> 3, at.x * heads + head);
-                else
-                    for (int c = 0; c < CH; ++c)
-                        tma_load_4d(dst + (key >> 3) * (CH * 1024) + c * 1024 + (key & 7) * 128, map, bar,
-                                    c * 64, head, at.y, at.x);
-            }
-            __syncwarp();
-            b += count;
-        }
-        if (partial) {
-            if (!warp_wait(tail, s.tails & 1)) return false;
-            ++s.tails;
-            const int skip = none << box_log2;
-            const int keep = min(kv - key0, BN);
-            for (int i = lane; i < (BN - keep + skip) * CH * 8; i += 32) {
-                const int k = i / (CH * 8);
-                const int key = k < skip ? k : keep + k - skip;
-                const int c = i / 8 % CH;
-                *reinterpret_cast<uint4*>(ring + st * TILE + (key >> 3) * (CH * 1024) + c * 1024 +
-                                          (key & 7) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
-        }
-        ++s.n;
-    }
-    return true;
-}
-
-template <class Cfg>
-__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
-    paged_attention_kernel(const __grid_constant__ CUtensorMap tmK,
-                           const __grid_constant__ CUtensorMap tmV,
-                           const __grid_constant__ fp8bs_paged_attention_args a,
-                           const AttentionModes modes, const int piece_len, const int pieces, const AttnParts parts) {
-    constexpr int DK = Cfg::DK, DV = Cfg::DV, NQ = Cfg::NQ, BN = Cfg::BN;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Item s_item[Cfg::SLOTS];
-    __shared__ int2 s_window[2][32];                      // (page, slot) of 32 boxes: keys', values'
-    __shared__ uint32_t s_tmem;
-    uint8_t* smem = align_1024(smem_raw);
-    uint8_t* sQ = smem;                                   // [NQ][DK/64][128 rows][128 bytes]
-    uint8_t* sK = sQ + NQ * Cfg::Q_TILE;                  // [KST][BN/8][DK/64][8 keys][128 bytes]
-    uint8_t* sV = sK + Cfg::KST * Cfg::K_TILE;            // [VST][BN/8][DV/64][8 keys][128 bytes]
-    uint64_t* k_full = reinterpret_cast<uint64_t*>(sV + Cfg::VST * Cfg::V_TILE);
-    uint64_t* k_empty = k_full + Cfg::KST;
-    uint64_t* v_full = k_empty + Cfg::KST;
-    uint64_t* v_empty = v_full + Cfg::VST;
-    uint64_t* s_full = v_empty + Cfg::VST;                // [SBUF]
-    uint64_t* p_full = s_full + Cfg::SBUF;                // [SBUF]
-    uint64_t* q_full = p_full + Cfg::SBUF;                // [NQ] queries of an item
-    uint64_t* o_done = q_full + NQ;                       // [NQ] each product with V
-    uint64_t* o_last = o_done + NQ;                       // [NQ] the last one of an item
-    uint64_t* v_tail = o_last + NQ;                       // an item's last, partly valid value tile
-    uint64_t* i_full = v_tail + 1;                        // [SLOTS]
-    uint64_t* i_empty = i_full + Cfg::SLOTS;              // [SLOTS]
-    uint64_t* drain = i_empty + Cfg::SLOTS;               // all products, when given up
-    uint64_t* q_first = drain + 1;                        // the first queries, once, for the value warp
-
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const int group = static_cast<int>(a.q_heads / a.cache.heads);
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < Cfg::KST; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-        }
-        for (int i = 0; i < Cfg::VST; ++i) {
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
-        }
-        for (int i = 0; i < Cfg::SBUF; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-        }
-        for (int i = 0; i < NQ; ++i) {
-            mbar_init(&q_full[i], 4);
-            mbar_init(&o_done[i], 1);
-            mbar_init(&o_last[i], 1);
-        }
-        mbar_init(v_tail, 1);
-        mbar_init(drain, 1);
-        mbar_init(q_first, 1);
-        for (int i = 0; i < Cfg::SLOTS; ++i) {
-            mbar_init(&i_full[i], 1);
-            mbar_init(&i_empty[i], Cfg::SOFT_WARPS + 2);
-        }
-        fence_barrier_init();
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-    }
-    if (warp == Cfg::MMA_WARP) tmem_alloc(&s_tmem, Cfg::TMEM_COLS);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    grid_dependency_wait();
-    grid_launch_dependents();
-
-    // An item's key tiles start here, and are so many.
-    auto first_tile = [](const Item& it) { return it.key_lo / BN * BN; };
-    auto key_tiles = [&](const Item& it) {
-        return it.key_hi > it.key_lo ? (it.key_hi - first_tile(it) + BN - 1) / BN : 0;
-    };
-    // The x-th item of this CTA (x counts from 0), for the other warps: to be waited for, and given back.
-    auto item_ready = [&](int x) { return warp_wait(&i_full[x % Cfg::SLOTS], (x / Cfg::SLOTS) & 1); };
-    auto item_done = [&](int x) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&i_empty[x % Cfg::SLOTS]);
-    };
-
-    // Two query tiles, registers: 168 x 384 threads at launch; the softmax's row of S needs more, the third
-    // warpgroup less (208 x 256 + 80 x 128 = 63488 of 64512).
-    if (warp < Cfg::SOFT_WARPS) {
-        if constexpr (NQ == 2) regs_inc<208>();
-        // ---- softmax warps: thread = row of query tile q
-        const int q = warp >> 2;
-        const int quarter = warp & 3;
-        const int r = q * 128 + quarter * 32 + lane;          // row of the item's tile
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
-        // (a scale of zero: any tiny factor keeps -inf apart from the finite scores; one that is NaN stays so)
-        const float c = max_nan(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-        // Queries of query tile q into shared memory (K-major, 128-byte swizzle), valid rows only (what the
-        // others hold is of no consequence: rows do not meet). A negative scale turns their signs, so that
-        // the row maximum is always that of the largest S.
-        auto load_queries = [&](const Item& it) {
-            const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
-            constexpr int PIECES = DK / 8;                           // 16-byte pieces of a row
-            constexpr int BATCH = 8;
-            const int here = max(0, min(128, it.rows - q * 128));
-            const int tid = threadIdx.x & 127;
-#pragma unroll 1
-            for (int i0 = tid; i0 < here * PIECES; i0 += 128 * BATCH) {
-                uint4 v[BATCH];
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int e = i0 + i * 128;
-                    const int row = e / PIECES;
-                    if (row < here) {
-                        const int pr = it.first_row + q * 128 + row;
-                        const int tok = pr / group;
-                        v[i] = __ldg(reinterpret_cast<const uint4*>(
-                                         static_cast<const __nv_bfloat16*>(a.q) +
-                                         (it.q0 + tok) * a.q_token_stride +
-                                         (it.head * group + pr - tok * group) * a.q_head_stride) +
-                                     e % PIECES);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int e = i0 + i * 128;
-                    const int row = e / PIECES;
-                    const int ch = e % PIECES;
-                    if (row < here) {
-                        v[i].x ^= flip; v[i].y ^= flip; v[i].z ^= flip; v[i].w ^= flip;
-                        *reinterpret_cast<uint4*>(sQ + q * Cfg::Q_TILE + (ch >> 3) * (128 * 128) +
-                                                  row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v[i];
-                    }
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[q]);
-        };
-        // An item's output rows as (token, query head).
-        auto out_row = [&](const Item& it, int row) {
-            const int pr = it.first_row + row;
-            const int tok = pr / group;
-            return (it.q0 + tok) * a.q_heads + it.head * group + (pr - tok * group);
-        };
-        bool ok = true;
-        int n0 = 0, used = 0;
-        ok = item_ready(0);
-        if (ok && s_item[0].seq >= 0 && key_tiles(s_item[0]) > 0) load_queries(s_item[0]);
-        for (int x = 0; ok && s_item[x % Cfg::SLOTS].seq >= 0; ++x) {
-            const Item& it = s_item[x % Cfg::SLOTS];
-            const int nt = key_tiles(it);
-            const int k0 = first_tile(it);
-            const bool live = r < it.rows;
-            const bool idle = q * 128 + quarter * 32 >= it.rows;     // no valid row in this warp
-            if (live && it.piece == 0)
-                // pieces that this sequence does not have are empty
-                for (int p = it.pieces; p < pieces; ++p)
-                    parts.ml[p * parts.rows + out_row(it, r)] = make_float2(-INFINITY, 0.0f);
-            float m = -INFINITY;           // maximum in use, raw score
-            float l = 0.0f;
-            if (nt > 0) {
-                const KeyRange kr =
-                    keys_of(a, it.n, it.kv, (it.first_row + min(r, it.rows - 1)) / group);
-                // tiles that need no mask for any row of this query tile
-                const int last_row = min(it.rows, (q + 1) * 128) - 1;
-                const int full_hi = min(it.key_hi,
-                    keys_of(a, it.n, it.kv, (it.first_row + min(q * 128, it.rows - 1)) / group).hi);
-                const int full_lo = max(it.key_lo,
-                    keys_of(a, it.n, it.kv, (it.first_row + max(last_row, 0)) / group).lo);
-                const int row_lo = max(kr.lo, it.key_lo), row_hi = min(kr.hi, it.key_hi);
-                for (int j = 0; j < nt; ++j) {
-                    const int n = n0 + j;
-                    const int buf = NQ == 2 ? q : n & 1;
-                    const uint32_t sph = NQ == 2 ? n & 1 : (n >> 1) & 1;
-                    if (!warp_wait(&s_full[buf], sph)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (!idle) {
-                        const uint32_t s_tmem_row = tmem + lanes + buf * BN;
-                        const int kb = k0 + j * BN;
-                        const bool masked = kb < full_lo || kb + BN > full_hi;
-                        uint32_t p[BN / 2];
-                        float2 sum[2];
-                        auto load_row = [&](float* s) {
-#pragma unroll
-                            for (int i = 0; i < BN / 32; ++i) tmem_ld_32cols(s_tmem_row + 32 * i, s + 32 * i);
-#pragma unroll
-                            for (int i = 0; i < BN / 32; ++i) tmem_wait_ld_32(s + 32 * i);
-                            if (masked) {
-                                const int lo = row_lo - kb, hi = row_hi - kb;
-#pragma unroll
-                                for (int i = 0; i < BN; ++i)
-                                    if (i < lo || i >= hi) s[i] = -INFINITY;
-                            }
-                        };
-                        // Probabilities with the maximum in use, and this tile's maximum beside them: it is only
-                        // looked at afterwards, and hardly ever asks for another pass (kRescale). The first tile
-                        // of a row has no maximum yet and looks before; so does the form with one query tile,
-                        // whose softmax waits for the keys (64 ragged sequences: 192 us, 204 the other way; the
-                        // chunk of 4096 with two tiles: 321 and 313).
-                        float top = m;
-                        auto probabilities = [&](const float* s) {
-                            const float mc = m == -INFINITY ? 0.0f : m * c;
-                            const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-                            sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int k = 0; k < BN / 2; ++k) {
-                                mx[k & 3] = fmaxf(mx[k & 3], fmaxf(s[2 * k], s[2 * k + 1]));
-                                float2 y = __ffma2_rn(make_float2(s[2 * k], s[2 * k + 1]), c2, mc2);
-                                y.x = exp2_fast(y.x);
-                                y.y = exp2_fast(y.y);
-                                sum[k & 1] = __fadd2_rn(sum[k & 1], y);
-                                p[k] = pack_bf16x2(y.x, y.y);
-                            }
-                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        };
-                        bool look = NQ == 1 || j == 0 || __any_sync(0xffffffffu, m == -INFINITY);
-                        if (!look) {
-                            float s[BN];
-                            load_row(s);
-                            probabilities(s);
-                            look = __any_sync(0xffffffffu, (top - m) * c > kRescale);
-                        }
-                        if (look) {
-                            float s[BN];
-                            load_row(s);
-                            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                            for (int i = 4; i < BN; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                            const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
-                            const float keep = grow ? exp2_fast((m - top) * c) : 1.0f;
-                            if (grow) m = top;
-                            l *= keep;
-                            probabilities(s);
-                            if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                                if (!warp_wait(&o_done[q], (n - 1) & 1)) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int i = 0; i < DV / 16; ++i) {
-                                    float o[16];
-                                    tmem_ld_16cols(o_tmem + 16 * i, o);
-                                    tmem_wait_ld_16(o);
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[k] *= keep;
-                                    tmem_st_16cols(o_tmem + 16 * i, reinterpret_cast<const uint32_t*>(o));
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) tmem_st_16cols(s_tmem_row + 16 * i, p + 16 * i);
-                        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[buf]);
-                    } else if (lane == 0) {
-                        mbar_arrive(&p_full[buf]);
-                    }
-                }
-                n0 += nt;
-            }
-            // The next item's queries: every S of this one has been computed (this warp has seen the last),
-            // so their place is free, and the next S can be computed while this O is written out.
-            if (ok) ok = item_ready(x + 1);
-            const Item& next = s_item[(x + 1) % Cfg::SLOTS];
-            if (ok && next.seq >= 0 && key_tiles(next) > 0) load_queries(next);
-            if (nt > 0) {
-                if (ok && !warp_wait(&o_last[q], used & 1)) ok = false;
-                ++used;
-                tc_fence_after();
-            }
-            if (ok && !idle) {
-                const int64_t row = live ? out_row(it, r) : 0;
-                const float mc = m == -INFINITY ? -INFINITY : m * c;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;       // (NaN stays NaN)
-                if (pieces > 1) {
-                    float* dst = parts.o + (it.piece * parts.rows + row) * DV;
-                    if (nt > 0)
-#pragma unroll
-                        for (int i = 0; i < DV / 32; ++i) {
-                            float o[32];
-                            tmem_ld_32cols(o_tmem + 32 * i, o);
-                            tmem_wait_ld_32(o);
-                            if (live)
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    *reinterpret_cast<float4*>(dst + 32 * i + 4 * k) =
-                                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                        }
-                    if (live) parts.ml[it.piece * parts.rows + row] = make_float2(mc, l);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * DV);
-#pragma unroll
-                    for (int i = 0; i < DV / 32; ++i) {
-                        float o[32];
-                        if (nt > 0) {
-                            tmem_ld_32cols(o_tmem + 32 * i, o);
-                            tmem_wait_ld_32(o);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = 0.0f;
-                        }
-                        if (live)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                dst[4 * i + k] = make_uint4(
-                                    pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                    pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                    pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                    pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                    }
-                    if (live && a.lse)
-                        a.lse[row] = l == 0.0f ? -INFINITY : (mc + log2_fast(l)) * 0.6931471805599453f;
-                }
-            }
-            tc_fence_before();
-            item_done(x);
-        }
-        if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
-    } else {
-        if constexpr (NQ == 2) regs_dec<80>();
-        if (warp == Cfg::KEY_WARP) {
-            // ---- hands out the items and brings their keys
-            ItemFinder finder;
-            finder.base = finder.before = 0;
-            finder.loaded = false;
-            bool ok = true;
-            Stream ks = {0, 0};
-            int x = 0;
-            // The items are dealt out in rounds, every other one backwards: long items and short ones even out. Where
-            // the last round is not whole, some CTAs have an item more than the others. Of one sequence, whose
-            // items come longest first, those are dealt the short ones (a chunk of 4096 over 8192 keys: 169 key tiles
-            // for the busiest CTA instead of 182, 282 us instead of 315); in a batch they may be any. (Two query
-            // tiles only: few rows mean pieces of one length, and a batch of 9 us takes 0.3 more with it.)
-            int ctas = gridDim.x, mine = blockIdx.x, start = 0, rounds = INT32_MAX;
-            if (NQ == 2 && __builtin_expect(a.B == 1, 0)) {
-                load_sequences(finder, a, Cfg::ROWS, piece_len, lane);
-                const int items = __shfl_sync(0xffffffffu, finder.incl, 31) * static_cast<int>(a.cache.heads);
-                const int whole = items / ctas, more = items % ctas;
-                if (mine < ctas - more) {
-                    ctas -= more;
-                    rounds = whole;
-                } else {
-                    mine -= ctas - more;
-                    start = (ctas - more) * whole;
-                    ctas = more;
-                    rounds = whole + 1;
-                }
-            }
-            for (int round = 0; ok; ++round) {
-                const int64_t at = round < rounds ? start + static_cast<int64_t>(round) * ctas +
-                                                        (round & 1 ? ctas - 1 - mine : mine)
-                                                  : int64_t{INT32_MAX};
-                const Item it = find_item(finder, a, static_cast<int>(min(at, int64_t{INT32_MAX})), Cfg::ROWS,
-                                          BN, piece_len, lane);
-                if (it.seq == -2) {
-                    if (lane == 0) record_error(FP8BS_DEVERR_INDEX);
-                    continue;
-                }
-                if (!warp_wait(&i_empty[x % Cfg::SLOTS], ((x / Cfg::SLOTS) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    s_item[x % Cfg::SLOTS] = it;
-                    mbar_arrive(&i_full[x % Cfg::SLOTS]);
-                }
-                __syncwarp();
-                ++x;
-                if (it.seq < 0) break;
-                const int nt = key_tiles(it);
-                if (nt == 0) continue;
-                // (the first queries come first: behind a full ring of keys they take several times as long)
-                ok = bring_tiles<Cfg, true>(ks, &tmK, a, it, first_tile(it), nt, modes.box_log2, modes.k, sK,
-                                            k_full, k_empty, nullptr, s_window[0], lane, [&] {
-                                                for (int q = 0; q < NQ; ++q)
-                                                    if (!warp_wait(&q_full[q], 0)) return false;
-                                                if (lane == 0) mbar_arrive(q_first);
-                                                return true;
-                                            });
-            }
-            if (!ok && lane == 0) drain_tiles<Cfg::KST>(ks, k_full);
-        } else if (warp == Cfg::VALUE_WARP) {
-            // ---- brings the items' values
-            bool ok = true;
-            Stream vs = {0, 0};
-            for (int x = 0; ok; ++x) {
-                ok = item_ready(x);
-                if (!ok) break;
-                const Item it = s_item[x % Cfg::SLOTS];
-                item_done(x);
-                if (it.seq < 0) break;
-                const int nt = key_tiles(it);
-                if (nt == 0) continue;
-                ok = bring_tiles<Cfg, false>(vs, &tmV, a, it, first_tile(it), nt, modes.box_log2, modes.v, sV,
-                                             v_full, v_empty, v_tail, s_window[1], lane,
-                                             [&] { return warp_wait(q_first, 0); });
-            }
-            if (!ok && lane == 0) {
-                drain_tiles<Cfg::VST>(vs, v_full);
-                mbar_wait(v_tail, vs.tails & 1, kDrainLimitNs);
-            }
-        } else if (warp == Cfg::MMA_WARP) {
-            // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j), then S of the tile's next keys, which
-            // takes P's place (the tensor core works in order).
-            // With two query tiles one's products run under the other's softmax.
-            constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV) | kIdescBMajorMN;
-            // descriptors of the first stages; those of other stages and steps lie at constant distances (in
-            // units of 16 bytes, which do not carry out of the address field)
-            const uint64_t q_desc = smem_desc_k_sw128(smem_addr(sQ));
-            const uint64_t k_desc = smem_desc_groups(smem_addr(sK), DK / 64 * 1024);
-            const uint64_t v_desc = smem_desc_groups(smem_addr(sV), DV / 64 * 1024);
-            const uint32_t o_tmem = tmem + Cfg::SBUF * BN;
-            bool ok = true;
-            int n0 = 0;                        // key tiles of the items before
-            int used = 0;                      // items with keys before
-            // S(n): buffer q (two tiles) or n % 2, keys of tile n
-            auto qk = [&](int q, int n) {
-                const int st = n % Cfg::KST;
-                if (q == 0) {
-                    if (!warp_wait(&k_full[st], (n / Cfg::KST) & 1)) return false;
-                    tc_fence_after();
-                }
-                const int buf = NQ == 2 ? q : n & 1;
-                const uint64_t kd = k_desc + static_cast<uint32_t>(st * (Cfg::K_TILE / 16));
-                if (elect_one()) {
-#pragma unroll
-                    for (int d = 0; d < DK / 16; ++d)
-                        mma_bf16(tmem + buf * BN,
-                                 q_desc + (q * Cfg::Q_TILE + (d / 4) * (128 * 128) + (d % 4) * 32) / 16,
-                                 kd + ((d / 4) * 1024 + (d % 4) * 32) / 16, idesc_qk, d > 0 ? 1u : 0u);
-                    mma_commit(&s_full[buf]);
-                    if (q == NQ - 1) mma_commit(&k_empty[st]);
-                }
-                __syncwarp();
-                return true;
-            };
-            for (int x = 0; ok; ++x) {
-                if (!item_ready(x)) {
-                    ok = false;
-                    break;
-                }
-                const int seq = s_item[x % Cfg::SLOTS].seq;
-                const int nt = __shfl_sync(0xffffffffu, key_tiles(s_item[x % Cfg::SLOTS]), 0);
-                item_done(x);
-                if (seq < 0) break;
-                if (nt == 0) continue;
-                for (int q = 0; ok && q < NQ; ++q)
-                    ok = warp_wait(&q_full[q], used & 1) && qk(q, n0);
-                if (ok && NQ == 1 && nt > 1) ok = qk(0, n0 + 1);
-                for (int j = 0; ok && j < nt; ++j) {
-                    const int n = n0 + j;
-                    const int st = n % Cfg::VST;
-                    const uint32_t pph = NQ == 2 ? n & 1 : (n >> 1) & 1;
-                    const uint64_t vd = v_desc + static_cast<uint32_t>(st * (Cfg::V_TILE / 16));
-                    if (!warp_wait(&v_full[st], (n / Cfg::VST) & 1)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        const int buf = NQ == 2 ? q : n & 1;
-                        if (!warp_wait(&p_full[buf], pph)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < BN / 16; ++k)
-                                mma_bf16_ta(o_tmem + q * DV, tmem + buf * BN + 8 * k,
-                                            vd + k * (DV / 64 * 2048 / 16), idesc_pv,
-                                            j > 0 || k > 0 ? 1u : 0u);
-                            mma_commit(&o_done[q]);
-                            if (q == NQ - 1) mma_commit(&v_empty[st]);
-                            if (j == nt - 1) mma_commit(&o_last[q]);
-                        }
-                        __syncwarp();
-                        const int next = NQ == 2 ? j + 1 : j + 2;
-                        if (next < nt) ok = qk(q, n0 + next);
-                    }
-                }
-                n0 += nt;
-                ++used;
-            }
-            if (!ok) {
-                // abandoned: the products in flight still read shared memory; let them end
-                if (lane == 0) record_error(FP8BS_DEVERR_MMA_WAIT);
-                if (elect_one()) mma_commit(drain);
-                __syncwarp();
-                if (!warp_wait(drain, 0) && lane == 0) record_error(FP8BS_DEVERR_DRAIN_WAIT);
-            }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == Cfg::MMA_WARP) tmem_dealloc(tmem, Cfg::TMEM_COLS);
-}
 
 // Whether the two-tile form is used: where the average sequence has more rows than one tile holds. (32 sequences of
 // 2048 keys, 8 heads of 128 channels, one tile and two: 128 rows 62 and 76 us, 160 rows 122 and 80, 512 rows 268 and
@@ -734,7 +71,7 @@ cudaError_t launch_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
     const int64_t resident = static_cast<int64_t>(num_sms) * Cfg::CTAS;
     const unsigned grid = static_cast<unsigned>(items < resident ? items : resident);
     e = launch_pdl(kernel, grid, Cfg::THREADS, Cfg::SMEM, stream, tmK, tmV, a, modes, plan.piece_len,
-                   plan.pieces, parts);
+                   plan.pieces, parts, Scales{}, 0);
     if (e != cudaSuccess || plan.pieces == 1) return e;
     // Many pieces of few rows: four warps a row; else a warp each (more blocks than the GPU holds at once would
     // keep the next kernel from starting: 4096 rows of 8 pieces took 30 us with four warps each, none to be seen
@@ -750,7 +87,10 @@ cudaError_t launch_attention(const CUtensorMap& tmK, const CUtensorMap& tmV,
 }  // namespace
 
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms) {
-    const bool two = two_tiles(a);
+    return attention_plan(a, num_sms, two_tiles(a));
+}
+
+AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms, bool two) {
     const int64_t rows = two ? 256 : 128;
     const int64_t group = a.q_heads / a.cache.heads;
     // (sequences of one length, as in decoding, are counted exactly)

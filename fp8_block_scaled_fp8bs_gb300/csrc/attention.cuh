@@ -67,8 +67,9 @@ __device__ __forceinline__ Cut cut_of(const fp8bs_paged_attention_args& a, int r
     return c;
 }
 
+// more_rows: sequences of so many rows or fewer have no items here.
 __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_attention_args& a, int rows,
-                                               int piece_len, int lane) {
+                                               int piece_len, int lane, int more_rows) {
     const int group = static_cast<int>(a.q_heads / a.cache.heads);
     f.sum = 0;
 #pragma unroll
@@ -83,7 +84,7 @@ __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_
         f.units[i] = 0;
         if (n > a.max_q_len || f.kv[i] > a.max_kv_len) {
             f.units[i] = 1;      // out of bounds: handed out once, to be reported
-        } else if (n > 0) {
+        } else if (n > 0 && static_cast<int64_t>(n) * group > more_rows) {
             const Cut c = cut_of(a, rows, piece_len, n, f.kv[i], group);
             f.units[i] = c.tiles * c.pieces;
         }
@@ -99,7 +100,7 @@ __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_
 }
 
 __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_attention_args& a, int item, int rows,
-                                          int bn, int piece_len, int lane) {
+                                          int bn, int piece_len, int lane, int more_rows) {
     Item it;
     it.seq = -1;
     const int heads = static_cast<int>(a.cache.heads);
@@ -107,7 +108,7 @@ __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_atten
     const int unit = item / heads;
     it.head = item - unit * heads;
     while (f.base < a.B) {
-        if (!f.loaded) load_sequences(f, a, rows, piece_len, lane);
+        if (!f.loaded) load_sequences(f, a, rows, piece_len, lane, more_rows);
         const unsigned hit = __ballot_sync(0xffffffffu, f.before + f.incl > unit);
         if (hit) {
             const int src = __ffs(hit) - 1;

@@ -1,0 +1,64 @@
+// attention_fp8_tiles.cu -- attention over a paged cache of e4m3 codes for sequences of many query rows: the kernel of
+// attention.cu with two query tiles, its keys taken as codes and its values widened on the way (attention_tiles.cuh).
+#include "attention_tiles.cuh"
+
+namespace fp8bs {
+
+namespace {
+
+AttnParts parts_of(const fp8bs_paged_attention_args& a, const AttentionPlan& plan) {
+    AttnParts p = {};
+    p.rows = a.T * a.q_heads;
+    if (plan.pieces > 1) {
+        p.o = static_cast<float*>(a.workspace);
+        p.ml = reinterpret_cast<float2*>(p.o + plan.pieces * p.rows * a.cache.dv);
+    }
+    return p;
+}
+
+template <int DK, int DV>
+cudaError_t launch_tiles(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a, const Scales& scales,
+                         const AttentionPlan& plan, int more_rows, int num_sms, cudaStream_t stream) {
+    using Cfg = AttnCfg<DK, DV, 2, true>;
+    auto kernel = paged_attention_kernel<Cfg>;
+    const cudaError_t e = set_smem(kernel, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t items = tile_bound(a, Cfg::ROWS) * a.cache.heads * plan.pieces;
+    if (items >= INT32_MAX) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
+    AttentionModes modes = {};
+    modes.box_log2 = maps.box_log2;
+    return launch_pdl(kernel, grid, Cfg::THREADS, Cfg::SMEM, stream, maps.k, maps.v, a, modes, plan.piece_len,
+                      plan.pieces, parts_of(a, plan), scales, more_rows);
+}
+
+template <int DV>
+cudaError_t launch_join(const fp8bs_paged_attention_args& a, const AttentionPlan& plan, cudaStream_t stream) {
+    const AttnParts parts = parts_of(a, plan);
+    return launch_pdl(attention_join_kernel<DV, 1, true>, static_cast<unsigned>((parts.rows + 3) / 4), 128, 0, stream,
+                      parts, plan.pieces, static_cast<__nv_bfloat16*>(a.out), a.lse);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_fp8_tiles(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a,
+                                       const float* k_scale, const float* v_scale, const AttentionPlan& plan,
+                                       int more_rows, int num_sms, cudaStream_t stream) {
+    const Scales scales = {k_scale, v_scale};
+    switch (a.cache.dk) {
+        case 64: return launch_tiles<64, 64>(maps, a, scales, plan, more_rows, num_sms, stream);
+        case 128: return launch_tiles<128, 128>(maps, a, scales, plan, more_rows, num_sms, stream);
+        default: return launch_tiles<192, 128>(maps, a, scales, plan, more_rows, num_sms, stream);
+    }
+}
+
+cudaError_t launch_attention_fp8_tiles_join(const fp8bs_paged_attention_args& a, const AttentionPlan& plan,
+                                            cudaStream_t stream) {
+    return a.cache.dv == 64 ? launch_join<64>(a, plan, stream) : launch_join<128>(a, plan, stream);
+}
+
+cudaError_t read_error_attention_fp8_tiles(unsigned int* out, bool clear, cudaStream_t stream) {
+    return read_tu_error(out, clear, stream);
+}
+
+}  // namespace fp8bs

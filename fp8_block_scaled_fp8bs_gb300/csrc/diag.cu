@@ -44,7 +44,7 @@ cudaError_t launch_probe_wait(uint64_t timeout_ns, cudaStream_t stream) {
 }
 
 cudaError_t read_device_error(unsigned int* out, bool clear, cudaStream_t stream) {
-    unsigned int words[10] = {};
+    unsigned int words[11] = {};
     cudaError_t e = read_tu_error(&words[0], clear, stream);
     if (e == cudaSuccess) e = read_error_tn(&words[1], clear, stream);
     if (e == cudaSuccess) e = read_error_bs(&words[2], clear, stream);
@@ -55,6 +55,7 @@ cudaError_t read_device_error(unsigned int* out, bool clear, cudaStream_t stream
     if (e == cudaSuccess) e = read_error_moe(&words[7], clear, stream);
     if (e == cudaSuccess) e = read_error_norm_rope_fp8(&words[8], clear, stream);
     if (e == cudaSuccess) e = read_error_attention_fp8(&words[9], clear, stream);
+    if (e == cudaSuccess) e = read_error_attention_fp8_tiles(&words[10], clear, stream);
     if (e == cudaSuccess && clear) e = reset_static_workspace_counters(stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     *out = 0;

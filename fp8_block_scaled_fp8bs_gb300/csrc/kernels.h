@@ -200,6 +200,7 @@ struct AttentionPlan {
     int piece_len;     // keys per piece, a multiple of the key tile
 };
 AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms);
+AttentionPlan attention_plan(const fp8bs_paged_attention_args& a, int num_sms, bool two);     // of that many query tiles
 size_t attention_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan);
 // How keys and values are fetched, by mode:
 //   0  5-D map {64 channels, 8 slots, heads * d/64, page_size/8, pages}: pages of a multiple of 8 slots, heads
@@ -215,20 +216,29 @@ cudaError_t launch_paged_attention(const CUtensorMap& tmK, const CUtensorMap& tm
                                    const fp8bs_paged_attention_args& a, const AttentionModes& modes,
                                    const AttentionPlan& plan, int num_sms, cudaStream_t stream);
 
-// Attention over a paged cache of e4m3 codes (fp8bs_paged_attention_fp8); plan and workspace as above. The maps are
+// Attention over a paged cache of e4m3 codes (fp8bs_paged_attention_fp8). The maps are
 // 4-D, {d codes, heads, slots, pages}, with boxes of 2^box_log2 slots of one head, swizzled by the box's row: `key
 // chunk` codes of a key, all of a value.
 struct AttentionMapsFp8 {
     CUtensorMap k, v;
     int box_log2;
 };
+// Sequences of up to kFewRows rows (query tokens times query heads of a key head) are computed by one kernel
+// (attention_fp8.cu), the others by another (attention_fp8_tiles.cu); a call that may have both runs both.
+constexpr int kFewRows = 32;
 int attention_fp8_box_log2(const fp8bs_kv_cache& c);
 int attention_fp8_key_chunk(int64_t dk);
-AttentionPlan attention_fp8_plan(const fp8bs_paged_attention_args& a, int num_sms);
-size_t attention_fp8_workspace(const fp8bs_paged_attention_args& a, const AttentionPlan& plan);
+size_t attention_fp8_workspace(const fp8bs_paged_attention_args& a, int num_sms);
 cudaError_t launch_paged_attention_fp8(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a,
+                                       const float* k_scale, const float* v_scale, int num_sms, cudaStream_t stream);
+
+// Its part for sequences of more than kFewRows rows: the kernel (more_rows: those of that many rows or fewer are not its
+// own) and, where the plan has pieces, the join, as calls of their own. Their workspace stands at `a.workspace`.
+cudaError_t launch_attention_fp8_tiles(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a,
                                        const float* k_scale, const float* v_scale, const AttentionPlan& plan,
-                                       int num_sms, cudaStream_t stream);
+                                       int more_rows, int num_sms, cudaStream_t stream);
+cudaError_t launch_attention_fp8_tiles_join(const fp8bs_paged_attention_args& a, const AttentionPlan& plan,
+                                            cudaStream_t stream);
 
 // Mixture-of-experts layer for a few tokens. The workspace's parts, in bytes from its start.
 constexpr int kMoeMaxTokens = 64;
@@ -280,6 +290,7 @@ cudaError_t read_error_swapab(unsigned int* out, bool clear, cudaStream_t stream
 cudaError_t read_error_linear(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_norm_rope(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_attention(unsigned int* out, bool clear, cudaStream_t stream);
+cudaError_t read_error_attention_fp8_tiles(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_norm_rope_fp8(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_attention_fp8(unsigned int* out, bool clear, cudaStream_t stream);
 cudaError_t read_error_moe(unsigned int* out, bool clear, cudaStream_t stream);
