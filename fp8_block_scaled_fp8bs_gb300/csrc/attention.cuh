@@ -67,7 +67,8 @@ __device__ __forceinline__ Cut cut_of(const fp8bs_paged_attention_args& a, int r
     return c;
 }
 
-// more_rows: sequences of so many rows or fewer have no items here.
+// SOME: sequences of more_rows rows or fewer have no items.
+template <bool SOME>
 __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_attention_args& a, int rows,
                                                int piece_len, int lane, int more_rows) {
     const int group = static_cast<int>(a.q_heads / a.cache.heads);
@@ -84,7 +85,7 @@ __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_
         f.units[i] = 0;
         if (n > a.max_q_len || f.kv[i] > a.max_kv_len) {
             f.units[i] = 1;      // out of bounds: handed out once, to be reported
-        } else if (n > 0 && static_cast<int64_t>(n) * group > more_rows) {
+        } else if (n > 0 && (!SOME || static_cast<int64_t>(n) * group > more_rows)) {
             const Cut c = cut_of(a, rows, piece_len, n, f.kv[i], group);
             f.units[i] = c.tiles * c.pieces;
         }
@@ -99,6 +100,7 @@ __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_
     f.loaded = true;
 }
 
+template <bool SOME>
 __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_attention_args& a, int item, int rows,
                                           int bn, int piece_len, int lane, int more_rows) {
     Item it;
@@ -108,7 +110,7 @@ __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_atten
     const int unit = item / heads;
     it.head = item - unit * heads;
     while (f.base < a.B) {
-        if (!f.loaded) load_sequences(f, a, rows, piece_len, lane, more_rows);
+        if (!f.loaded) load_sequences<SOME>(f, a, rows, piece_len, lane, more_rows);
         const unsigned hit = __ballot_sync(0xffffffffu, f.before + f.incl > unit);
         if (hit) {
             const int src = __ffs(hit) - 1;

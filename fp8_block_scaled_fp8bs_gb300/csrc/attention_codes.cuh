@@ -36,6 +36,11 @@ __device__ __forceinline__ void two_codes(float x, float y, uint32_t* hi, uint32
     *lo = pack_e4m3x2(x - h.x, y - h.y);
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 struct Scales {
     const float *k, *v;          // [pages, heads]
 };

@@ -10,8 +10,10 @@ namespace {
 constexpr float kRescale = 8.0f;
 
 // CODES: the cache holds e4m3 codes. The keys' product then takes them as they are, and each query as the sum of two
-// e4m3 numbers per channel (their products go to one S); values are widened to bf16, their page's scale with them, by
-// four warps of their own on the way from a ring of codes to the ring of values.
+// e4m3 numbers per channel (their products go to one S). The keys' scale joins the softmax's factor, 16 keys at a time,
+// and the values' its exponent (P = exp2(c ks S + log2 vs - m), so that pages whose values differ in size share a tile);
+// the row sum takes it out again. Values are widened to binary16 by four warps of their own, on the way from a ring of
+// codes to the ring of values, and P is binary16 too (2^-12 of it, and 2^-25 of the reference's).
 template <int DK_, int DV_, int NQ_, bool CODES_ = false>
 struct AttnCfg {
     static constexpr int DK = DK_, DV = DV_, NQ = NQ_;
@@ -176,32 +178,22 @@ __device__ __forceinline__ bool bring_tiles(Stream& s, const CUtensorMap* map, c
     return true;
 }
 
-// Eight bf16 numbers of eight codes times `factor` * 2^-120: a code's bits in the place of bf16's sign, the low four of
-// its exponent and the high three of its significand are the code times 2^-120.
-__device__ __forceinline__ void widen8(uint32_t w0, uint32_t w1, __nv_bfloat162 factor, uint32_t* out) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w = i < 2 ? w0 : w1;
-        const uint32_t y = __byte_perm(w, 0, i & 1 ? 0x3424 : 0x1404);         // two codes, each in a high byte
-        const uint32_t bits = (y & 0x80008000u) | (y >> 4 & 0x07F007F0u);
-        const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&bits), factor);
-        out[i] = *reinterpret_cast<const uint32_t*>(&z);
-    }
-}
-
-// Two codes, of which one may be NaN.
-__device__ __forceinline__ uint32_t widen2_nan(uint32_t pair, float scale) {
-    const float2 f = e4m3x2_values(pair);
-    return pack_bf16x2(f.x * scale, f.y * scale);
-}
-
-// Four warps: values from codes to bf16, in the order of the key tiles; those that do not count become zeros (whatever
-// stood there must not meet a probability of zero). Per 16 codes a 16-byte load, two stores and about 40 instructions.
+// Four warps: values from codes to binary16, which holds them exactly, in the order of the key tiles; those that do not
+// count become zeros (whatever stood there must not meet a probability of zero). Per 16 codes a load, eight conversions
+// and two stores. (As bf16, the page's scale with them, it took 45 instructions, and 5700 cycles a tile of 128 x 128,
+// twice what the products and the softmax of two query tiles take: the chunk of 4096 585 us.)
 template <class Cfg>
-__device__ __forceinline__ void widen_values(const Item* s_item, const float (*s_vs)[8], const uint8_t* sVC, uint8_t* sV,
+__device__ __forceinline__ void widen_values(const Item* s_item, const uint8_t* sVC, uint8_t* sV,
                                              uint64_t* vc_full, uint64_t* vc_empty, uint64_t* v_full, uint64_t* v_empty,
                                              uint64_t* i_full, uint64_t* i_empty, int w, int lane) {
     constexpr int BN = Cfg::BN, DV = Cfg::DV, PIECES = DV / 16;      // 16 codes each, of a key
+    constexpr int STEP = 128 / PIECES, ROUNDS = BN / STEP;           // keys at a time (8 of them or more: the swizzle is the
+                                                                     // same for all of a thread's)
+    static_assert(STEP % 8 == 0 && BN % STEP == 0, "rounds of whole groups of 8 keys");
+    const int first = (w * 32 + lane) / PIECES, c = lane % PIECES;   // a thread's first key, its piece
+    const int in = first * DV + (swizzled(first, c, DV) << 4);
+    const int out_block = (first >> 3) * (DV / 64 * 1024) + (2 * c / 8) * 1024 + (first & 7) * 128;
+    const int place0 = ((2 * c % 8) ^ (first & 7)) << 4, place1 = ((2 * c % 8 + 1) ^ (first & 7)) << 4;
     bool ok = true;
     int n = 0;
     for (int x = 0; ok; ++x) {
@@ -219,44 +211,25 @@ __device__ __forceinline__ void widen_values(const Item* s_item, const float (*s
             ok = warp_wait(&vc_full[from], (n / Cfg::VCST) & 1) && warp_wait(&v_empty[to], ((n / Cfg::VST) & 1) ^ 1);
             if (!ok) break;
             const int key0 = k0 + j * BN;
-            const int lo = max(key_lo, key0), hi = min(kv, key0 + BN);    // (keys before a window are not brought whole)
-            const uint8_t* src = sVC + from * Cfg::VC_TILE;
-            uint8_t* dst = sV + to * Cfg::V_TILE;
+            const int lo = key_lo - key0, hi = kv - key0;             // keys of the tile that count
+            const uint8_t* src = sVC + from * Cfg::VC_TILE + in;
+            uint8_t* dst = sV + to * Cfg::V_TILE + out_block;
+            const bool part = lo > 0 || hi < BN;
 #pragma unroll 4
-            for (int e = w * 32 + lane; e < BN * PIECES; e += 128) {
-                const int key = e / PIECES, c = e % PIECES;
-                uint32_t out[8] = {};
-                if (key0 + key >= lo && key0 + key < hi) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + key * DV + (swizzled(key, c, DV) << 4));
-                    const float scale = s_vs[from][key >> 4];
-                    // (2^120 times a scale up to 2^7 is a bf16 number; larger scales go in two steps)
-                    const __nv_bfloat162 factor = __float2bfloat162_rn(fminf(scale, 128.0f) * 0x1p120f);
-                    widen8(v.x, v.y, factor, out);
-                    widen8(v.z, v.w, factor, out + 4);
-                    if (scale > 128.0f) {
-                        const __nv_bfloat162 more = __float2bfloat162_rn(scale * 0x1p-7f);
+            for (int i = 0; i < ROUNDS; ++i) {
+                uint4 v = *reinterpret_cast<const uint4*>(src + i * (STEP * DV));
+                if (part && (i * STEP + first < lo || i * STEP + first >= hi)) v = make_uint4(0, 0, 0, 0);
+                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+                uint32_t out[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&out[i]), more);
-                            out[i] = *reinterpret_cast<const uint32_t*>(&z);
-                        }
-                    }
-                    // a code that is NaN: its low seven bits are ones
-                    const uint32_t nan = ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                                         ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
-                    if (nan & 0x80808080u) {
-                        const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) out[i] = widen2_nan(words[i / 2] >> (16 * (i & 1)) & 0xFFFFu, scale);
-                    }
+                for (int k = 0; k < 8; ++k) {
+                    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
+                        static_cast<__nv_fp8x2_storage_t>(words[k / 2] >> (16 * (k & 1)) & 0xFFFFu), __NV_E4M3));
+                    out[k] = *reinterpret_cast<const uint32_t*>(&h);
                 }
-                uint8_t* block = dst + (key >> 3) * (DV / 64 * 1024) + (2 * c / 8) * 1024 + (key & 7) * 128;
-                const uint4 first = make_uint4(out[0], out[1], out[2], out[3]);
-                const uint4 second = make_uint4(out[4], out[5], out[6], out[7]);
-                // (the two halves of a row the other way round: eight lanes' stores then meet no bank twice)
-                const int p = 2 * c % 8, turn = 2 * c / 8;
-                *reinterpret_cast<uint4*>(block + (((p + turn) ^ (key & 7)) << 4)) = turn ? second : first;
-                *reinterpret_cast<uint4*>(block + (((p + 1 - turn) ^ (key & 7)) << 4)) = turn ? first : second;
+                uint8_t* row = dst + i * (STEP / 8 * (DV / 64) * 1024);
+                *reinterpret_cast<uint4*>(row + place0) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(row + place1) = make_uint4(out[4], out[5], out[6], out[7]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -282,8 +255,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     __shared__ Item s_item[Cfg::SLOTS];
     __shared__ int2 s_window[2][32];                      // (page, slot) of 32 boxes: keys', values'
     __shared__ float s_unit[CODES ? NQ * 128 : 1];        // codes: what a row's queries have been divided by
-    __shared__ __align__(16) float s_ks[CODES ? Cfg::CST : 1][8];     // scales of 16 keys each
-    __shared__ float s_vs[CODES ? Cfg::VCST : 1][8];
+    __shared__ float4 s_scale[CODES ? Cfg::CST : 1][8];   // of 16 keys each: ks, log2 vs, 1 / vs
     __shared__ uint32_t s_tmem;
     uint8_t* smem = align_1024(smem_raw);
     uint8_t* sQ = smem;                                   // [NQ][DK/64][128 rows][128 bytes]; codes: [NQ][2][DK/CHK][..][CHK]
@@ -507,7 +479,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 // pieces that this sequence does not have are empty
                 for (int p = it.pieces; p < pieces; ++p)
                     parts.ml[p * parts.rows + out_row(it, r)] = make_float2(-INFINITY, 0.0f);
-            float m = -INFINITY;           // maximum in use, raw score (codes: times its key's scale)
+            float m = -INFINITY;           // maximum in use, raw score (codes: in log2 units, its value's scale with it)
             float l = 0.0f;
             const float c = CODES ? max_nan(c_all * s_unit[r], 1e-30f) : c_all;
             if (nt > 0) {
@@ -530,13 +502,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                             break;
                         }
                     }
+                    // (of 16 keys each, on hand before the scores are: a factor that keeps -inf apart even where the
+                    // score's is next to nothing; log2 vs; 1 / vs)
+                    float ck[CODES ? BN / 16 : 1], lv[CODES ? BN / 16 : 1], iv[CODES ? BN / 16 : 1];
+                    if constexpr (CODES)
+#pragma unroll
+                        for (int g = 0; g < BN / 16; ++g) {
+                            const float4 sc = s_scale[n % Cfg::CST][g];
+                            ck[g] = max_nan(c * sc.x, 1.2e-38f), lv[g] = sc.y, iv[g] = sc.z;
+                        }
                     if (!warp_wait(&s_full[buf], sph)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     if (!idle) {
-                        const float* ks = s_ks[CODES ? n % Cfg::CST : 0];
                         const uint32_t s_tmem_row = tmem + lanes + buf * BN;
                         const int kb = k0 + j * BN;
                         const bool masked = kb < full_lo || kb + BN > full_hi;
@@ -554,12 +534,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                         if (k < lo || k >= hi) s[k] = -INFINITY;
                                 }
                             };
-                            float top = m;
                             auto probabilities = [&]() {
-                                const float mc = m == -INFINITY ? 0.0f : m * c;
-                                const float2 mc2 = make_float2(-mc, -mc);
-                                sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-                                float mx[2] = {-INFINITY, -INFINITY};
+                                const float ref = m == -INFINITY ? 0.0f : m;
+                                float total = 0.0f, size = 0.0f;
                                 float s[2][32];
                                 load_block(0, s[0]);
 #pragma unroll
@@ -570,32 +547,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                     mask_block(i, now);
 #pragma unroll
                                     for (int g = 0; g < 2; ++g) {            // 16 keys of one scale
-                                        const float k1 = ks[2 * i + g];
-                                        const float ck = max_nan(c * k1, 1.2e-38f);
-                                        const float2 c2 = make_float2(ck, ck);
-                                        float of16[2] = {-INFINITY, -INFINITY};
+                                        const float off = lv[2 * i + g] - ref;
+                                        const float2 c2 = make_float2(ck[2 * i + g], ck[2 * i + g]);
+                                        const float2 off2 = make_float2(off, off);
+                                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
                                         for (int k = 0; k < 8; ++k) {
                                             const float2 z = make_float2(now[16 * g + 2 * k], now[16 * g + 2 * k + 1]);
-                                            of16[k & 1] = fmaxf(of16[k & 1], fmaxf(z.x, z.y));
-                                            float2 y = __ffma2_rn(z, c2, mc2);
+                                            float2 y = __ffma2_rn(z, c2, off2);
                                             y.x = exp2_fast(y.x);
                                             y.y = exp2_fast(y.y);
                                             sum[k & 1] = __fadd2_rn(sum[k & 1], y);
-                                            p[16 * i + 8 * g + k] = pack_bf16x2(y.x, y.y);
+                                            p[16 * i + 8 * g + k] = pack_half2(y.x, y.y);
                                         }
-                                        mx[g] = fmaxf(mx[g], fmaxf(of16[0], of16[1]) * k1);
+                                        const float2 both = __fadd2_rn(sum[0], sum[1]);
+                                        total = fmaf(both.x + both.y, iv[2 * i + g], total);
+                                        size += both.x + both.y;
                                     }
                                 }
-                                top = fmaxf(mx[0], mx[1]);
+                                sum[0] = make_float2(total, 0.0f);
+                                sum[1] = make_float2(0.0f, 0.0f);
+                                return size;
                             };
+                            // The maximum is not looked for where it is not needed: probabilities above 1 are as good as
+                            // others until their sum says that one may be past 2^13, of the 2^16 that binary16 holds.
                             bool look = j == 0 || __any_sync(0xffffffffu, m == -INFINITY);
-                            if (!look) {
-                                probabilities();
-                                look = __any_sync(0xffffffffu, (top - m) * c > kRescale);
-                            }
+                            if (!look) look = __any_sync(0xffffffffu, probabilities() > 8192.0f);
                             if (look) {
-                                top = -INFINITY;
+                                float top = -INFINITY;
 #pragma unroll 1
                                 for (int i = 0; i < BN / 32; ++i) {
                                     float s[32];
@@ -607,14 +586,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                         float of16[2] = {s[16 * g], s[16 * g + 1]};
 #pragma unroll
                                         for (int k = 2; k < 16; ++k) of16[k & 1] = fmaxf(of16[k & 1], s[16 * g + k]);
-                                        top = fmaxf(top, fmaxf(of16[0], of16[1]) * ks[2 * i + g]);
+                                        const float4 sc = s_scale[n % Cfg::CST][2 * i + g];
+                                        top = fmaxf(top, fmaf(fmaxf(of16[0], of16[1]), max_nan(c * sc.x, 1.2e-38f), sc.y));
                                     }
                                 }
-                                const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
-                                const float keep = grow ? exp2_fast((m - top) * c) : 1.0f;
+                                const bool grow = top > m;
+                                const float keep = grow ? exp2_fast(m - top) : 1.0f;
                                 if (grow) m = top;
                                 l *= keep;
-                                probabilities();
+                                (void)probabilities();
                                 if (j > 0 && __any_sync(0xffffffffu, grow)) {
                                     if (!warp_wait(&o_done[q], (n - 1) & 1)) {
                                         ok = false;
@@ -729,7 +709,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
             if (ok && !idle) {
                 const int64_t row = live ? out_row(it, r) : 0;
-                const float mc = m == -INFINITY ? -INFINITY : m * c;
+                const float mc = m == -INFINITY ? -INFINITY : CODES ? m : m * c;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;       // (NaN stays NaN)
                 if (!whole) {
                     float* dst = parts.o + (it.piece * parts.rows + row) * DV;
@@ -792,7 +772,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             // tiles only: few rows mean pieces of one length, and a batch of 9 us takes 0.3 more with it.)
             int ctas = gridDim.x, mine = blockIdx.x, start = 0, rounds = INT32_MAX;
             if (NQ == 2 && __builtin_expect(a.B == 1, 0)) {
-                load_sequences(finder, a, Cfg::ROWS, piece_len, lane, CODES ? more_rows : 0);
+                load_sequences<CODES>(finder, a, Cfg::ROWS, piece_len, lane, more_rows);
                 const int items = __shfl_sync(0xffffffffu, finder.incl, 31) * static_cast<int>(a.cache.heads);
                 const int whole = items / ctas, more = items % ctas;
                 if (mine < ctas - more) {
@@ -809,8 +789,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const int64_t at = round < rounds ? start + static_cast<int64_t>(round) * ctas +
                                                         (round & 1 ? ctas - 1 - mine : mine)
                                                   : int64_t{INT32_MAX};
-                const Item it = find_item(finder, a, static_cast<int>(min(at, int64_t{INT32_MAX})), Cfg::ROWS,
-                                          BN, piece_len, lane, CODES ? more_rows : 0);
+                const Item it = find_item<CODES>(finder, a, static_cast<int>(min(at, int64_t{INT32_MAX})), Cfg::ROWS,
+                                          BN, piece_len, lane, more_rows);
                 if (it.seq == -2) {
                     if (lane == 0) record_error(FP8BS_DEVERR_INDEX);
                     continue;
@@ -830,11 +810,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 if (nt == 0) continue;
                 if constexpr (CODES) {
                     ok = bring_codes<Cfg::KST, DK, Cfg::CHK, BN, true>(
-                        ks, &tmK, a, Scales{scales.k, nullptr}, it, first_tile(it), nt, modes.box_log2, sK, k_full, k_empty,
+                        ks, &tmK, a, scales, it, first_tile(it), nt, modes.box_log2, sK, k_full, k_empty,
                         nullptr, lane, warp_wait, [&](int, int tile, int first, float2 f) {
                             const int cs = tile % Cfg::CST;
-                            const float k1 = __shfl_sync(0xffffffffu, f.x, (first + (lane * 16 >> modes.box_log2)) & 31);
-                            if (lane < BN / 16) s_ks[cs][lane] = k1;
+                            const int from = (first + (lane * 16 >> modes.box_log2)) & 31;
+                            const float k1 = __shfl_sync(0xffffffffu, f.x, from), v1 = __shfl_sync(0xffffffffu, f.y, from);
+                            const float lv = static_cast<float>(static_cast<int>(__float_as_uint(v1) >> 23) - 127);
+                            if (lane < BN / 16) s_scale[cs][lane] = make_float4(k1, lv, exp2_fast(-lv), 0.0f);
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&c_full[cs]);
                         });
@@ -864,12 +846,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 if (nt == 0) continue;
                 if constexpr (CODES) {
                     ok = bring_codes<Cfg::VCST, DV, DV, BN, false>(
-                        vs, &tmV, a, Scales{nullptr, scales.v}, it, first_tile(it), nt, modes.box_log2, sVC, vc_full,
-                        vc_empty, nullptr, lane, warp_wait, [&](int st, int, int first, float2 f) {
-                            const float v1 = __shfl_sync(0xffffffffu, f.y, (first + (lane * 16 >> modes.box_log2)) & 31);
-                            if (lane < BN / 16) s_vs[st][lane] = v1;
-                            __syncwarp();
-                        });
+                        vs, &tmV, a, Scales{nullptr, nullptr}, it, first_tile(it), nt, modes.box_log2, sVC, vc_full,
+                        vc_empty, nullptr, lane, warp_wait, [](int, int, int, float2) {});
                     continue;
                 }
                 ok = bring_tiles<Cfg, false>(vs, &tmV, a, it, first_tile(it), nt, modes.box_log2, modes.v, sV,
@@ -886,14 +864,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
         } else if (CODES && warp >= Cfg::WIDEN_WARP) {
             if constexpr (CODES)
-                widen_values<Cfg>(s_item, s_vs, sVC, sV, vc_full, vc_empty, v_full, v_empty, i_full, i_empty,
+                widen_values<Cfg>(s_item, sVC, sV, vc_full, vc_empty, v_full, v_empty, i_full, i_empty,
                                   warp - Cfg::WIDEN_WARP, lane);
         } else if (warp == Cfg::MMA_WARP) {
             // ---- MMA issuer. Per key tile and query tile: O += P(j) V(j), then S of the tile's next keys, which
             // takes P's place (the tensor core works in order).
             // With two query tiles one's products run under the other's softmax.
             constexpr uint32_t idesc_qk = CODES ? idesc_e4m3_f32(128, BN) : idesc_bf16_f32(128, BN);
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DV) | kIdescBMajorMN;
+            // (codes: P and V in binary16, whose format is the descriptor's zero)
+            constexpr uint32_t idesc_pv =
+                (idesc_bf16_f32(128, DV) & ~(CODES ? 1u << 7 | 1u << 10 : 0u)) | kIdescBMajorMN;
             // descriptors of the first stages; those of other stages and steps lie at constant distances (in
             // units of 16 bytes, which do not carry out of the address field)
             const uint64_t q_desc =
