@@ -45,11 +45,12 @@ __host__ __device__ inline int64_t key_span(const fp8bs_paged_attention_args& a,
 
 // The work items in order, for one warp: sequences in order, in each the row tiles from the last (whose keys
 // are the most) to the first, for each tile its pieces, for each piece the key heads (which read the same
-// slots). Calls ask for rising items; the sequences are read 256 at a time, eight per lane.
+// slots). Calls ask for rising items; the sequences are read 32 PER at a time, PER per lane.
+template <int PER>
 struct ItemFinder {
     int base, before;       // first sequence of the chunk in hand, units (items / heads) before it
-    int start[9], kv[8];    // lane's sequences: first query tokens (and the next one's), keys
-    int units[8];           // of each
+    int start[PER + 1], kv[PER];   // lane's sequences: first query tokens (and the next one's), keys
+    int units[PER];         // of each
     int incl, sum;          // of the chunk up to and with this lane, of this lane
     bool loaded;
 };
@@ -68,19 +69,19 @@ __device__ __forceinline__ Cut cut_of(const fp8bs_paged_attention_args& a, int r
 }
 
 // SOME: sequences of more_rows rows or fewer have no items.
-template <bool SOME>
-__device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_attention_args& a, int rows,
+template <bool SOME, int PER>
+__device__ __forceinline__ void load_sequences(ItemFinder<PER>& f, const fp8bs_paged_attention_args& a, int rows,
                                                int piece_len, int lane, int more_rows) {
     const int group = static_cast<int>(a.q_heads / a.cache.heads);
     f.sum = 0;
 #pragma unroll
-    for (int i = 0; i < 9; ++i) {
-        const int64_t b = f.base + 8 * lane + i;
+    for (int i = 0; i < PER + 1; ++i) {
+        const int64_t b = f.base + PER * lane + i;
         f.start[i] = a.q_start[b < a.B ? b : a.B];
-        if (i < 8) f.kv[i] = b < a.B ? a.kv_len[b] : 0;
+        if (i < PER) f.kv[i] = b < a.B ? a.kv_len[b] : 0;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int n = f.start[i + 1] - f.start[i];
         f.units[i] = 0;
         if (n > a.max_q_len || f.kv[i] > a.max_kv_len) {
@@ -100,8 +101,8 @@ __device__ __forceinline__ void load_sequences(ItemFinder& f, const fp8bs_paged_
     f.loaded = true;
 }
 
-template <bool SOME>
-__device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_attention_args& a, int item, int rows,
+template <bool SOME, int PER>
+__device__ __forceinline__ Item find_item(ItemFinder<PER>& f, const fp8bs_paged_attention_args& a, int item, int rows,
                                           int bn, int piece_len, int lane, int more_rows) {
     Item it;
     it.seq = -1;
@@ -119,9 +120,9 @@ __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_atten
                 int left = unit - f.before - (f.incl - f.sum);
                 int mine = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < PER; ++i) {
                     if (left >= 0 && left < f.units[i]) {
-                        seq = f.base + 8 * lane + i;
+                        seq = f.base + PER * lane + i;
                         n = f.start[i + 1] - f.start[i];
                         q0 = f.start[i];
                         kv = f.kv[i];
@@ -155,7 +156,7 @@ __device__ __forceinline__ Item find_item(ItemFinder& f, const fp8bs_paged_atten
             return it;
         }
         f.before += __shfl_sync(0xffffffffu, f.incl, 31);
-        f.base += 256;
+        f.base += 32 * PER;
         f.loaded = false;
     }
     return it;

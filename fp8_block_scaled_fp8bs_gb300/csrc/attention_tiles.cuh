@@ -41,7 +41,7 @@ struct AttnCfg {
     // Codes: bytes of a key per swizzled chunk; tiles of values as codes; tiles' key scales, whose place is free when the
     // tile KST + 1 before has been read (the product that frees that key tile's place follows its P).
     static constexpr int CHK = DK % 128 == 0 ? 128 : 64;
-    static constexpr int VC_TILE = CODES ? BN * DV : 0, VCST = CODES ? 2 : 0;
+    static constexpr int VC_TILE = CODES ? BN * DV : 0, VCST = !CODES ? 0 : DK == 64 ? 4 : 2;
     static constexpr int CST = CODES ? KST + 1 : 0;
     static constexpr int READERS = SOFT_WARPS + 2 + (CODES ? 4 : 0);         // warps that read a work item
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
@@ -759,7 +759,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         if constexpr (NQ == 2) regs_dec<CODES ? 64 : 80>();
         if (warp == Cfg::KEY_WARP) {
             // ---- hands out the items and brings their keys
-            ItemFinder finder;
+            // (codes: two sequences a lane, so that the first item is on hand sooner: a mixed batch of 8 62 -> 59 us)
+            ItemFinder<CODES ? 2 : 8> finder;
             finder.base = finder.before = 0;
             finder.loaded = false;
             bool ok = true;
