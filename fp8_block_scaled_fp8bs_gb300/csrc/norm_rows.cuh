@@ -40,6 +40,8 @@ struct TokenRows {
     float eps, inv_d;
 
     // Norm (w: the lane's weights) and rotation of one row's chunks, in binary32; every lane of the warp calls it.
+    // REFINE: the reciprocal root with a step of Newton's method, to about half its last bit (codes have borders).
+    template <bool REFINE = false>
     __device__ __forceinline__ void values(const Chunk16& x, const float2* w, bool norm, float2* f) const {
         unpack16(x, f);
         if (norm) {
@@ -49,7 +51,12 @@ struct TokenRows {
             float ss = s2.x + s2.y;
 #pragma unroll
             for (int m = LPR / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            const float inv = rsqrtf(fmaf(ss, inv_d, eps));
+            const float mean = fmaf(ss, inv_d, eps);
+            float inv = rsqrtf(mean);
+            if constexpr (REFINE) {
+                const float better = fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.0f), inv);
+                if (better == better) inv = better;              // (a mean of 0 or infinity: the root stands)
+            }
             const float2 i2 = make_float2(inv, inv);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], i2), w[i]);
