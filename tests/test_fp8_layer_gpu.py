@@ -293,6 +293,25 @@ def test_write_chunks(T, page, off):
     write_check(cache, slots=torch.arange(off + page, off + page + T, device="cuda"), **x)
 
 
+@pytest.mark.parametrize("dk,dv,rot", [(64, 64, 64), (128, 128, 128), (192, 128, 64)])
+@pytest.mark.parametrize("T,page", [(511, 512), (512, 80), (700, 512)])
+@pytest.mark.parametrize("heads", [1, 5])
+def test_write_windows(dk, dv, rot, T, page, heads):
+    # runs longer than what a block keeps, and those that end in the next block's tokens, in pages that are held in
+    # part and whose scales grow; tables of cosines at odd addresses
+    off = 37
+    pages = (T + off) // page + 3
+    cache = empty_cache(pages, page, heads, dk, dv)
+    x = write_inputs(T + heads, off, heads, heads, dk, dv, rot, True, scale=0.01)
+    write_check(cache, slots=torch.arange(page, page + off, device="cuda"), **x)
+    x = write_inputs(T, T, 2 * heads, heads, dk, dv, rot, True)
+    for name in ("cos", "sin"):
+        odd = torch.empty(x[name].numel() + 1, device="cuda")
+        odd[1:] = x[name].flatten()
+        x[name] = odd[1:].view(x[name].shape)
+    write_check(cache, slots=torch.arange(off + page, off + page + T, device="cuda"), **x)
+
+
 def test_write_chunk_of_many_sequences():
     # 2048 tokens and more: runs that begin anywhere among the tokens that one block looks at
     page, hk = 16, 2
