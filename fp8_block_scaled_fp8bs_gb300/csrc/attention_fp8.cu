@@ -208,13 +208,20 @@ __device__ __forceinline__ int64_t look_at(SequenceLook& f, int base, const fp8b
     const int group = static_cast<int>(a.q_heads / a.cache.heads);
     const int count = static_cast<int>(min(int64_t{256}, a.B - base));
     int64_t before = 0;
+    auto load = [&](int b) {                                 // first token, the next one's, keys
+        return b < count ? make_int3(a.q_start[base + b], a.q_start[base + b + 1], a.kv_len[base + b])
+                         : make_int3(0, 0, 0);
+    };
+    int3 next = load(lane);
     __syncwarp();
 #pragma unroll 1
     for (int i = 0; i < count; i += 32) {
         const int b = i + lane;
-        int64_t cost = 0;
+        const int3 seq = next;
+        next = load(b + 32);
+        int cost = 0;                                        // (2^24 tiles at most)
         if (b < count) {
-            const int q0 = a.q_start[base + b], n = a.q_start[base + b + 1] - q0, kv = a.kv_len[base + b];
+            const int q0 = seq.x, n = seq.y - q0, kv = seq.z;
             f.start[b] = q0;
             f.kv[b] = kv;
             if (b == count - 1) f.start[b + 1] = q0 + n;
@@ -225,10 +232,10 @@ __device__ __forceinline__ int64_t look_at(SequenceLook& f, int base, const fp8b
             else if (n > 0 && static_cast<int64_t>(n) * group <= rows)
                 cost = tiles_of_rows(a, n, kv).tiles + kItemTiles;
         }
-        int64_t incl = cost;
+        int incl = cost;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, m);
+            const int o = __shfl_up_sync(0xffffffffu, incl, m);
             if (lane >= m) incl += o;
         }
         if (b < count) f.at[b] = before + incl - cost;
@@ -237,6 +244,12 @@ __device__ __forceinline__ int64_t look_at(SequenceLook& f, int base, const fp8b
     if (lane == 0) f.at[count] = before;
     __syncwarp();
     return before;
+}
+
+// x * y / z of numbers that are not negative; in 32 bits, if they fit, which takes a fraction of the time.
+__device__ __forceinline__ int64_t part_of(int64_t x, int64_t y, int64_t z) {
+    const int64_t xy = x * y;
+    return (xy | z) >> 32 == 0 ? static_cast<int64_t>(static_cast<uint32_t>(xy) / static_cast<uint32_t>(z)) : xy / z;
 }
 
 // The sequence of a look that holds position `at` (one that counts something): the last that begins at or before it.
@@ -576,13 +589,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (B > 256) now = look_at(f, 0, a, plan.whole, R, lane);
         const int64_t chunks = min(static_cast<int64_t>(plan.chunks), max(all, int64_t{1}));
         for (int64_t id = blockIdx.x; ok && id < static_cast<int64_t>(plan.chunks) * heads; id += gridDim.x) {
-            const int64_t chunk = id / heads;
+            const int64_t chunk = part_of(id, 1, heads);
             const int head = static_cast<int>(id - chunk * heads);
             JoinHead join = {0, 0, 0, 0};
             if (chunk < chunks) {
                 // positions [at, end)
-                int64_t at = chunk * all / chunks;
-                const int64_t end = (chunk + 1) * all / chunks;
+                int64_t at = part_of(chunk, all, chunks);
+                const int64_t end = part_of(chunk + 1, all, chunks);
                 while (ok && at < end) {
                     // the look that holds `at` (chunks of a CTA rise)
                     while (at >= before + now) {
@@ -624,7 +637,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         it.slot = static_cast<int>(2 * id);
                         if (hi == t.tiles)
                             // chunk that holds the sequence's first tile: the last to begin at or before it
-                            join.first = static_cast<int>(((first + kItemTiles + 1) * chunks - 1) / all),
+                            join.first = static_cast<int>(part_of((first + kItemTiles + 1) * chunks - 1, 1, all)),
                             join.parts = static_cast<int>(chunk) - join.first + 1, join.q0 = it.q0, join.rows = it.rows;
                     } else if (hi < t.tiles) {
                         it.slot = static_cast<int>(2 * id + 1);
@@ -969,6 +982,7 @@ __global__ void __launch_bounds__(DV) attention_rows_join_kernel(const __grid_co
                                                                  const RowsParts parts) {
     grid_dependency_wait();
     grid_launch_dependents();
+    __shared__ float2 s_ml[DV];
     const JoinHead j = parts.head[blockIdx.x];
     if (j.parts == 0) return;
     const int heads = static_cast<int>(a.cache.heads);
@@ -978,15 +992,28 @@ __global__ void __launch_bounds__(DV) attention_rows_join_kernel(const __grid_co
     auto slot = [&](int i) { return (2 * (static_cast<int64_t>(j.first + i) * heads + head) + (i == 0 ? 1 : 0)) * R; };
     for (int r = blockIdx.y; r < j.rows; r += gridDim.y) {
         float top = kNoReference, l = 0.0f, o = 0.0f;
-        for (int i = 0; i < j.parts; ++i) top = fmaxf(top, parts.ml[slot(i) + r].x);
-#pragma unroll 4
-        for (int i = 0; i < j.parts; ++i) {
-            const float2 ml = parts.ml[slot(i) + r];
-            const float part = parts.o[(slot(i) + r) * DV + threadIdx.x];
-            // (no reference: no keys, or scores that are not numbers, which the sum says)
-            const float w = ml.x == kNoReference ? 0.0f : exp2_fast(ml.x - top);
-            l += ml.x == kNoReference ? ml.y : ml.y * w;
-            o = fmaf(w == 0.0f ? 0.0f : part, w, o);
+        for (int i0 = 0; i0 < j.parts; i0 += DV) {
+            // (references and sums of as many parts as there are threads, one each)
+            const int count = min(DV, j.parts - i0);
+            __syncthreads();
+            if (static_cast<int>(threadIdx.x) < count) s_ml[threadIdx.x] = parts.ml[slot(i0 + threadIdx.x) + r];
+            __syncthreads();
+            const float before = top;
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) top = fmaxf(top, s_ml[i].x);
+            if (i0 > 0) {
+                const float keep = before == kNoReference ? 1.0f : exp2_fast(before - top);
+                l *= keep, o *= keep;
+            }
+#pragma unroll 8
+            for (int i = 0; i < count; ++i) {
+                const float2 ml = s_ml[i];
+                const float part = parts.o[(slot(i0 + i) + r) * DV + threadIdx.x];
+                // (no reference: no keys, or scores that are not numbers, which the sum says)
+                const float w = ml.x == kNoReference ? 0.0f : exp2_fast(ml.x - top);
+                l += ml.x == kNoReference ? ml.y : ml.y * w;
+                o = fmaf(w == 0.0f ? 0.0f : part, w, o);
+            }
         }
         const int tok = r / group;
         const int64_t row = (j.q0 + tok) * a.q_heads + head * group + (r - tok * group);
