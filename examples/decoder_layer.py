@@ -1,17 +1,19 @@
 """One decoder layer of a mixture-of-experts model on the FP8 block-scaled path, served from a paged cache.
 
-    python examples/decoder_layer.py [--dim 2048] [--sequences 3] [--prompt 100] [--decode 8]
+    python examples/decoder_layer.py [--dim 2048] [--sequences 3] [--prompt 100] [--decode 8] [--codes]
 
 The layer is what a serving program calls for every step, with whatever new tokens there are -- the rest of a
 prompt, single tokens of other sequences, or both in one batch:
 
-    act_quant + fp8_gemm    q, k and v of the normalised input
+    rms_norm + fp8_gemm     q, k and v of the normalised input, which is only held as codes
     qk_norm_rope            norm and rotation of q and k per head; keys and values into their cache slots
     paged_attention         the new tokens over all keys of their sequences
     act_quant + fp8_gemm    output projection
+    rms_norm                residual addition and norm
     moe_layer               router, experts and weighted sum, 64 tokens at a time
 
-Weights are random, in the library's format: e4m3 codes with one fp32 scale per 128 x 128 block.
+Weights are random, in the library's format: e4m3 codes with one fp32 scale per 128 x 128 block. With --codes the
+cache holds e4m3 codes too, with one scale per page and head: half the bytes.
 """
 from __future__ import annotations
 
@@ -36,11 +38,6 @@ def quantised(g, *shape):
     blocks = (*shape[:-2], shape[-2] // BLOCK, shape[-1] // BLOCK)
     scales = torch.exp2(torch.rand(*blocks, generator=g, device="cuda") - 0.5)
     return codes, scales / (32 * shape[-1] ** 0.5)
-
-
-def rms_norm(x, w):
-    y = x.float()
-    return (y * torch.rsqrt(y.pow(2).mean(-1, keepdim=True) + 1e-6) * w.float()).bfloat16()
 
 
 class DecoderLayer:
@@ -69,7 +66,8 @@ class DecoderLayer:
         """x bf16 [T, dim] -> bf16 [T, dim]; the new tokens' keys and values go into the cache."""
         T = x.shape[0]
         hq, hk, d = self.q_heads, self.k_heads, self.head_dim
-        qkv = self.linear(rms_norm(x, self.attn_norm), self.wqkv)
+        n = fp8bs.rms_norm(x, self.attn_norm, quant="fp32")
+        qkv = fp8bs.fp8_gemm(n.y, n.s, *self.wqkv, weights_constant=True)
         q = qkv[:, :hq * d].unflatten(1, (hq, d))
         k = qkv[:, hq * d:(hq + hk) * d].unflatten(1, (hk, d))
         v = qkv[:, (hq + hk) * d:].unflatten(1, (hk, d))
@@ -77,12 +75,11 @@ class DecoderLayer:
                                k_weight=self.k_norm, cache=cache, v=v, slots=batch["slots"])
         o = fp8bs.paged_attention(q, cache, batch["page_table"], batch["q_start"], batch["kv_len"],
                                   max_q_len=batch["max_q_len"], max_kv_len=batch["max_kv_len"])
-        x = x + self.linear(o.flatten(1), self.wo)
-        h = rms_norm(x, self.moe_norm)
+        m = fp8bs.rms_norm(self.linear(o.flatten(1), self.wo), self.moe_norm, residual=x)
         most = fp8bs.MOE_MAX_TOKENS
-        y = [fp8bs.moe_layer(h[t:t + most], self.router, *self.w13, *self.w2, self.top_k,
+        y = [fp8bs.moe_layer(m.n[t:t + most], self.router, *self.w13, *self.w2, self.top_k,
                              bias=self.router_bias) for t in range(0, T, most)]
-        return x + torch.cat(y)
+        return m.h + torch.cat(y)
 
 
 class Pages:
@@ -120,8 +117,11 @@ class Pages:
         self.length.pop(s, None)
 
 
-def new_cache(layer, pages, page_size):
+def new_cache(layer, pages, page_size, codes=False):
     shape = (pages, page_size, layer.k_heads, layer.head_dim)
+    if codes:
+        return fp8bs.PagedCacheFp8(*(torch.zeros(shape, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)),
+                                   *(torch.zeros(pages, layer.k_heads, device="cuda") for _ in range(2)))
     return fp8bs.PagedCache(*(torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
 
 
@@ -131,10 +131,11 @@ def main():
     ap.add_argument("--sequences", type=int, default=3)
     ap.add_argument("--prompt", type=int, default=100)
     ap.add_argument("--decode", type=int, default=8)
+    ap.add_argument("--codes", action="store_true", help="a cache of e4m3 codes")
     a = ap.parse_args()
     layer = DecoderLayer(dim=a.dim)
     pages = Pages(256, 16)
-    cache = new_cache(layer, 256, 16)
+    cache = new_cache(layer, 256, 16, a.codes)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     tokens = lambda n: torch.randn(n, a.dim, generator=g, device="cuda").bfloat16()  # noqa: E731

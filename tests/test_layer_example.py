@@ -55,3 +55,23 @@ def test_pages_of_a_sequence(example):
         assert len(p.free) == 7 and 0 not in p.length
     finally:
         torch.tensor = real
+
+
+@pytest.mark.gpu
+def test_layer_over_a_cache_of_codes(example):
+    import torch
+    layer = example.DecoderLayer(dim=512, q_heads=8, k_heads=2, experts=8, inter=256)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn(60, 512, generator=g, device="cuda").bfloat16()
+    out = []
+    for codes in (False, True):
+        pages, cache = example.Pages(32, 16), example.new_cache(layer, 32, 16, codes)
+        y = [layer(x[:40], cache, pages.step({0: 40})), layer(x[40:57], cache, pages.step({1: 17}))]
+        y += [layer(x[57:59], cache, pages.step({0: 1, 1: 1})), layer(x[59:], cache, pages.step({1: 1}))]
+        out.append(torch.cat(y).double())
+    # A key and a value are off by 2^-4 of themselves at most, and so is o for either (a score moves by 2^-4 of the sum
+    # of its terms' sizes, about 3 here, and scores are about 1); o's share of a row, beside the residual and the
+    # experts, is well below a half.
+    assert float((out[0] - out[1]).norm() / out[0].norm()) < 0.1
+    assert not torch.equal(*out)
