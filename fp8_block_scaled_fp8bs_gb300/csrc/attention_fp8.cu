@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int64_t at = (it.q0 + tok) * a.q_token_stride +
                                (it.head * group + mine - tok * group) * a.q_head_stride;
             int my_e = 2;
-            constexpr int BATCH = 4;                                         // rows on their way at once
+            constexpr int BATCH = R == 32 ? 8 : 4;                           // rows on their way at once
 #pragma unroll 1
             for (int r0 = 0; r0 < R; r0 += BATCH) {
                 uint32_t v[BATCH][PARTS][PER / 2];
