@@ -1024,9 +1024,12 @@ __global__ void __launch_bounds__(DV) attention_rows_join_kernel(const __grid_co
     }
 }
 
-// Rows per item: the smallest form that holds the longest sequence's.
+// Rows per item: the smallest form that holds the longest sequence's; where those of many rows go to the other kernel,
+// that holds a single token's, and all longer ones go there (a chunk of 256 beside 200 single tokens, groups of 4 heads:
+// 140 us; with the form of 32 rows for them 240).
 int row_form(const fp8bs_paged_attention_args& a) {
-    const int64_t rows = a.max_q_len * (a.q_heads / a.cache.heads);
+    const int64_t group = a.q_heads / a.cache.heads;
+    const int64_t rows = a.max_q_len * group <= kFewRows ? a.max_q_len * group : group;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : kFewRows;
 }
 
@@ -1103,7 +1106,8 @@ Fp8Plan fp8_plan(const fp8bs_paged_attention_args& a, int num_sms) {
     Fp8Plan p = {};
     const int64_t rows = a.max_q_len * (a.q_heads / a.cache.heads);
     p.tiles = rows > kFewRows;
-    p.few = !p.tiles || a.T != a.B * a.max_q_len;          // (else all sequences are alike)
+    // (both: unless all sequences are alike, or a single token has too many rows)
+    p.few = !p.tiles || (a.T != a.B * a.max_q_len && a.q_heads / a.cache.heads <= kFewRows);
     if (p.tiles) {
         p.of_tiles = attention_plan(a, num_sms, true);
         if (p.of_tiles.pieces > 1) p.tile_bytes = (p.of_tiles.pieces * part_bytes(a) + 255) / 256 * 256;
@@ -1139,7 +1143,7 @@ cudaError_t launch_paged_attention_fp8(const AttentionMapsFp8& maps, const fp8bs
     const Fp8Plan p = fp8_plan(a, num_sms);
     cudaError_t e = cudaSuccess;
     if (p.tiles)
-        e = launch_attention_fp8_tiles(maps, a, k_scale, v_scale, p.of_tiles, kFewRows, num_sms, stream);
+        e = launch_attention_fp8_tiles(maps, a, k_scale, v_scale, p.of_tiles, p.few ? row_form(a) : 0, num_sms, stream);
     if (e == cudaSuccess && p.few) {
         const bool early = p.tiles;
         switch (a.cache.dk) {

@@ -223,8 +223,9 @@ struct AttentionMapsFp8 {
     CUtensorMap k, v;
     int box_log2;
 };
-// Sequences of up to kFewRows rows (query tokens times query heads of a key head) are computed by one kernel
-// (attention_fp8.cu), the others by another (attention_fp8_tiles.cu); a call that may have both runs both.
+// Sequences of few rows (query tokens times query heads of a key head; kFewRows at most) are computed by one kernel
+// (attention_fp8.cu), the others by another (attention_fp8_tiles.cu); a call that may have both runs both. (32 sequences
+// of 32 rows, up to 3000 keys: 36 us by the first, 65 by the second, whose tiles of 128 rows they would not fill.)
 constexpr int kFewRows = 32;
 int attention_fp8_box_log2(const fp8bs_kv_cache& c);
 int attention_fp8_key_chunk(int64_t dk);

@@ -663,6 +663,31 @@ def test_mixed_batch(dk, dv, hq, hk):
     fp8_check(fp8_case(18, news, lens, hq, hk, dk, dv, 16), news, lens)
 
 
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("hq,hk", [(3, 3), (8, 1), (24, 2), (24, 1), (40, 1)])
+def test_mixed_batch_of_every_row_form(dk, dv, hq, hk):
+    # single tokens beside a chunk: those of the chunk's kernel, and few of either side of what the other takes
+    news, lens = [130, 1, 3, 8, 9, 1, 33, 0], [200, 700, 40, 300, 9, 1, 1100, 5]
+    fp8_check(fp8_case(31, news, lens, hq, hk, dk, dv, 16), news, lens, max_q_len=130, max_kv_len=1100)
+
+
+@pytest.mark.parametrize("news,most", [([1, 40], 40), ([3, 0, 1], 50), ([1, 1], 2), ([7, 7], 40)])
+@pytest.mark.parametrize("hq,hk", [(4, 4), (8, 1), (40, 1)])
+def test_padded_batches(news, most, hq, hk):
+    # as many rows as sequences of the largest length would have; those behind the last sequence stay as they were
+    lens = [n + 100 for n in news]
+    c = fp8_case(32, news, lens, hq, hk, 128, 128, 16)
+    T, rows = len(news) * most, sum(news)
+    out = torch.full((T, hq, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    o, l, far, off = fp8_ref(c, news, lens, 128 ** -0.5, True, 0)
+    q = torch.full((T, hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q[:rows] = c["q"]
+    got, lse = fp8bs.paged_attention(**{**c, "q": q}, out=out, return_lse=True, max_q_len=most, max_kv_len=max(lens))
+    assert bool(((got[:rows].double() - o).abs() <= far).all())
+    assert bool(((lse[:rows].double() - l).abs() <= off).all())
+    assert bool((got[rows:] == 3).all())
+
+
 @pytest.mark.parametrize("scale", [0.0, 1.0, 3.0, -0.125])
 def test_scales(scale):
     for news, lens in (([1, 1], [600, 700]), ([1, 130], [600, 700])):
