@@ -1096,11 +1096,21 @@ cudaError_t launch_rows(const AttentionMapsFp8& maps, const fp8bs_paged_attentio
 // Which kernels a call runs, and what they leave for their joins: of the tiles first, then of the few rows.
 struct Fp8Plan {
     bool tiles, few;
+    bool two;              // query tiles per CTA
     AttentionPlan of_tiles;
     RowsPlan of_rows;
     size_t tile_bytes, bytes;
     RowsParts parts;
 };
+
+// Whether the other kernel's CTAs take two query tiles: where the average sequence has more rows than one tile holds, or
+// the longest has many. (32 sequences of 2048 keys, 8 heads of 128 channels, one tile and two: 128 rows 63 and 80 us,
+// 160 rows 149 and 82; heads of 64 44 and 65, 116 and 66; of 192 84 and 107, 205 and 109. Beside 63 single tokens a
+// sequence of 2048 rows 165 and 142; beside 32 one of 528 rows 47 and 65, beside 200 one of 1024 rows 133 and 138.)
+bool two_tiles(const fp8bs_paged_attention_args& a) {
+    const int64_t group = a.q_heads / a.cache.heads;
+    return a.T * group > 128 * a.B || a.max_q_len * group > 1024;
+}
 
 Fp8Plan fp8_plan(const fp8bs_paged_attention_args& a, int num_sms) {
     Fp8Plan p = {};
@@ -1109,7 +1119,8 @@ Fp8Plan fp8_plan(const fp8bs_paged_attention_args& a, int num_sms) {
     // (both: unless all sequences are alike, or a single token has too many rows)
     p.few = !p.tiles || (a.T != a.B * a.max_q_len && a.q_heads / a.cache.heads <= kFewRows);
     if (p.tiles) {
-        p.of_tiles = attention_plan(a, num_sms, true);
+        p.two = two_tiles(a);
+        p.of_tiles = attention_plan(a, num_sms, p.two);
         if (p.of_tiles.pieces > 1) p.tile_bytes = (p.of_tiles.pieces * part_bytes(a) + 255) / 256 * 256;
     }
     p.bytes = p.tile_bytes;
@@ -1126,8 +1137,8 @@ Fp8Plan fp8_plan(const fp8bs_paged_attention_args& a, int num_sms) {
 }  // namespace
 
 int attention_fp8_box_log2(const fp8bs_kv_cache& c) {
-    // the largest power of two that divides the page and the key tiles (128, and 96 for many rows of 192-wide keys)
-    const int most = c.dk > 128 ? 5 : 7;
+    // the largest power of two that divides the page and the key tiles (64 and 128, or 64 and 96)
+    const int most = c.dk > 128 ? 5 : 6;
     int b = 4;
     while (b < most && c.page_size % (int64_t{2} << b) == 0) ++b;
     return b;
@@ -1143,7 +1154,7 @@ cudaError_t launch_paged_attention_fp8(const AttentionMapsFp8& maps, const fp8bs
     const Fp8Plan p = fp8_plan(a, num_sms);
     cudaError_t e = cudaSuccess;
     if (p.tiles)
-        e = launch_attention_fp8_tiles(maps, a, k_scale, v_scale, p.of_tiles, p.few ? row_form(a) : 0, num_sms, stream);
+        e = launch_attention_fp8_tiles(maps, a, k_scale, v_scale, p.of_tiles, p.two, p.few ? row_form(a) : 0, num_sms, stream);
     if (e == cudaSuccess && p.few) {
         const bool early = p.tiles;
         switch (a.cache.dk) {

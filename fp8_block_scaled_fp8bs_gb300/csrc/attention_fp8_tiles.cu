@@ -16,16 +16,17 @@ AttnParts parts_of(const fp8bs_paged_attention_args& a, const AttentionPlan& pla
     return p;
 }
 
-template <int DK, int DV>
+template <int DK, int DV, int NQ>
 cudaError_t launch_tiles(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a, const Scales& scales,
                          const AttentionPlan& plan, int more_rows, int num_sms, cudaStream_t stream) {
-    using Cfg = AttnCfg<DK, DV, 2, true>;
+    using Cfg = AttnCfg<DK, DV, NQ, true>;
     auto kernel = paged_attention_kernel<Cfg>;
     const cudaError_t e = set_smem(kernel, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t items = tile_bound(a, Cfg::ROWS) * a.cache.heads * plan.pieces;
     if (items >= INT32_MAX) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
+    const int64_t resident = static_cast<int64_t>(num_sms) * Cfg::CTAS;
+    const unsigned grid = static_cast<unsigned>(items < resident ? items : resident);
     AttentionModes modes = {};
     modes.box_log2 = maps.box_log2;
     return launch_pdl(kernel, grid, Cfg::THREADS, Cfg::SMEM, stream, maps.k, maps.v, a, modes, plan.piece_len,
@@ -43,12 +44,18 @@ cudaError_t launch_join(const fp8bs_paged_attention_args& a, const AttentionPlan
 
 cudaError_t launch_attention_fp8_tiles(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a,
                                        const float* k_scale, const float* v_scale, const AttentionPlan& plan,
-                                       int more_rows, int num_sms, cudaStream_t stream) {
+                                       bool two, int more_rows, int num_sms, cudaStream_t stream) {
     const Scales scales = {k_scale, v_scale};
     switch (a.cache.dk) {
-        case 64: return launch_tiles<64, 64>(maps, a, scales, plan, more_rows, num_sms, stream);
-        case 128: return launch_tiles<128, 128>(maps, a, scales, plan, more_rows, num_sms, stream);
-        default: return launch_tiles<192, 128>(maps, a, scales, plan, more_rows, num_sms, stream);
+        case 64:
+            return two ? launch_tiles<64, 64, 2>(maps, a, scales, plan, more_rows, num_sms, stream)
+                       : launch_tiles<64, 64, 1>(maps, a, scales, plan, more_rows, num_sms, stream);
+        case 128:
+            return two ? launch_tiles<128, 128, 2>(maps, a, scales, plan, more_rows, num_sms, stream)
+                       : launch_tiles<128, 128, 1>(maps, a, scales, plan, more_rows, num_sms, stream);
+        default:
+            return two ? launch_tiles<192, 128, 2>(maps, a, scales, plan, more_rows, num_sms, stream)
+                       : launch_tiles<192, 128, 1>(maps, a, scales, plan, more_rows, num_sms, stream);
     }
 }
 

@@ -13,12 +13,12 @@ constexpr float kRescale = 8.0f;
 // e4m3 numbers per channel (their products go to one S). The keys' scale joins the softmax's factor, 16 keys at a time,
 // and the values' its exponent (P = exp2(c ks S + log2 vs - m), so that pages whose values differ in size share a tile);
 // the row sum takes it out again. Values are widened to binary16 by four warps of their own, on the way from a ring of
-// codes to the ring of values, and P is binary16 too (2^-12 of it, and 2^-25 of the reference's).
+// codes to the ring of values, and P is binary16 too (2^-12 of it, and 2^-23 of the largest's: the reference is up to
+// four times that).
 template <int DK_, int DV_, int NQ_, bool CODES_ = false>
 struct AttnCfg {
     static constexpr int DK = DK_, DV = DV_, NQ = NQ_;
     static constexpr bool CODES = CODES_;
-    static_assert(!CODES || NQ == 2, "codes: two query tiles");
     // Keys per tile. (192-wide keys: 96, so that two tiles of values fit.)
     static constexpr int BN = NQ == 1 ? 64 : DK <= 128 ? 128 : 96;
     static constexpr int ROWS = NQ * 128;
@@ -37,12 +37,12 @@ struct AttnCfg {
     static constexpr int MMA_WARP = SOFT_WARPS + 2;
     static constexpr int WIDEN_WARP = SOFT_WARPS + 4;            // (codes) the first of four
     // (two query tiles: a whole third warpgroup beside the softmax's, for the split of registers below)
-    static constexpr int THREADS = 32 * (SOFT_WARPS + (NQ == 2 ? 4 : 3) + (CODES ? 4 : 0));
+    static constexpr int THREADS = 32 * (SOFT_WARPS + (NQ == 2 || CODES ? 4 : 3) + (CODES ? 4 : 0));
     // Codes: bytes of a key per swizzled chunk; tiles of values as codes; tiles' key scales, whose place is free when the
-    // tile KST + 1 before has been read (the product that frees that key tile's place follows its P).
+    // tile CST before has been read (the product that frees the place of the key tile KST before follows that P).
     static constexpr int CHK = DK % 128 == 0 ? 128 : 64;
-    static constexpr int VC_TILE = CODES ? BN * DV : 0, VCST = !CODES ? 0 : DK == 64 ? 4 : 2;
-    static constexpr int CST = CODES ? KST + 1 : 0;
+    static constexpr int VC_TILE = CODES ? BN * DV : 0, VCST = !CODES ? 0 : DK == 64 || NQ == 1 ? 4 : 2;
+    static constexpr int CST = CODES ? KST + (NQ == 2 ? 1 : 2) : 0;
     static constexpr int READERS = SOFT_WARPS + 2 + (CODES ? 4 : 0);         // warps that read a work item
     static constexpr uint32_t TMEM_COLS = tmem_cols_for(SBUF * BN + NQ * DV);
     static constexpr int BARS = 2 * KST + 2 * VST + 2 * SBUF + 3 * NQ + 3 + 2 * SLOTS + 2 * VCST + CST;
@@ -339,9 +339,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     };
 
     // Two query tiles, registers: 168 x 384 threads at launch; the softmax's row of S needs more, the third
-    // warpgroup less (208 x 256 + 80 x 128 = 63488 of 64512). Codes: 128 x 512, then 192 x 256 + 64 x 256 = 65536.
+    // warpgroup less (208 x 256 + 80 x 128 = 63488 of 64512). Codes: 128 x 512, then 192 x 256 + 64 x 256 = 65536;
+    // one query tile and two CTAs per SM 80 x 384, then 128 x 128 + 56 x 256 = 30720.
     if (warp < Cfg::SOFT_WARPS) {
-        if constexpr (NQ == 2) regs_inc<CODES ? 192 : 208>();
+        if constexpr (NQ == 2)
+            regs_inc<CODES ? 192 : 208>();
+        else if constexpr (CODES && Cfg::CTAS == 2)
+            regs_inc<128>();
         // ---- softmax warps: thread = row of query tile q
         const int q = warp >> 2;
         const int quarter = warp & 3;
@@ -570,9 +574,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                 return size;
                             };
                             // The maximum is not looked for where it is not needed: probabilities above 1 are as good as
-                            // others until their sum says that one may be past 2^13, of the 2^16 that binary16 holds.
+                            // others until their sum says that one may be past 2^15, of the 2^16 that binary16 holds. A warp
+                            // looks for all of its rows, and a new reference is four times the largest so far, so that
+                            // looks are few (a row at a time: the chunk of 4096 332 us instead of 317).
                             bool look = j == 0 || __any_sync(0xffffffffu, m == -INFINITY);
-                            if (!look) look = __any_sync(0xffffffffu, probabilities() > 8192.0f);
+                            if (!look) look = __any_sync(0xffffffffu, probabilities() > 32768.0f);
                             if (look) {
                                 float top = -INFINITY;
 #pragma unroll 1
@@ -591,10 +597,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                     }
                                 }
                                 const bool grow = top > m;
-                                const float keep = grow ? exp2_fast(m - top) : 1.0f;
-                                if (grow) m = top;
+                                const float keep = grow ? exp2_fast(m - top - 2.0f) : 1.0f;
+                                if (grow) m = top + 2.0f;
                                 l *= keep;
-                                (void)probabilities();
+                                // (scores that are not numbers: the sum says so, any reference will do)
+                                const float found = probabilities();
+                                if (found != found && m == -INFINITY) m = 0.0f;
                                 if (j > 0 && __any_sync(0xffffffffu, grow)) {
                                     if (!warp_wait(&o_done[q], (n - 1) & 1)) {
                                         ok = false;
@@ -756,7 +764,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         }
         if (!ok && lane == 0) record_error(FP8BS_DEVERR_EPILOGUE_WAIT);
     } else {
-        if constexpr (NQ == 2) regs_dec<CODES ? 64 : 80>();
+        if constexpr (NQ == 2)
+            regs_dec<CODES ? 64 : 80>();
+        else if constexpr (CODES && Cfg::CTAS == 2)
+            regs_dec<56>();
         if (warp == Cfg::KEY_WARP) {
             // ---- hands out the items and brings their keys
             // (codes: two sequences a lane, so that the first item is on hand sooner: a mixed batch of 8 62 -> 59 us)

@@ -237,7 +237,7 @@ cudaError_t launch_paged_attention_fp8(const AttentionMapsFp8& maps, const fp8bs
 // own) and, where the plan has pieces, the join, as calls of their own. Their workspace stands at `a.workspace`.
 cudaError_t launch_attention_fp8_tiles(const AttentionMapsFp8& maps, const fp8bs_paged_attention_args& a,
                                        const float* k_scale, const float* v_scale, const AttentionPlan& plan,
-                                       int more_rows, int num_sms, cudaStream_t stream);
+                                       bool two, int more_rows, int num_sms, cudaStream_t stream);
 cudaError_t launch_attention_fp8_tiles_join(const fp8bs_paged_attention_args& a, const AttentionPlan& plan,
                                             cudaStream_t stream);
 
