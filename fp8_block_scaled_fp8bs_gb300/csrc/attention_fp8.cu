@@ -11,13 +11,19 @@
 //                  V as the cache holds it (keys outermost: an MN-major operand), one fp32 tile in TMEM per key tile,
 //                  which the threads (one per channel) add to their sums in registers
 // The sum of a row is taken from P in binary32 before its rounding, each term divided by its value's scale (a power of
-// two), so lse is exact to binary32. Two groups of four warps take every other step of one or two key tiles, one's
-// softmax under the other's products; the query warp puts their sums of an item together, in a fixed order.
+// two), so lse is exact to binary32. Two or three groups of four warps take steps of one or two key tiles in turn, one's
+// softmax under the others' products; the query warp puts their sums of an item together, in a fixed order.
 // A row without keys is one whose sum is zero. A score that is not a number, or +infinite, makes the sum NaN.
 //
 // The work is cut into equal chunks of key tiles for each key head (RowsPlan), whatever the sequences' lengths: a chunk
 // is the end of one sequence, some whole ones and the beginning of another. Parts of a sequence are joined in key order
 // by a second kernel.
+//
+// Measured: 64 sequences of up to 8192 keys, 64 / 8 heads of 128, 556 MB: 108 us (0.77 of a copy's rate; the bf16 cache of
+// twice the bytes 195); one sequence of 32785 keys 23.7 us; 24 sequences of up to 5000 keys, three tokens each, 16 heads of
+// 192 / 128: 64 us for 322 MB. What bounds it then is a step's chain, not memory: S^T read, maxima over four warps,
+// probabilities as codes, the product, of which three groups cover most; short sequences are bound by what starts and ends
+// an item (queries into codes, sums of the groups): 128 sequences of up to 300 keys 38 us.
 #include "attention_codes.cuh"
 
 namespace fp8bs {

@@ -3,6 +3,9 @@
 // One CTA per token, whose row stays in registers: PER chunks of 8 channels a thread, a block of 128 channels in 16
 // neighbouring lanes. The sum of squares is one reduction over the CTA, a block's amax one over 16 lanes. Bound by
 // memory: x and the residual are read once, their sum, the codes and (where asked for) the bf16 norm written once.
+//
+// Measured: 8192 tokens of 7168 channels, residual and codes, 65 us for 413 MB (0.95 of a copy's rate), four chunks a
+// thread; five tokens 5 us among other calls, a launch, a load and two reductions, one chunk a thread (fewer rows than SMs).
 #include "gemm_common.cuh"
 #include "quant_math.cuh"
 
@@ -65,7 +68,13 @@ __global__ void __launch_bounds__(PER == 1 ? 1024 : 512) rms_norm_kernel(const _
     sum = 0.0f;
     const int warps = blockDim.x >> 5;
     for (int i = 0; i < warps; ++i) sum += s_sum[i];
-    const float inv = rsqrtf(sum / static_cast<float>(a.D) + a.eps);
+    const float mean = sum / static_cast<float>(a.D) + a.eps;
+    float inv = rsqrtf(mean);
+    {
+        // a step of Newton's method, to about half the last bit (codes have borders)
+        const float better = fmaf(0.5f * inv, fmaf(-mean * inv, inv, 1.0f), inv);
+        if (better == better) inv = better;                      // (a mean of 0 or infinity: the root stands)
+    }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
