@@ -365,23 +365,38 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 constexpr int LANES = DK / 8;                        // of a row, 8 channels each
                 constexpr int ROWS = LANES <= 16 ? 32 / LANES : 1;   // at a time
                 constexpr int BATCH = 4;
+                static_assert(32 % (ROWS * BATCH) == 0, "whole batches");
+                // Wide rows: a batch on its way under the one before (32 sequences of 128 rows and 2048 keys, heads of 128
+                // 63.6 -> 62 us, of 192 83 -> 79). Not where the softmax comes out slower beside it: two query tiles of 128
+                // channels (the chunk of 4096 334 us instead of 318), heads of 64 (the mixed batch of 8 38.2 and 37.6).
+                constexpr bool AHEAD = DK > 128 || (NQ == 1 && DK == 128);
                 const int piece = lane % LANES;
                 const bool has = lane < ROWS * LANES;
-#pragma unroll 1
-                for (int r0 = 0; r0 < 32; r0 += ROWS * BATCH) {
-                    uint4 v[BATCH];
+                auto load = [&](int r0, uint4* to) {
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
                         const int row = q * 128 + quarter * 32 + r0 + i * ROWS + lane / LANES;
-                        v[i] = make_uint4(0, 0, 0, 0);
+                        to[i] = make_uint4(0, 0, 0, 0);
                         if (has && row < it.rows) {
                             const int pr = it.first_row + row;
                             const int tok = pr / group;
-                            v[i] = __ldg(reinterpret_cast<const uint4*>(
-                                             static_cast<const __nv_bfloat16*>(a.q) +
-                                             (it.q0 + tok) * a.q_token_stride +
-                                             (it.head * group + pr - tok * group) * a.q_head_stride) + piece);
+                            to[i] = __ldg(reinterpret_cast<const uint4*>(
+                                              static_cast<const __nv_bfloat16*>(a.q) +
+                                              (it.q0 + tok) * a.q_token_stride +
+                                              (it.head * group + pr - tok * group) * a.q_head_stride) + piece);
                         }
+                    }
+                };
+                uint4 v[BATCH], next[BATCH];
+                if (AHEAD) load(0, next);
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += ROWS * BATCH) {
+                    if constexpr (AHEAD) {
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) v[i] = next[i];
+                        if (r0 + ROWS * BATCH < 32) load(r0 + ROWS * BATCH, next);
+                    } else {
+                        load(r0, v);
                     }
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
