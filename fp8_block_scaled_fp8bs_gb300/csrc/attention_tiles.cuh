@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 
     // Two query tiles, registers: 168 x 384 threads at launch; the softmax's row of S needs more, the third
     // warpgroup less (208 x 256 + 80 x 128 = 63488 of 64512). Codes: 128 x 512, then 192 x 256 + 64 x 256 = 65536;
-    // one query tile and two CTAs per SM 80 x 384, then 128 x 128 + 56 x 256 = 30720.
+    // one query tile and two CTAs per SM 80 x 384, then 128 x 128 + 56 x 256.
     if (warp < Cfg::SOFT_WARPS) {
         if constexpr (NQ == 2)
             regs_inc<CODES ? 192 : 208>();
