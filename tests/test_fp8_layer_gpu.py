@@ -930,3 +930,21 @@ def test_graphs_of_one_capture_stream_in_flight_at_once(call):
                 eager.append(calls[1]())
         torch.cuda.synchronize()
         assert all(torch.equal(o, r) for o, r in zip(outs, refs)) and all(torch.equal(o, refs[1]) for o in eager)
+
+
+def narrow_call(seed):
+    c = fp8_case(seed, [30, 1, 1], [9000, 5000, 40], 16, 4, 128, 128, 16)
+    return lambda: fp8bs.paged_attention(**c, max_q_len=30, max_kv_len=9000)
+
+
+def test_graphs_of_short_chunks_in_flight_at_once():
+    test_graphs_of_one_capture_stream_in_flight_at_once(narrow_call)
+
+
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("chunks", [{5: 40, 70: 300, 149: 33}, {149: 400}, {0: 20, 63: 20, 64: 20, 128: 20}])
+def test_chunks_among_many_sequences(dk, dv, chunks):
+    # more sequences than are looked through at once, some out of order in length, some without tokens
+    news = [chunks.get(b, 0 if b % 11 == 3 else 1) for b in range(150)]
+    lens = [n + 7 * b % 500 for b, n in enumerate(news)]
+    fp8_check(fp8_case(33, news, lens, 8, 2, dk, dv, 16), news, lens, max_q_len=max(news), max_kv_len=max(lens))
