@@ -25,6 +25,7 @@
 // probabilities as codes, the product, of which three groups cover most; short sequences are bound by what starts and ends
 // an item (queries into codes, sums of the groups): 128 sequences of up to 300 keys 38 us.
 #include "attention_codes.cuh"
+#include "attention_join.h"
 
 namespace fp8bs {
 
@@ -73,13 +74,7 @@ struct RowsPlan {
 constexpr int kItemTiles = 2;
 
 // Parts of sequences, for the join: of each (chunk, key head) the one that a chunk begins with (slot 0) and the one that
-// it ends with (slot 1), and, where the part that it begins with ends its sequence, what is to be joined.
-struct JoinHead {
-    int parts;             // 0: nothing
-    int first;             // chunk of the first part
-    int q0, rows;
-};
-
+// it ends with (slot 1), and, where the part that it begins with ends its sequence, what is to be joined (JoinHead).
 struct RowsParts {
     float2* mark;          // null, or where the other kernel's join is told which rows are none of its own
     float* o;              // [chunk][head][2][R][DV], unnormalised
@@ -594,11 +589,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         int64_t before = 0;                        // after so many positions
         if (B > 256) now = look_at(f, 0, a, plan.whole, R, lane);
         const int64_t chunks = min(static_cast<int64_t>(plan.chunks), max(all, int64_t{1}));
-        for (int64_t id = blockIdx.x; ok && id < static_cast<int64_t>(plan.chunks) * heads; id += gridDim.x) {
+        // (after a wait that ran out the rest of the ids get heads without parts: the join follows all of them)
+        for (int64_t id = blockIdx.x; id < static_cast<int64_t>(plan.chunks) * heads; id += gridDim.x) {
             const int64_t chunk = part_of(id, 1, heads);
             const int head = static_cast<int>(id - chunk * heads);
             JoinHead join = {0, 0, 0, 0};
-            if (chunk < chunks) {
+            if (ok && chunk < chunks) {
                 // positions [at, end)
                 int64_t at = part_of(chunk, all, chunks);
                 const int64_t end = part_of(chunk + 1, all, chunks);
@@ -670,7 +666,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             });
                 }
             }
-            if (!plan.whole && lane == 0) parts.head[id] = join;
+            if (!plan.whole && lane == 0) parts.head[id] = ok ? join : JoinHead{0, 0, 0, 0};
         }
         if (ok) {
             RowItem none = {};
@@ -985,14 +981,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 // rows), one thread per channel, the parts in key order.
 template <int DV, int R>
 __global__ void __launch_bounds__(DV) attention_rows_join_kernel(const __grid_constant__ fp8bs_paged_attention_args a,
-                                                                 const RowsParts parts) {
+                                                                 const RowsParts parts, const int chunks) {
     grid_dependency_wait();
     grid_launch_dependents();
     __shared__ float2 s_ml[DV];
     const JoinHead j = parts.head[blockIdx.x];
-    if (j.parts == 0) return;
     const int heads = static_cast<int>(a.cache.heads);
     const int group = static_cast<int>(a.q_heads / heads);
+    if (!join_in_reach(j, chunks, R, group, a.T)) return;
     const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(heads));
     // where the i-th part stands: at the end of its chunk for the first, at the beginning for the others
     auto slot = [&](int i) { return (2 * (static_cast<int64_t>(j.first + i) * heads + head) + (i == 0 ? 1 : 0)) * R; };
@@ -1086,7 +1082,7 @@ cudaError_t launch_rows(const AttentionMapsFp8& maps, const fp8bs_paged_attentio
     if (e != cudaSuccess || plan.whole) return e;
     const unsigned rows = static_cast<unsigned>(std::min<int64_t>(Cfg::R, a.max_q_len * (a.q_heads / a.cache.heads)));
     return launch_pdl(attention_rows_join_kernel<Cfg::DV, Cfg::R>, dim3(static_cast<unsigned>(ids), rows), Cfg::DV, 0,
-                      stream, a, parts);
+                      stream, a, parts, plan.chunks);
 }
 
 template <int DK, int DV>
