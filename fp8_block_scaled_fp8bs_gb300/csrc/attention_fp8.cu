@@ -982,14 +982,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 template <int DV, int R>
 __global__ void __launch_bounds__(DV) attention_rows_join_kernel(const __grid_constant__ fp8bs_paged_attention_args a,
                                                                  const RowsParts parts, const int chunks) {
+    __shared__ float2 s_ml[DV];
+    const int heads = static_cast<int>(a.cache.heads);
+    const int group = static_cast<int>(static_cast<unsigned>(a.q_heads) / static_cast<unsigned>(heads));
+    const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(heads));
     grid_dependency_wait();
     grid_launch_dependents();
-    __shared__ float2 s_ml[DV];
     const JoinHead j = parts.head[blockIdx.x];
-    const int heads = static_cast<int>(a.cache.heads);
-    const int group = static_cast<int>(a.q_heads / heads);
-    if (!join_in_reach(j, chunks, R, group, a.T)) return;
-    const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(heads));
+    if (!join_in_reach(j, chunks, R, group, static_cast<uint32_t>(a.T))) return;
     // where the i-th part stands: at the end of its chunk for the first, at the beginning for the others
     auto slot = [&](int i) { return (2 * (static_cast<int64_t>(j.first + i) * heads + head) + (i == 0 ? 1 : 0)) * R; };
     for (int r = blockIdx.y; r < j.rows; r += gridDim.y) {

@@ -20,10 +20,13 @@ struct JoinHead {
 };
 
 // Whether the parts stand in `chunks` chunks and the rows among `tokens` tokens of `group` rows each, `most` rows at most:
-// what the join reads and writes is within its buffers then, whatever else the head says.
-FP8BS_BOTH inline bool join_in_reach(const JoinHead& j, int64_t chunks, int64_t most, int64_t group, int64_t tokens) {
-    return j.parts > 0 && j.first >= 0 && static_cast<int64_t>(j.first) + j.parts <= chunks && j.rows > 0 &&
-           j.rows <= most && j.q0 >= 0 && j.q0 + (j.rows - 1) / group < tokens;
+// what the join reads and writes is within its buffers then, whatever else the head says. (In 32 bits, negative numbers
+// as large ones: in 64 one token of 32k keys took 24.6 us instead of 23.6.)
+FP8BS_BOTH inline bool join_in_reach(const JoinHead& j, uint32_t chunks, uint32_t most, uint32_t group, uint32_t tokens) {
+    const uint32_t parts = static_cast<uint32_t>(j.parts), first = static_cast<uint32_t>(j.first);
+    const uint32_t q0 = static_cast<uint32_t>(j.q0), rows = static_cast<uint32_t>(j.rows);
+    if (parts - 1 >= chunks || first > chunks - parts || rows - 1 >= most || q0 >= tokens) return false;
+    return (tokens - q0 < most ? tokens - q0 : most) * group >= rows;        // (`most` tokens have that many rows)
 }
 
 }  // namespace fp8bs

@@ -13,7 +13,8 @@ int main() {
     const int forms[] = {8, 16, 32};
     for (int n = 0; n < 4000000; ++n) {
         const int most = forms[below(3)];
-        const int64_t group = 1 + below(most), tokens = 1 + below(n & 1 ? 300 : 2147483647), chunks = 1 + below(1300);
+        const int64_t group = 1 + below(n & 2 ? most : 65535), tokens = 1 + below(n & 1 ? 300 : 2147483647);
+        const int64_t chunks = 1 + below(n & 4 ? 1300 : 2147483647);
         fp8bs::JoinHead j;
         int* field[] = {&j.parts, &j.first, &j.q0, &j.rows};
         for (int i = 0; i < 4; ++i) {
