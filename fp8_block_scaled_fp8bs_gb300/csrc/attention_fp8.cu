@@ -473,11 +473,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         break;
                     }
                     // P's reference: 2^8 below the largest so far, so that P uses e4m3's range up to 256. Every warp of
-                    // the group finds the same; it hardly ever moves.
-                    const float now = fmaxf(fmaxf(tops[0][lane % R], tops[1][lane % R]),
-                                            fmaxf(tops[2][lane % R], tops[3][lane % R])) - 8.0f;
-                    if (__any_sync(0xffffffffu, now > m_lane)) {
-                        if (now > m_lane) m_lane = now;
+                    // the group finds the same; it hardly ever moves. (From 2^24 on binary32 does not hold every such
+                    // difference: where it comes out larger, the largest itself is the reference, and P at most 1.)
+                    const float most = fmaxf(fmaxf(tops[0][lane % R], tops[1][lane % R]),
+                                             fmaxf(tops[2][lane % R], tops[3][lane % R]));
+                    const bool move = most - m_lane > 8.0f;
+                    if (__any_sync(0xffffffffu, move)) {
+                        if (move) {
+                            const float ref = most - 8.0f;
+                            m_lane = most - ref > 8.0f ? most : ref;
+                        }
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
                             const float ref = __shfl_sync(0xffffffffu, m_lane, r);

@@ -1,14 +1,19 @@
 """The operators that keep a decoder layer in 8 bits, and attention over a bf16 cache, at the ends of what they accept:
 memory of any content, scores and scales of any size, slots with gaps, calls without queries. Tolerances are derived beside
 each comparison."""
+import math
+
 import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_fp8_layer_gpu import fp8_case
-from test_layer_gpu import no_device_error  # noqa: F401
+from test_fp8_layer_gpu import SHAPES, fp8_case
+from test_layer_gpu import gen, no_device_error, paged_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+LOG2E = 1 / math.log(2)
 
 
 # ------------------------------------------------------------------------------------------ workspaces
@@ -46,3 +51,68 @@ def test_a_workspace_of_any_content(news, lens, fill):
         fp8bs.fp8bs_paged_attention_fp8(raw_args(c, out, work, max(news)), *scales, stream)
         assert torch.equal(out, ref)
         out.zero_()
+
+
+# ------------------------------------------------------------------------------------ sizes of scores
+
+def level_case(codes, news, lens, hq, hk, dk, dv, low, high):
+    """Keys that are all alike, so that each row's scores are one number, of low .. high in units of log2 and either
+    sign from row to row: o is the mean of the values, however coarse binary32 is there."""
+    case = fp8_case(71, news, lens, hq, hk, dk, dv, 16, poison=False, k_spread=0, v_spread=0) if codes else \
+        paged_case(71, news, lens, hq, hk, dk, dv, 16, poison=False)
+    g = gen(72)
+    k = case["cache"].k
+    row = (torch.rand(hk, dk, generator=g, device="cuda") * 100 + 20).to(E4M3)
+    if codes:
+        k.view(torch.uint8)[:] = row.view(torch.uint8)
+        case["cache"].k_scale.fill_(1.0)
+    else:
+        k[:] = row.bfloat16()
+    q = torch.rand(case["q"].shape, generator=g, device="cuda", dtype=torch.float64) + 0.5
+    size = torch.rand(q.shape[:2], generator=g, device="cuda", dtype=torch.float64)
+    size = torch.exp2(low + (high - low) * size)
+    size[:, ::2] *= -1
+    s = (q * row.double().repeat_interleave(hq // hk, 0)).sum(-1) * (dk ** -0.5 * LOG2E)
+    case["q"] = (q * (size / s)[..., None]).bfloat16()
+    return case, row
+
+
+def check_level(codes, news, lens, hq, hk, dk, dv, low, high):
+    c, row = level_case(codes, news, lens, hq, hk, dk, dv, low, high)
+    out, lse = fp8bs.paged_attention(**c, max_q_len=max(news), return_lse=True)
+    cache, t = c["cache"], 0
+    for b, (n, L) in enumerate(zip(news, lens)):
+        j = torch.arange(L, device="cuda")
+        pg = c["page_table"][b].long()[j // 16]
+        if codes:
+            v = cache.v.view(torch.uint8)[pg, j % 16].view(E4M3).double() * cache.v_scale.double()[pg][..., None]
+        else:
+            v = cache.v[pg, j % 16].double()
+        v = v.repeat_interleave(hq // hk, 1)
+        q = c["q"][t:t + n].double()
+        terms = q * row.double().repeat_interleave(hq // hk, 0)
+        s = terms.sum(-1) * dk ** -0.5
+        count = (L - n + 1 + torch.arange(n, device="cuda"))
+        o = v.cumsum(0)[count - 1] / count[:, None, None]
+        mag = v.abs().cumsum(0)[count - 1] / count[:, None, None]
+        # the probabilities of a row are all the same number: one rounding of it to bf16, or to two e4m3 numbers (2^-8)
+        # and one of the output (2^-8); binary32 sums 2^-12
+        err = (out[t:t + n].double() - o).abs()
+        assert bool((err <= (2.0 ** -7 + 2.0 ** -12) * mag).all()), float((err / mag).nan_to_num(math.inf).max())
+        # a score: queries to 2^-17 of their largest channel, binary32 sums of 192 terms 2^-16 of them; then three
+        # roundings of the sum, 2^-20
+        size = (c["q"][t:t + n].double().abs().amax(-1) * row.double().sum(-1).repeat_interleave(hq // hk)) * dk ** -0.5
+        l = s + count.double().log()[:, None]
+        far = size * (2.0 ** -17 + 2.0 ** -16) + 2.0 ** -20 * l.abs() + 1e-5
+        assert bool(((lse[t:t + n].double() - l).abs() <= far).all())
+        t += n
+
+
+LEVELS = [([1, 1, 1, 1, 2], [1, 2, 40, 300, 129]), ([1], [20000])]
+
+
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("news,lens", LEVELS)
+@pytest.mark.parametrize("low,high", [(20, 26), (26, 29), (29, 40)])
+def test_scores_of_any_size_over_codes(dk, dv, news, lens, low, high):
+    check_level(True, news, lens, 16, 2, dk, dv, low, high)
