@@ -108,7 +108,8 @@ def check_level(codes, news, lens, hq, hk, dk, dv, low, high):
         t += n
 
 
-LEVELS = [([1, 1, 1, 1, 2], [1, 2, 40, 300, 129]), ([1], [20000])]
+LEVELS = [([1, 1, 1, 1, 2], [1, 2, 40, 300, 129]), ([1], [20000]), ([130, 1, 3], [600, 1, 5]), ([300], [400]),
+          ([40], [9000])]
 
 
 @pytest.mark.parametrize("dk,dv", SHAPES)
