@@ -10,10 +10,11 @@ namespace {
 constexpr float kRescale = 8.0f;
 
 // Where a row's maximum is this large, in log2 units, binary32 holds the terms of the fused product that makes exponents of
-// scores to 8 and more, by which a probability would be out of range: a function of its own takes the scores relative to the
-// maximum first (far_tiles; the chunk of 4096 over codes 323 us, 317 without it, and 326 to 366 with the same in the loop of
-// all rows).
-constexpr float kFar = 67108864.0f;
+// scores to 8 and more (a bf16 cache: 128), by which a probability would be out of the range of binary16 (bf16): a function
+// of its own takes the scores relative to the maximum first (far_tiles; the chunk of 4096 over codes 318 us, 316 without it,
+// 326 to 366 with the same in the loop of all rows; 192-wide heads over bf16 57.4, 56.6 without). Asked where a maximum grows.
+template <bool CODES>
+constexpr float kFar = CODES ? 67108864.0f : 1073741824.0f;
 
 // CODES: the cache holds e4m3 codes. The keys' product then takes them as they are, and each query as the sum of two
 // e4m3 numbers per channel (their products go to one S). The keys' scale joins the softmax's factor, 16 keys at a time,
@@ -267,34 +268,37 @@ struct FarRows {
     bool ok;
 };
 
-// What the softmax warps do with an item's tiles (codes), from the j-th on, whose maximum is far in some row (kFar): 16 keys
-// at a time, each score rounded to binary32 in log2 units before the maximum is taken from it. row_lo, row_hi: the row's
-// keys, counted from the item's first tile.
+// What the softmax warps do with an item's tiles, from the j-th on, whose maximum is far in some row (kFar): 16 keys at a
+// time, the reference taken from each score (codes: from the score in log2 units, rounded to binary32). row_lo, row_hi: the
+// row's keys, counted from the item's first tile.
 template <class Cfg>
 __device__ __noinline__ FarRows far_tiles(uint32_t tmem, uint32_t o_tmem, int q, float c, const float4* scales,
                                           uint64_t* c_full, uint64_t* s_full, uint64_t* p_full, uint64_t* o_done, int n0,
                                           int j, int nt, int row_lo, int row_hi, float m, float l, int lane) {
     constexpr int BN = Cfg::BN;
+    constexpr bool CODES = Cfg::CODES;
+    constexpr int CST = CODES ? Cfg::CST : 1;
     bool ok = true;
 #pragma unroll 1
     for (; j < nt; ++j) {
         const int n = n0 + j;
         const int buf = Cfg::NQ == 2 ? q : n & 1;
-        ok = warp_wait(&c_full[n % Cfg::CST], (n / Cfg::CST) & 1) &&
+        ok = (!CODES || warp_wait(&c_full[n % CST], (n / CST) & 1)) &&
              warp_wait(&s_full[buf], Cfg::NQ == 2 ? n & 1 : (n >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_tmem_row = tmem + buf * BN;
         const int lo = row_lo - j * BN, hi = row_hi - j * BN;
-        const float4* sc16 = scales + n % Cfg::CST * 8;
+        const float4* sc16 = scales + n % CST * 8;
         auto load_scores = [&](int i, float* s) {
             tmem_ld_16cols(s_tmem_row + 16 * i, s);
             tmem_wait_ld_16(s);
-            const float4 sc = sc16[i];
+            float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if constexpr (CODES) sc = sc16[i];
             const float by = max_nan(c * sc.x, 1.2e-38f);
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-                s[k] = 16 * i + k < lo || 16 * i + k >= hi ? -INFINITY : fmaf(s[k], by, sc.y);
+                s[k] = 16 * i + k < lo || 16 * i + k >= hi ? -INFINITY : CODES ? fmaf(s[k], by, sc.y) : s[k];
         };
         float top = -INFINITY, total = 0.0f;
 #pragma unroll 1
@@ -304,24 +308,30 @@ __device__ __noinline__ FarRows far_tiles(uint32_t tmem, uint32_t o_tmem, int q,
 #pragma unroll
             for (int k = 0; k < 16; ++k) top = fmaxf(top, s[k]);
         }
-        const bool grow = top > m;
-        const float keep = grow ? exp2_fast(m - top - 2.0f) : 1.0f;
-        if (grow) m = top + 2.0f;
+        const bool grow = CODES ? top > m : (top - m) * c > kRescale || (m == -INFINITY && top > m);
+        const float keep = !grow ? 1.0f : CODES ? exp2_fast(m - top - 2.0f) : exp2_fast((m - top) * c);
+        if (grow) m = CODES ? top + 2.0f : top;
         const float ref = m == -INFINITY ? 0.0f : m;
+        // (bf16: other rows keep the rounded product that their probabilities have been taken relative to so far)
+        const float rest = !CODES && fabsf(ref * c) < kFar<CODES> ? fmaf(ref, c, -(ref * c)) : 0.0f;
 #pragma unroll 1
         for (int i = 0; i < BN / 16; ++i) {
             float s[16], sum = 0.0f;
             load_scores(i, s);
             uint32_t p[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum += s[k] = exp2_fast(s[k] - ref);
-            total = fmaf(sum, sc16[i].z, total);
+            for (int k = 0; k < 16; ++k) sum += s[k] = exp2_fast(CODES ? s[k] - ref : fmaf(s[k] - ref, c, rest));
+            if constexpr (CODES)
+                total = fmaf(sum, sc16[i].z, total);
+            else
+                total += sum;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) p[k] = pack_half2(s[2 * k], s[2 * k + 1]);
+            for (int k = 0; k < 8; ++k)
+                p[k] = CODES ? pack_half2(s[2 * k], s[2 * k + 1]) : pack_bf16x2(s[2 * k], s[2 * k + 1]);
             tmem_st_4cols(s_tmem_row + 8 * i, p[0], p[1], p[2], p[3]);
             tmem_st_4cols(s_tmem_row + 8 * i + 4, p[4], p[5], p[6], p[7]);
         }
-        if (total != total && m == -INFINITY) m = 0.0f;
+        if (CODES && total != total && m == -INFINITY) m = 0.0f;
         l = fmaf(l, keep, total);
         if (j > 0 && __any_sync(0xffffffffu, grow)) {
             ok = warp_wait(o_done, (n - 1) & 1);
@@ -708,16 +718,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                         top = fmaxf(top, fmaf(fmaxf(of16[0], of16[1]), max_nan(c * sc.x, 1.2e-38f), sc.y));
                                     }
                                 }
-                                far = __any_sync(0xffffffffu, fabsf(top) >= kFar && top != -INFINITY);
-                                if (far) break;
                                 const bool grow = top > m;
+                                const bool any_grows = __any_sync(0xffffffffu, grow);
+                                if (any_grows) {
+                                    far = __any_sync(0xffffffffu, grow && fabsf(top) >= kFar<true>);
+                                    if (far) break;
+                                }
                                 const float keep = grow ? exp2_fast(m - top - 2.0f) : 1.0f;
                                 if (grow) m = top + 2.0f;
                                 l *= keep;
                                 // (scores that are not numbers: the sum says so, any reference will do)
                                 const float found = probabilities();
                                 if (found != found && m == -INFINITY) m = 0.0f;
-                                if (j > 0 && __any_sync(0xffffffffu, grow)) {
+                                if (j > 0 && any_grows) {
                                     if (!warp_wait(&o_done[q], (n - 1) & 1)) {
                                         ok = false;
                                         break;
@@ -776,11 +789,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                 for (int i = 4; i < BN; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
                                 top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                                 const bool grow = (top - m) * c > kRescale || (m == -INFINITY && top > m);
+                                const bool any_grows = __any_sync(0xffffffffu, grow);
+                                if (any_grows) {
+                                    // (the rows behind the last hold whatever stood in memory)
+                                    far = __any_sync(0xffffffffu, grow && live && fabsf(top * c) >= kFar<false>);
+                                    if (far) break;
+                                }
                                 const float keep = grow ? exp2_fast((m - top) * c) : 1.0f;
                                 if (grow) m = top;
                                 l *= keep;
                                 probabilities(s);
-                                if (j > 0 && __any_sync(0xffffffffu, grow)) {
+                                if (j > 0 && any_grows) {
                                     if (!warp_wait(&o_done[q], (n - 1) & 1)) {
                                         ok = false;
                                         break;
@@ -801,12 +820,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         mbar_arrive(&p_full[buf]);
                     }
                 }
-                if constexpr (CODES) {
-                    if (far) {
-                        const FarRows f = far_tiles<Cfg>(tmem + lanes, o_tmem, q, c, s_scale[0], c_full, s_full, p_full,
-                                                         &o_done[q], n0, j, nt, row_lo - k0, row_hi - k0, m, l, lane);
-                        m = f.m, l = f.l, ok = f.ok;
-                    }
+                if (far) {
+                    const FarRows f = far_tiles<Cfg>(tmem + lanes, o_tmem, q, c, s_scale[0], c_full, s_full, p_full,
+                                                     &o_done[q], n0, j, nt, row_lo - k0, row_hi - k0, m, l, lane);
+                    m = f.m, l = f.l, ok = f.ok;
                 }
                 n0 += nt;
             }

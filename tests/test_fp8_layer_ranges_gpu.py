@@ -117,3 +117,10 @@ LEVELS = [([1, 1, 1, 1, 2], [1, 2, 40, 300, 129]), ([1], [20000]), ([130, 1, 3],
 @pytest.mark.parametrize("low,high", [(20, 26), (26, 29), (29, 40)])
 def test_scores_of_any_size_over_codes(dk, dv, news, lens, low, high):
     check_level(True, news, lens, 16, 2, dk, dv, low, high)
+
+
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("news,lens", LEVELS)
+@pytest.mark.parametrize("low,high", [(20, 29), (29, 40)])
+def test_scores_of_any_size_over_bf16(dk, dv, news, lens, low, high):
+    check_level(False, news, lens, 16, 2, dk, dv, low, high)
