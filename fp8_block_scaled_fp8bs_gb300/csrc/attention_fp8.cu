@@ -439,10 +439,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                         for (int r = 0; r < R; r += 2) {
                             const float2 f = *reinterpret_cast<const float2*>(&s_factor[b][r]);
-                            const float2 z = __fmul2_rn(__fadd2_rn(make_float2(y[r], y[r + 1]),
-                                                                   make_float2(y[R + r], y[R + r + 1])),
-                                                        make_float2(sc.x, sc.x));
-                            fma2_to(&t[h][r], z, f, make_float2(sc.y, sc.y));
+                            // (the factors first: large scales and small queries meet before either is out of range)
+                            const float2 z = __fadd2_rn(make_float2(y[r], y[r + 1]), make_float2(y[R + r], y[R + r + 1]));
+                            fma2_to(&t[h][r], z, __fmul2_rn(f, make_float2(sc.x, sc.x)), make_float2(sc.y, sc.y));
                         }
                         const int kb = k0 + (j + h) * KEYS;
                         if (kb < full_lo || kb + KEYS > full_hi) {

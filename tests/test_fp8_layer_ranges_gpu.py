@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_fp8_layer_gpu import SHAPES, fp8_case
+from test_fp8_layer_gpu import SHAPES, fp8_case, fp8_check
 from test_layer_gpu import gen, no_device_error, paged_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +124,22 @@ def test_scores_of_any_size_over_codes(dk, dv, news, lens, low, high):
 @pytest.mark.parametrize("low,high", [(20, 29), (29, 40)])
 def test_scores_of_any_size_over_bf16(dk, dv, news, lens, low, high):
     check_level(False, news, lens, 16, 2, dk, dv, low, high)
+
+
+# ------------------------------------------------------------------------- sizes of queries, keys, scale
+
+@pytest.mark.parametrize("size,unit", [(1e-28, 2.0 ** 85), (2.0 ** -115, 2.0 ** 110), (1e25, 2.0 ** -90)])
+def test_small_queries_over_large_keys(size, unit):
+    for news, lens in (([1, 3], [500, 200]), ([1, 130], [500, 200])):
+        c = fp8_case(73, news, lens, 8, 2, 128, 128, 16, k_spread=0)
+        c["cache"].k_scale.fill_(unit)
+        c["q"] = (c["q"].double() * (size * 2.0 ** -7)).bfloat16()
+        fp8_check(c, news, lens, scale=128 ** -0.5 / (size * unit))
+        fp8_check(c, news, lens, scale=0.0)
+
+
+def test_scale_of_zero_over_large_queries():
+    for news, lens in (([1, 3], [500, 200]), ([1, 130], [500, 200])):
+        c = fp8_case(74, news, lens, 8, 2, 128, 128, 16, k_spread=0)
+        c["q"] = (c["q"].double() * 1e25).bfloat16()
+        fp8_check(c, news, lens, scale=0.0)
