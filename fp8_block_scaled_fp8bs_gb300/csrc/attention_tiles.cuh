@@ -457,10 +457,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const int r = q * 128 + quarter * 32 + lane;          // row of the item's tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
-        // (a scale of zero: any tiny factor keeps -inf apart from the finite scores; one that is NaN stays so. Codes: their
+        // (a scale of zero: the smallest factor keeps -inf apart from the finite scores; one that is NaN stays so. Codes: their
         // factor is only bounded where the key's scale has joined it, as a small one may belong to large keys. The maximum
         // with zero is none; without it the compiler orders the loop below otherwise, 328 us for the chunk of 4096, not 321.)
-        const float c_all = max_nan(fabsf(a.scale) * 1.4426950408889634f, CODES ? 0.0f : 1e-30f);
+        const float c_all = max_nan(fabsf(a.scale) * 1.4426950408889634f, CODES ? 0.0f : 1e-45f);
         // Queries of query tile q into shared memory (K-major, 128-byte swizzle), valid rows only (what the
         // others hold is of no consequence: rows do not meet). A negative scale turns their signs, so that
         // the row maximum is always that of the largest S.

@@ -8,7 +8,7 @@ import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
 from test_fp8_layer_gpu import SHAPES, fp8_case, fp8_check
-from test_layer_gpu import gen, no_device_error, paged_case  # noqa: F401
+from test_layer_gpu import attention_check, gen, no_device_error, paged_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,11 @@ def test_scale_of_zero_over_large_queries():
         c = fp8_case(74, news, lens, 8, 2, 128, 128, 16, k_spread=0)
         c["q"] = (c["q"].double() * 1e25).bfloat16()
         fp8_check(c, news, lens, scale=0.0)
+
+
+def test_scale_of_zero_over_large_bf16_keys():
+    for news, lens in (([1, 3], [500, 200]), ([1, 130], [500, 200]), ([300], [400])):
+        c = paged_case(75, news, lens, 8, 2, 128, 128, 16)
+        c["q"] = (c["q"].double() * 1e18).bfloat16()
+        c["cache"].k.copy_((c["cache"].k.double() * 1e18).bfloat16())
+        attention_check(c, news, lens, scale=0.0)
