@@ -129,8 +129,9 @@ __device__ __forceinline__ void two_codes_p(float x, float y, uint32_t* hi, uint
     *lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
 }
 
-// A reference that no key has set yet: far below any score, and finite, so that a difference from it is never NaN.
-constexpr float kNoReference = -3.0e38f;
+// A reference that no key has set yet: the lowest number, below any score but itself, and finite, so that a difference from
+// it is never NaN.
+constexpr float kNoReference = -3.402823466e38f;
 
 // Each of the R values summed over the warp's lanes, R a power of two: halves change hands until every lane holds one
 // value's sum over some lanes, in l[0], then those. Returns which value it is.

@@ -121,6 +121,12 @@ def test_scores_of_any_size_over_codes(dk, dv, news, lens, low, high):
 
 @pytest.mark.parametrize("dk,dv", SHAPES)
 @pytest.mark.parametrize("news,lens", LEVELS)
+def test_scores_at_the_ends_of_binary32(dk, dv, news, lens):
+    check_level(True, news, lens, 16, 2, dk, dv, 127.84, 127.95)
+
+
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("news,lens", LEVELS)
 @pytest.mark.parametrize("low,high", [(20, 29), (29, 40)])
 def test_scores_of_any_size_over_bf16(dk, dv, news, lens, low, high):
     check_level(False, news, lens, 16, 2, dk, dv, low, high)
