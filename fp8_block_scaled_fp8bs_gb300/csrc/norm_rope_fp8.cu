@@ -33,18 +33,20 @@ struct Run {
     float by[2], ratio[2];   // of keys and values: 1 / the new scale; old / new scale where codes are to be rounded again
 };
 
-// A page's slot is given to a token of the call: its position and slot are valid.
+// A token's slot. known: its position and slot are not out of range (a negative slot is none); ok: a page's slot is given
+// to it.
 struct TokenSlot {
     int64_t slot;
-    bool ok;
+    bool known, ok;
 };
 
 __device__ __forceinline__ TokenSlot token_slot(const fp8bs_qk_norm_rope_args& a, int64_t t) {
-    TokenSlot s = {-1, false};
+    TokenSlot s = {-1, true, false};
     if (t >= 0 && t < a.T) {
         s.slot = a.slots[t];
         const int pos = a.positions[t];
-        s.ok = s.slot >= 0 && s.slot < a.cache.pages * a.cache.page_size && pos >= 0 && pos < a.max_positions;
+        s.known = pos >= 0 && pos < a.max_positions && s.slot < a.cache.pages * a.cache.page_size;
+        s.ok = s.known && s.slot >= 0;
     }
     return s;
 }
@@ -191,15 +193,17 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
     const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(hk));
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(hk)) * window;
     // One token a thread, those of the window and of a page behind it, where its last run ends if not before.
-    TokenSlot mine = {-1, false};
+    TokenSlot mine = {-1, true, false};
     bool more = false;
     if (32 * warp < window + a.cache.page_size) {
         mine = token_slot(a, t0 + tid);
-        TokenSlot before = {__shfl_up_sync(0xffffffffu, mine.slot, 1), __shfl_up_sync(0xffffffffu, mine.ok, 1) != 0};
+        TokenSlot before = {__shfl_up_sync(0xffffffffu, mine.slot, 1), true, __shfl_up_sync(0xffffffffu, mine.ok, 1) != 0};
         if (lane == 0) before = token_slot(a, t0 + tid - 1);
         more = continues(a, before, mine);
     }
     const bool starts = tid < window && mine.ok && !more;
+    // (where there are queries, theirs report it)
+    if (a.q_heads == 0 && head == 0 && tid < window && !mine.known) record_error(FP8BS_DEVERR_INDEX);
     {
         const unsigned b0 = __ballot_sync(0xffffffffu, starts), b1 = __ballot_sync(0xffffffffu, more);
         const unsigned b2 = __ballot_sync(0xffffffffu, mine.ok);

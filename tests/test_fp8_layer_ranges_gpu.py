@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_fp8_layer_gpu import SHAPES, fp8_case, fp8_check
+from test_fp8_layer_gpu import SHAPES, empty_cache, fp8_case, fp8_check, write_inputs
 from test_layer_gpu import attention_check, gen, no_device_error, paged_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +157,23 @@ def test_scale_of_zero_over_large_bf16_keys():
         c["q"] = (c["q"].double() * 1e18).bfloat16()
         c["cache"].k.copy_((c["cache"].k.double() * 1e18).bfloat16())
         attention_check(c, news, lens, scale=0.0)
+
+
+# ------------------------------------------------------------------------------ writes without queries
+
+def test_write_without_queries_reports_bad_indices():
+    page, hk, d = 16, 3, 64
+    for T, bad in ((5, 1), (200, 199), (200, 0), (600, 300)):
+        for pos, slot, want in ((4000, None, fp8bs.DEVERR_INDEX), (-1, None, fp8bs.DEVERR_INDEX),
+                                (None, 41 * page, fp8bs.DEVERR_INDEX), (None, -1, 0)):
+            cache = empty_cache(41, page, hk, d, d)
+            x = write_inputs(76, T, 0, hk, d, d, 32, True)
+            slots = torch.arange(page, page + T, device="cuda")
+            if pos is not None:
+                x["pos"][bad] = pos
+            if slot is not None:
+                slots[bad] = slot
+            q = fp8bs.qk_norm_rope(x["q"], x["k"], x["cos"], x["sin"], x["pos"], q_weight=x["qw"], k_weight=x["kw"],
+                                   cache=cache, v=x["v"], slots=slots)
+            assert q.shape == (T, 0, d)
+            assert fp8bs.fp8bs_device_error(clear=True) == want
