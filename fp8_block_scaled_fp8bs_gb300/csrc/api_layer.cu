@@ -108,8 +108,8 @@ extern "C" int fp8bs_rms_norm(const fp8bs_rms_norm_args* args, void* stream) {
     if (!a.x || !a.weight || !a.residual != !a.residual_out || !a.y != !a.s || (!a.norm_out && !a.y))
         return FP8BS_ERR_INVALID_ARG;
     // in place: rows over themselves alone
-    if (a.residual && ((a.residual_out == a.x && a.x_stride != a.D) ||
-                       (a.residual_out == a.residual && a.residual_stride != a.D)))
+    if (a.residual && a.T > 1 && ((a.residual_out == a.x && a.x_stride != a.D) ||
+                                  (a.residual_out == a.residual && a.residual_stride != a.D)))
         return FP8BS_ERR_INVALID_ARG;
     if (!aligned16(a.x) || !aligned16(a.residual) || !aligned16(a.weight) || !aligned16(a.residual_out) ||
         !aligned16(a.norm_out) || !aligned16(a.y) || !aligned4(a.s))

@@ -489,7 +489,7 @@ FP8BS_API int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args, 
  *   x, residual: bf16 [T, D], rows contiguous, strides multiples of 8; residual may be NULL.
  *   weight: bf16 [D].
  *   residual_out: bf16 [T, D] contiguous, h; NULL without a residual, else required. It may be x or the residual
- *       itself (the same pointer, and D its stride).
+ *       itself (the same pointer, and D its stride where there is more than one row).
  *   norm_out: bf16 [T, D] contiguous, n rounded once, or NULL.
  *   y: e4m3 [T, D] contiguous, s: fp32 [T, D/128]; both or neither. One of norm_out and y at least.
  *   D: a multiple of 128 up to 16384. All pointers 16-byte aligned, s 4-byte.

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_fp8_layer_gpu import SHAPES, empty_cache, fp8_case, fp8_check, write_inputs
-from test_layer_gpu import attention_check, gen, no_device_error, paged_case  # noqa: F401
+from test_fp8_layer_gpu import SHAPES, empty_cache, fp8_case, fp8_check, same, write_inputs
+from test_layer_gpu import attention_check, gen, no_device_error, paged_case, rand  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,17 @@ def test_write_without_queries_reports_bad_indices():
                                    cache=cache, v=x["v"], slots=slots)
             assert q.shape == (T, 0, d)
             assert fp8bs.fp8bs_device_error(clear=True) == want
+
+
+# ------------------------------------------------------------------------------------ rows of one token
+
+def test_norm_of_one_row_in_place_whatever_its_stride():
+    g = gen(77)
+    D = 640
+    wide, w = rand(g, 4, D + 264), rand(g, D)
+    for i in range(2):
+        x, r = wide[:1, 8:8 + D], rand(g, 3, 2 * D)[:1, :D]
+        ref = fp8bs.rms_norm(x.clone(), w, residual=r.clone(), quant="fp32", norm=True)
+        out = (x, r)[i]
+        got = fp8bs.rms_norm(x, w, residual=r, quant="fp32", norm=True, residual_out=out)
+        assert got.h.data_ptr() == out.data_ptr() and all(same(a, b) for a, b in zip(got, ref))
