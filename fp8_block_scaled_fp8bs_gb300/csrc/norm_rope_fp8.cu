@@ -29,33 +29,32 @@ constexpr int CHUNK = 512;           // tokens from which on a call is taken for
 // A run, in shared memory.
 struct Run {
     int64_t page, off;       // page, slot of its first token there
-    int first, n;            // that token in the window, tokens
     float by[2], ratio[2];   // of keys and values: 1 / the new scale; old / new scale where codes are to be rounded again
 };
 
-// A token's slot. known: its position and slot are not out of range (a negative slot is none); ok: a page's slot is given
-// to it.
+// A token's slot, and where it stands in its page. known: position and slot are not out of range (a negative slot is none);
+// ok: a page's slot is given to it.
 struct TokenSlot {
-    int64_t slot;
+    int64_t slot, off;
     bool known, ok;
 };
 
 __device__ __forceinline__ TokenSlot token_slot(const fp8bs_qk_norm_rope_args& a, int64_t t) {
-    TokenSlot s = {-1, true, false};
+    TokenSlot s = {-1, 0, true, false};
     if (t >= 0 && t < a.T) {
         s.slot = a.slots[t];
         const int pos = a.positions[t];
         s.known = pos >= 0 && pos < a.max_positions && s.slot < a.cache.pages * a.cache.page_size;
         s.ok = s.known && s.slot >= 0;
+        const int64_t size = a.cache.page_size;
+        if (s.ok) s.off = (size & (size - 1)) == 0 ? s.slot & (size - 1) : s.slot % size;
     }
     return s;
 }
 
-// Whether token t continues the run of the token before it: the next slot of the same page.
-__device__ __forceinline__ bool continues(const fp8bs_qk_norm_rope_args& a, const TokenSlot& before, const TokenSlot& s) {
-    if (!before.ok || !s.ok || s.slot != before.slot + 1) return false;
-    const int64_t size = a.cache.page_size;
-    return ((size & (size - 1)) == 0 ? s.slot & (size - 1) : s.slot % size) != 0;
+// Whether a token continues the run of the one before it: a later slot of the same page.
+__device__ __forceinline__ bool continues(const TokenSlot& before, const TokenSlot& s) {
+    return before.ok && s.ok && before.slot < s.slot && before.slot >= s.slot - s.off;
 }
 
 // Codes of 16 values, by a scale's reciprocal (a power of two: the products are exact but for subnormals of binary32,
@@ -99,6 +98,7 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
     __shared__ Run s_run[MAX_WINDOW];
     __shared__ unsigned s_max[2][MAX_WINDOW];                // bits of numbers >= 0, which are in their order
     __shared__ int s_got[WARPS];
+    __shared__ int s_off[THREADS];                           // slots in their pages, of the tokens that are looked at first
     __shared__ float4 s_keys[KEEP][4][THREADS];              // a thread's own
     const int tid = threadIdx.x;
     const int p = tid % LPR;
@@ -193,13 +193,15 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
     const int head = static_cast<int>(blockIdx.x % static_cast<unsigned>(hk));
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(hk)) * window;
     // One token a thread, those of the window and of a page behind it, where its last run ends if not before.
-    TokenSlot mine = {-1, true, false};
+    TokenSlot mine = {-1, 0, true, false};
     bool more = false;
     if (32 * warp < window + a.cache.page_size) {
         mine = token_slot(a, t0 + tid);
-        TokenSlot before = {__shfl_up_sync(0xffffffffu, mine.slot, 1), true, __shfl_up_sync(0xffffffffu, mine.ok, 1) != 0};
+        TokenSlot before = {__shfl_up_sync(0xffffffffu, mine.slot, 1), 0, true,
+                            __shfl_up_sync(0xffffffffu, mine.ok, 1) != 0};
         if (lane == 0) before = token_slot(a, t0 + tid - 1);
-        more = continues(a, before, mine);
+        more = continues(before, mine);
+        s_off[tid] = static_cast<int>(mine.off);
     }
     const bool starts = tid < window && mine.ok && !more;
     // (where there are queries, theirs report it)
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
     };
     int end = window + continuing(window);                   // behind the last row
     while (end >= THREADS) {                                 // (longer than what has been looked at)
-        const bool on = continues(a, token_slot(a, t0 + end + tid - 1), token_slot(a, t0 + end + tid));
+        const bool on = continues(token_slot(a, t0 + end + tid - 1), token_slot(a, t0 + end + tid));
         const unsigned stop = ~__ballot_sync(0xffffffffu, on);
         __syncthreads();
         if (lane == 0) s_got[warp] = stop ? __ffs(stop) - 1 : 32;
@@ -257,10 +259,7 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
         run_mine = run_of(tid);
         Run& r = s_run[run_mine];
         r.page = mine.slot / a.cache.page_size;
-        r.off = mine.slot - r.page * a.cache.page_size;
-        r.first = tid;
-        const int n = 1 + continuing(tid + 1);
-        r.n = tid + n >= window ? end - tid : n;
+        r.off = mine.off;
         s_max[0][run_mine] = s_max[1][run_mine] = 0u;
         old_k = k_scale[r.page * hk + head], old_v = v_scale[r.page * hk + head];
     }
@@ -358,6 +357,7 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
         flush(run, most, s_max[0]);
     }
     __syncthreads();
+    bool grows = false;
     if (starts) {
         Run& r = s_run[run_mine];
         const float sk = grown_scale(old_k, page_scale(__uint_as_float(s_max[0][run_mine])), r.off);
@@ -368,8 +368,42 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
         // (0: the codes that the page holds stay as they are)
         r.ratio[0] = r.off > 0 && old_k > 0.0f && old_k < sk ? old_k / sk : 0.0f;
         r.ratio[1] = r.off > 0 && old_v > 0.0f && old_v < sv ? old_v / sv : 0.0f;
+        grows = r.ratio[0] != 0.0f || r.ratio[1] != 0.0f;
     }
-    __syncthreads();
+    if (__syncthreads_or(grows)) {
+        // Codes that pages hold already, by scales that have grown, before the runs' own: a warp takes a quarter of a page's
+        // keys or values.
+#pragma unroll 1
+        for (int job = warp; job < 8 * runs; job += WARPS) {
+            const Run& r = s_run[job >> 3];
+            const int of = job >> 2 & 1;
+            const float ratio = r.ratio[of];
+            if (ratio == 0.0f) continue;
+            uint8_t* codes = of == 0 ? static_cast<uint8_t*>(a.cache.k) + r.page * a.cache.k_page_stride + head * a.cache.k_head_stride
+                                     : static_cast<uint8_t*>(a.cache.v) + r.page * a.cache.v_page_stride + head * a.cache.v_head_stride;
+            const int64_t stride = of == 0 ? a.cache.k_slot_stride : a.cache.v_slot_stride;
+            const int pieces = (of == 0 ? dk : dv) / 16;
+            const int piece = lane % pieces, at_once = 32 / pieces;      // (d <= 256: 16 pieces at most)
+            if (lane >= at_once * pieces) continue;
+            const int64_t q0 = a.cache.page_size * (job & 3) / 4, q1 = a.cache.page_size * ((job & 3) + 1) / 4;
+            for (int64_t o0 = q0 + lane / pieces; o0 < q1; o0 += 4 * at_once) {
+                uint4* to[4];
+                uint4 c[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t o = o0 + i * at_once;
+                    to[i] = o < q1 ? reinterpret_cast<uint4*>(codes + o * stride) + piece : nullptr;
+                    if (o < q1) c[i] = *to[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (to[i])
+                        *to[i] = make_uint4(rescaled(c[i].x, ratio), rescaled(c[i].y, ratio), rescaled(c[i].z, ratio),
+                                            rescaled(c[i].w, ratio));
+            }
+        }
+        __syncthreads();
+    }
 #pragma unroll 1
     for (int i = 0; i < rounds; ++i) {
         const int e = row_of(i);
@@ -386,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
         }
         if (e < 0) continue;
         const Run& r = s_run[run_of(e)];
-        const int64_t slot = r.off + (e - r.first);
+        const int64_t slot = e < THREADS ? s_off[e] : a.slots[t0 + e] - r.page * a.cache.page_size;
         if (rows.has) {
             uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.cache.k) + r.page * a.cache.k_page_stride +
                                                   slot * a.cache.k_slot_stride + head * a.cache.k_head_stride);
@@ -399,37 +433,6 @@ __global__ void __launch_bounds__(THREADS, 5) qk_norm_rope_fp8_kernel(
             reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.cache.v) + r.page * a.cache.v_page_stride +
                                      slot * a.cache.v_slot_stride + head * a.cache.v_head_stride)[p] =
                 make_uint4(lo.x, lo.y, hi.x, hi.y);
-        }
-    }
-    // Codes that pages hold already, by scales that have grown: a warp takes a quarter of a page's keys or values.
-#pragma unroll 1
-    for (int job = warp; job < 8 * runs; job += WARPS) {
-        const Run& r = s_run[job >> 3];
-        const int of = job >> 2 & 1;
-        const float ratio = r.ratio[of];
-        if (ratio == 0.0f) continue;
-        uint8_t* codes = of == 0 ? static_cast<uint8_t*>(a.cache.k) + r.page * a.cache.k_page_stride + head * a.cache.k_head_stride
-                                 : static_cast<uint8_t*>(a.cache.v) + r.page * a.cache.v_page_stride + head * a.cache.v_head_stride;
-        const int64_t stride = of == 0 ? a.cache.k_slot_stride : a.cache.v_slot_stride;
-        const int pieces = (of == 0 ? dk : dv) / 16;
-        const int piece = lane % pieces, at_once = 32 / pieces;      // (d <= 256: 16 pieces at most)
-        if (lane >= at_once * pieces) continue;
-        const int64_t q0 = a.cache.page_size * (job & 3) / 4, q1 = a.cache.page_size * ((job & 3) + 1) / 4;
-        for (int64_t o0 = q0 + lane / pieces; o0 < q1; o0 += 4 * at_once) {
-            uint4* to[4];
-            uint4 c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t o = o0 + i * at_once;
-                const bool other = o < q1 && (o < r.off || o >= r.off + r.n);
-                to[i] = other ? reinterpret_cast<uint4*>(codes + o * stride) + piece : nullptr;
-                if (other) c[i] = *to[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (to[i])
-                    *to[i] = make_uint4(rescaled(c[i].x, ratio), rescaled(c[i].y, ratio), rescaled(c[i].z, ratio),
-                                        rescaled(c[i].w, ratio));
         }
     }
 }

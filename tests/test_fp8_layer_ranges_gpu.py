@@ -2,13 +2,14 @@
 memory of any content, scores and scales of any size, slots with gaps, calls without queries. Tolerances are derived beside
 each comparison."""
 import math
+import random
 
 import pytest
 import torch
 
 import fp8_block_scaled_fp8bs_gb300 as fp8bs
-from test_fp8_layer_gpu import SHAPES, empty_cache, fp8_case, fp8_check, same, write_inputs
-from test_layer_gpu import attention_check, gen, no_device_error, paged_case, rand  # noqa: F401
+from test_fp8_layer_gpu import SHAPES, copy, empty_cache, fp8_case, fp8_check, power_above, same, write_inputs
+from test_layer_gpu import attention_check, gen, no_device_error, norm_rope_ref, paged_case, rand  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -191,3 +192,58 @@ def test_norm_of_one_row_in_place_whatever_its_stride():
         out = (x, r)[i]
         got = fp8bs.rms_norm(x, w, residual=r, quant="fp32", norm=True, residual_out=out)
         assert got.h.data_ptr() == out.data_ptr() and all(same(a, b) for a, b in zip(got, ref))
+
+
+# ------------------------------------------------------------------------------------- slots with gaps
+
+def gaps_check(cache, x, runs):
+    """A write of one run a page, runs[page] = its rising slots of the page, against the definition."""
+    page, hk = cache.k.shape[1:3]
+    before = copy(cache)
+    slots = torch.tensor([pg * page + o for pg, at in runs.items() for o in at], device="cuda")
+    fp8bs.qk_norm_rope(x["q"], x["k"], x["cos"], x["sin"], x["pos"], q_weight=x["qw"], k_weight=x["kw"], cache=cache,
+                       v=x["v"], slots=slots)
+    rk = norm_rope_ref(x["k"], x["kw"], x["cos"], x["sin"], x["pos"], 0, False, 1e-6)
+    t = 0
+    for pg, at in runs.items():
+        rows = torch.arange(t, t + len(at), device="cuda")
+        t += len(at)
+        for name, want, exact in (("k", rk[rows], False), ("v", x["v"][rows].double(), True)):
+            codes, scale = getattr(cache, name)[pg], getattr(cache, name + "_scale")[pg].double()
+            old, kept = getattr(before, name)[pg], getattr(before, name + "_scale")[pg].double()
+            if at[0] == 0:
+                kept = torch.zeros_like(kept)
+            # (binary32: where the largest is within 2^-17 of a border, the power of two beside it)
+            need = want.abs().amax((0, 2)).clamp(min=1e-4) / 448
+            low = torch.maximum(kept, power_above(need * (1 - 2.0 ** -17)))
+            assert bool(((scale == low) | (scale == torch.maximum(kept, power_above(need * (1 + 2.0 ** -17))))).all())
+            if exact:
+                assert same(codes[at], (want / scale[:, None]).float().to(E4M3))
+            else:
+                # half a step, and the binary32 terms of norm and rotation, as large as the row's largest channel
+                err = (codes[at].double() * scale[:, None] - want).abs()
+                step = torch.maximum(2.0 ** -4 * want.abs(), scale[:, None] * 2.0 ** -10) * (1 + 2.0 ** -10)
+                assert bool((err <= step + 2.0 ** -16 * want.abs().amax(-1, keepdim=True)).all())
+            rest = [o for o in range(page) if o not in set(at)]
+            ratio = torch.where((kept > 0) & (scale > kept), kept / scale, torch.ones_like(scale)).float()
+            assert torch.equal(codes[rest].float(), (old[rest].float() * ratio[:, None]).to(E4M3).float())
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 512])
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 128), (192, 64)])
+def test_runs_with_gaps(page, d, rot):
+    # runs of some slots of each page, first from slot 0, then between what is there, with larger values; short runs among
+    # many pages, runs of hundreds of tokens, more than a block looks at
+    rng, hk, pages = random.Random(page + d), 3, 9
+    cache = empty_cache(pages, page, hk, d, d)
+    for c in (cache.k, cache.v):
+        c.view(torch.uint8)[:] = 0x30
+    for turn, scale in enumerate((0.1, 0.1, 40.0, 1.0, 3000.0)):
+        runs = {}
+        for pg in rng.sample(range(pages), 7):
+            at = sorted(rng.sample(range(page), rng.choice([1, 2, page // 3, page - 3])))
+            runs[pg] = [0] + [o for o in at if o > 1] if turn == 0 else [o for o in at if o > 0] or [1]
+        T = sum(map(len, runs.values()))
+        x = write_inputs(80 + turn, T, 4, hk, d, d, rot, True, scale=scale)
+        x["kw"] = (x["kw"].float() * scale).bfloat16()
+        gaps_check(cache, x, runs)
