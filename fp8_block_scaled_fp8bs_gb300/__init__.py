@@ -543,7 +543,8 @@ class PagedCacheFp8(NamedTuple):
     """The same in 8 bits: e4m3 codes k [pages, page_size, heads, dk] and v [pages, page_size, heads, dv]
     (page_size and the strides multiples of 16), each page and head with one scale, fp32 [pages, heads]:
     a code stands for code * scale. The scales are powers of two that qk_norm_rope writes and lets grow
-    with the page; zeros say that a page holds nothing yet."""
+    with the page; zeros say that a page holds nothing yet. paged_attention takes value scales of 2^-80 to
+    2^120, within 2^80 of one another among a query's keys."""
     k: Any
     v: Any
     k_scale: Any

@@ -3,15 +3,17 @@
 //
 // The codes go from HBM to the tensor core as they are: nothing is widened on the way. With 128 keys per tile as the
 // MMA's M side and the R query rows of a work item (token i, head g of the group: row i*G + g) on its N side,
-//   S^T = K Q^T    e4m3 x e4m3: each row of Q as the sum of two e4m3 numbers per channel (columns r and R + r), exact
-//                  but for channels 2^-17 below the row's largest; K as the cache holds it, S^T fp32 in TMEM
+//   S^T = K Q^T    e4m3 x e4m3: each row of Q as the sum of two e4m3 numbers per channel (columns r and R + r) in a unit
+//                  that leaves its largest in [224, 448): exact for channels of 0.25 units and more (2^-9 of the
+//                  largest), else off by 2^-10 units at most; K as the cache holds it, S^T fp32 in TMEM
 //   P = exp2(c ks S + log2 vs - m), one thread per key, m the row's running maximum of that: probability and
 //                  value scale in one, so that pages whose values differ in size share a tile
 //   O^T = V^T P    e4m3 x e4m3: P as p + p'/32, two e4m3 numbers again (2^-8 of it, and 2^-23 of the row's largest);
 //                  V as the cache holds it (keys outermost: an MN-major operand), one fp32 tile in TMEM per key tile,
 //                  which the threads (one per channel) add to their sums in registers
 // The sum of a row is taken from P in binary32 before its rounding, each term divided by its value's scale (a power of
-// two), so lse is exact to binary32. Two or three groups of four warps take steps of one or two key tiles in turn, one's
+// two): lse is as good as binary32 holds the exponentials, as long as a term does not vanish under the value scale of
+// another page 2^80 times as large, and 2^8 over the smallest scale is a number (the range that the header states). Two or three groups of four warps take steps of one or two key tiles in turn, one's
 // softmax under the others' products; the query warp puts their sums of an item together, in a fixed order.
 // A row without keys is one whose sum is zero. A score that is not a number, or +infinite, makes the sum NaN.
 //
@@ -117,7 +119,7 @@ __device__ __forceinline__ bool thread_test(uint64_t* bar, uint32_t parity) {
 
 constexpr uint32_t kIdescBothMN = 1u << 15 | 1u << 16;       // A and B MN-major
 
-// The same for probabilities (times 256 at most), what is left 32 times. By way of binary16, whose 11 bits hold a
+// Probabilities (up to 256) as two codes, what the first leaves 32 times. By way of binary16, whose 11 bits hold a
 // probability to 2^-12 of it and the difference from its code exactly.
 __device__ __forceinline__ void two_codes_p(float x, float y, uint32_t* hi, uint32_t* lo) {
     const __half2 e = __floats2half2_rn(x, y);

@@ -469,9 +469,16 @@ FP8BS_API int fp8bs_qk_norm_rope_fp8(const fp8bs_qk_norm_rope_args* args, float*
 
 /*
  * fp8bs_paged_attention_fp8 -- fp8bs_paged_attention over a cache in 8 bits (args->cache holds the codes), its keys
- * and values taken as code * scale. Scores, softmax sums and o are held in binary32. A query that is not finite gets
- * NaN. The scales of the pages that hold keys have to be positive powers of two. Everything else, the workspace too
- * (its size from fp8bs_paged_attention_fp8_workspace_size), is as in fp8bs_paged_attention.
+ * and values taken as code * scale. Scores, softmax sums and o are held in binary32; what the products take is rounded:
+ *
+ *   queries         to the sum of two e4m3 numbers a channel, in a unit in which the row's largest channel is 224 to 448
+ *                   (the unit is 2^-125 at least): exact from 2^-9 of that channel on, else off by 2^-17 of it at most
+ *   probabilities   times their value's scale, to 2^-8 of themselves or better, and to 2^-23 of the row's largest
+ *
+ * A query that is not finite gets NaN. The scales of the pages that hold keys have to be positive powers of two. The value
+ * scales that a query's keys have lie in 2^-80 .. 2^120 and within 2^80 of one another, else the sum that the
+ * probabilities are divided by may be lost (the write's own do where no value is larger than 2^66). Everything else, the
+ * workspace too (its size from fp8bs_paged_attention_fp8_workspace_size), is as in fp8bs_paged_attention.
  */
 FP8BS_API int fp8bs_paged_attention_fp8_workspace_size(const fp8bs_paged_attention_args* args, size_t* bytes);
 FP8BS_API int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args, const float* k_scale,

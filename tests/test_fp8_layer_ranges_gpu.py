@@ -160,6 +160,16 @@ def test_scale_of_zero_over_large_bf16_keys():
         attention_check(c, news, lens, scale=0.0)
 
 
+@pytest.mark.parametrize("mean,size", [(-33, 1.0), (20, 2.0 ** -8), (73, 2.0 ** -8)])
+def test_value_scales_at_the_ends_of_their_range(mean, size):
+    # scales within 2^80 of one another, from 2^-80 and up to 2^113
+    for news, lens in (([1, 3], [500, 200]), ([1, 130], [500, 200]), ([1], [9000])):
+        c = fp8_case(78, news, lens, 8, 2, 128, 128, 16, poison=False, k_spread=0, v_spread=40)
+        c["cache"].v_scale.mul_(2.0 ** mean)
+        c["cache"].v.copy_((c["cache"].v.float() * size).to(E4M3))
+        fp8_check(c, news, lens, scale=0.01)
+
+
 # ------------------------------------------------------------------------------ writes without queries
 
 def test_write_without_queries_reports_bad_indices():
