@@ -78,9 +78,9 @@ def level_case(codes, news, lens, hq, hk, dk, dv, low, high):
     return case, row
 
 
-def check_level(codes, news, lens, hq, hk, dk, dv, low, high):
+def check_level(codes, news, lens, hq, hk, dk, dv, low, high, window=0):
     c, row = level_case(codes, news, lens, hq, hk, dk, dv, low, high)
-    out, lse = fp8bs.paged_attention(**c, max_q_len=max(news), return_lse=True)
+    out, lse = fp8bs.paged_attention(**c, max_q_len=max(news), window=window, return_lse=True)
     cache, t = c["cache"], 0
     for b, (n, L) in enumerate(zip(news, lens)):
         j = torch.arange(L, device="cuda")
@@ -93,9 +93,15 @@ def check_level(codes, news, lens, hq, hk, dk, dv, low, high):
         q = c["q"][t:t + n].double()
         terms = q * row.double().repeat_interleave(hq // hk, 0)
         s = terms.sum(-1) * dk ** -0.5
-        count = (L - n + 1 + torch.arange(n, device="cuda"))
-        o = v.cumsum(0)[count - 1] / count[:, None, None]
-        mag = v.abs().cumsum(0)[count - 1] / count[:, None, None]
+        last = L - n + 1 + torch.arange(n, device="cuda")
+        first = (last - window).clamp(min=0) if window else torch.zeros_like(last)
+        count = last - first
+
+        def mean(x):
+            sums = torch.cat([torch.zeros_like(x[:1]), x.cumsum(0)])
+            return (sums[last] - sums[first]) / count[:, None, None]
+
+        o, mag = mean(v), mean(v.abs())
         # the probabilities of a row are all the same number: one rounding of it to bf16, or to two e4m3 numbers (2^-8)
         # and one of the output (2^-8); binary32 sums 2^-12
         err = (out[t:t + n].double() - o).abs()
@@ -118,6 +124,53 @@ LEVELS = [([1, 1, 1, 1, 2], [1, 2, 40, 300, 129]), ([1], [20000]), ([130, 1, 3],
 @pytest.mark.parametrize("low,high", [(20, 26), (26, 29), (29, 40)])
 def test_scores_of_any_size_over_codes(dk, dv, news, lens, low, high):
     check_level(True, news, lens, 16, 2, dk, dv, low, high)
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("window", [1, 70, 200])
+def test_scores_of_any_size_in_windows(codes, dk, dv, window):
+    # far rows beside others, tiles that are masked at both ends
+    for news, lens in LEVELS:
+        check_level(codes, news, lens, 16, 2, dk, dv, 18, 36, window)
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("low,high", [(10, 24), (24, 40)])
+def test_one_key_far_above_the_others(codes, dk, dv, low, high):
+    # one key of each sequence, in its middle, is twice the others: it is all that a row of positive scores has, and
+    # nothing to a row of negative ones, before which and after which its scores are alike
+    for news, lens in (([1, 1, 3], [300, 2, 900]), ([1], [9000]), ([200, 1], [700, 40]), ([300], [1000])):
+        c, row = level_case(codes, news, lens, 16, 2, dk, dv, low, high)
+        cache, t = c["cache"], 0
+        keys = cache.k.view(torch.uint8) if codes else cache.k
+        twice = (row.float() * 2).to(E4M3).view(torch.uint8) if codes else (row.float() * 2).bfloat16()
+        for b, L in enumerate(lens):
+            keys[int(c["page_table"][b, L // 2 // 16]), L // 2 % 16] = twice
+        out, lse = fp8bs.paged_attention(**c, max_q_len=max(news), return_lse=True)
+        for b, (n, L) in enumerate(zip(news, lens)):
+            j = torch.arange(L, device="cuda")
+            pg = c["page_table"][b].long()[j // 16]
+            if codes:
+                v = cache.v.view(torch.uint8)[pg, j % 16].view(E4M3).double() * cache.v_scale.double()[pg][..., None]
+            else:
+                v = cache.v[pg, j % 16].double()
+            v = v.repeat_interleave(8, 1)
+            star = (j == L // 2).double()
+            seen = (j <= L - n + torch.arange(n, device="cuda")[:, None]).double()
+            low_w, high_w = seen * (1 - star), seen * star
+            has = high_w.sum(1, keepdim=True)
+            w = torch.where(has > 0, high_w, low_w / low_w.sum(1, keepdim=True).clamp(min=1))       # positive rows
+            u = torch.where(low_w.sum(1, keepdim=True) > 0, low_w / low_w.sum(1, keepdim=True).clamp(min=1), high_w)
+            positive = (torch.arange(16, device="cuda") % 2 == 1)[:, None, None]
+            p = torch.where(positive, w, u)                                                          # [heads, n, keys]
+            o, mag = (torch.einsum("hnk,khd->nhd", p, x) for x in (v, v.abs()))
+            # scores are 2^10 and more apart, so that nothing is left to the other keys; one rounding of the probabilities,
+            # one of the output, binary32 sums
+            err = (out[t:t + n].double() - o).abs()
+            assert bool((err <= (2.0 ** -7 + 2.0 ** -12) * mag).all()), float((err / mag).nan_to_num(math.inf).max())
+            t += n
 
 
 @pytest.mark.parametrize("dk,dv", SHAPES)
