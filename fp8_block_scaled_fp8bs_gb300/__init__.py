@@ -600,7 +600,7 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     rot_start .. rot_start+R-1. With a PagedCache, the keys and v bf16 [T, Hk, Dv] go to its slots
     int64 [T] (negative: not written) and q bf16 [T, Hq, D] is returned; without, (q, k). With a
     PagedCacheFp8 they are held as codes; the tokens that go to one page stand next to one another, in
-    rising slots, and a token in a page's slot 0 begins it anew."""
+    rising slots (with gaps or without), and a token in a page's slot 0 begins it anew."""
     return (_host or _load_host()).qk_norm_rope(q, k, cos, sin, positions, q_weight, k_weight, eps, rot_start,
                                                 interleaved, cache, v, slots, out)
 

@@ -65,7 +65,7 @@ int qk_norm_rope(const fp8bs_qk_norm_rope_args& args, bool fp8, float* k_scale, 
         return FP8BS_ERR_INVALID_ARG;
     const int rc = fp8 ? check_cache_fp8(a.cache) : check_cache(a.cache, a.v != nullptr);
     if (rc == FP8BS_ERR_INVALID_ARG) return rc;
-    // (a block per token, and one per head and token that may begin a page)
+    // (blocks: one per token of queries, and of keys and values one per head and window of tokens, of one token at least)
     if (fp8 && a.T * (a.cache.heads + 1) >= kMaxDim) return FP8BS_ERR_INVALID_ARG;
     if (a.T == 0) return FP8BS_OK;
     if (fp8 && (!a.v || !a.slots || !k_scale || !v_scale)) return FP8BS_ERR_INVALID_ARG;

@@ -13,9 +13,10 @@
 //                  which the threads (one per channel) add to their sums in registers
 // The sum of a row is taken from P in binary32 before its rounding, each term divided by its value's scale (a power of
 // two): lse is as good as binary32 holds the exponentials, as long as a term does not vanish under the value scale of
-// another page 2^80 times as large, and 2^8 over the smallest scale is a number (the range that the header states). Two or three groups of four warps take steps of one or two key tiles in turn, one's
-// softmax under the others' products; the query warp puts their sums of an item together, in a fixed order.
-// A row without keys is one whose sum is zero. A score that is not a number, or +infinite, makes the sum NaN.
+// another page 2^80 times as large, and 2^8 over the smallest scale is a number (the range that the header states). Two
+// or three groups of four warps take steps of one or two key tiles in turn, one's softmax under the others' products;
+// the query warp puts their sums of an item together, in a fixed order. A row without keys is one whose sum is zero. A
+// score that is not a number, or +infinite, makes the sum NaN.
 //
 // The work is cut into equal chunks of key tiles for each key head (RowsPlan), whatever the sequences' lengths: a chunk
 // is the end of one sequence, some whole ones and the beginning of another. Parts of a sequence are joined in key order

@@ -1,10 +1,11 @@
 // attention_fp8_tiles.cu -- attention over a paged cache of e4m3 codes for sequences of many query rows: the kernel of
 // attention.cu, its keys taken as codes and its values widened on the way (attention_tiles.cuh).
 //
-// Measured: a chunk of 4096 tokens over 8192 keys, 32 / 8 heads of 128, 318 us (0.66 of the products' floor in bf16; a bf16
-// cache 282): the tensor pipe is at 55 % and a key tile's chain (softmax 1900 cycles of 3700, then P V and the next S) is
-// what lasts. Tried for it and slower: the next S under the softmax, P in columns of its own (409 us), the
-// softmax in two steps, each with its own product (359; issued as they come 445), 64-key tiles with two S (382).
+// Measured, on inputs that change from call to call: a chunk of 4096 tokens over 8192 keys, 32 / 8 heads of 128, 318 to
+// 320 us (0.66 of the products' floor in bf16; a bf16 cache 298): the tensor pipe is at 55 % and a key tile's chain
+// (softmax 1750 cycles of 3700 and 180 to store P, then P V and the next S) is what lasts. Tried for it and slower: the
+// next S under the softmax, P in columns of its own (409 us), the softmax in two steps, each with its own product (359;
+// issued as they come 445), 64-key tiles with two S (382).
 #include "attention_tiles.cuh"
 
 namespace fp8bs {

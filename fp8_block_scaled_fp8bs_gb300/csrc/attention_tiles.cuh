@@ -9,10 +9,11 @@ namespace {
 
 constexpr float kRescale = 8.0f;
 
-// Where a row's maximum is this large, in log2 units, binary32 holds the terms of the fused product that makes exponents of
-// scores to 8 and more (a bf16 cache: 128), by which a probability would be out of the range of binary16 (bf16): a function
-// of its own takes the scores relative to the maximum first (far_tiles; the chunk of 4096 over codes 318 us, 316 without it,
-// 326 to 366 with the same in the loop of all rows; 192-wide heads over bf16 57.4, 56.6 without). Asked where a maximum grows.
+// Where a row's maximum is this large, in log2 units, binary32 holds the terms of the fused product that makes exponents
+// of scores to 8 and more (a bf16 cache: 128), by which a probability would be out of the range of binary16 (bf16): a
+// function of its own takes the scores relative to the maximum first (far_tiles; the chunk of 4096 over codes 318 us,
+// 316 without it, 326 to 366 with the same in the loop of all rows; 192-wide heads over bf16 57.4, 56.6 without). Asked
+// where a maximum grows.
 template <bool CODES>
 constexpr float kFar = CODES ? 67108864.0f : 1073741824.0f;
 
@@ -457,9 +458,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const int r = q * 128 + quarter * 32 + lane;          // row of the item's tile
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t o_tmem = tmem + lanes + Cfg::SBUF * BN + q * DV;
-        // (a scale of zero: the smallest factor keeps -inf apart from the finite scores; one that is NaN stays so. Codes: their
-        // factor is only bounded where the key's scale has joined it, as a small one may belong to large keys. The maximum
-        // with zero is none; without it the compiler orders the loop below otherwise, 328 us for the chunk of 4096, not 321.)
+        // (a scale of zero: the smallest factor keeps -inf apart from the finite scores; one that is NaN stays so.
+        // Codes: their factor is only bounded where the key's scale has joined it, as a small one may belong to large
+        // keys. The maximum with zero is none; without it the compiler orders the loop below otherwise, 328 us for the
+        // chunk of 4096, not 321.)
         const float c_all = max_nan(fabsf(a.scale) * 1.4426950408889634f, CODES ? 0.0f : 1e-45f);
         // Queries of query tile q into shared memory (K-major, 128-byte swizzle), valid rows only (what the
         // others hold is of no consequence: rows do not meet). A negative scale turns their signs, so that

@@ -1,19 +1,21 @@
 // norm_rope_fp8.cu -- RMS norm of queries and keys per head, rotation by position and the write of keys and values
 // into a paged cache of e4m3 codes with one power-of-two scale per page and head (fp8bs_qk_norm_rope_fp8).
 //
-// Bound by memory: queries 4 bytes an element, keys and values 3. Two kinds of CTAs in one launch. Queries: whole tokens,
-// as in norm_rope.cu. Keys and values: the runs that begin in a window of tokens (a run: tokens of the call that go to one
-// page, one after another), of one key head, a row to a group of LPR lanes; runs may end behind the window. The largest
-// magnitudes of a run come together in shared memory, from them the page's new scale, by it the codes. No other CTA
-// touches that page and head, and a maximum does not depend on the order of what it is of, so the same call gives the
-// same bits. A page that grows keeps the larger of its scale and what the run asks for; where that is more than before,
-// its codes are rounded again by the ratio, a power of two (exact but for codes that become subnormal).
+// Bound by memory: queries 4 bytes an element, keys and values 3. Two kinds of CTAs in one launch. Queries: whole
+// tokens, as in norm_rope.cu. Keys and values: the runs that begin in a window of tokens (a run: tokens of the call that
+// go to one page, next to one another in rising slots), of one key head, a row to a group of LPR lanes; runs may end
+// behind the window. The largest magnitudes of a run come together in shared memory, from them the page's new scale, by
+// it the codes. No other CTA touches that page and head, and a maximum does not depend on the order of what it is of, so
+// the same call gives the same bits. A page that grows keeps the larger of its scale and what the run asks for; where
+// that is more than before, its codes are rounded again by the ratio, a power of two (exact but for codes that become
+// subnormal).
 //
-// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 channels 45 us for 185 MB (0.61 of a copy's rate; the queries alone
-// 25); 655 tokens of four sequences, 16 heads of 192 and 128, pages of 16 slots 10 us; 61 sequences a token each 5 us, a
-// launch, three loads that wait for one another and two barriers. What a CTA of keys and values waits for (slots, rows,
-// positions and then cosines) bounds it, so it takes four rounds of rows with the next one's on its way: with a CTA per
-// run and its rows read twice, the first case 62 us, the second 22, 200 sequences of 16 heads 18 (now 7).
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128 channels 44 us for 185 MB and 4 of cosines and sines (0.63 of a
+// copy's rate; the queries alone 25); 655 tokens of four sequences, 16 heads of 192 and 128, pages of 16 slots 10 us; 61
+// sequences a token each 5 us, a launch, three loads that wait for one another and two barriers. What a CTA of keys and
+// values waits for (slots, rows, positions and then cosines) bounds it, so it takes four rounds of rows with the next
+// one's on its way: with a CTA per run and its rows read twice, the first case 62 us, the second 22, 200 sequences of 16
+// heads 18 (now 7).
 #include "norm_rows.cuh"
 
 namespace fp8bs {
@@ -57,7 +59,7 @@ __device__ __forceinline__ bool continues(const TokenSlot& before, const TokenSl
     return before.ok && s.ok && before.slot < s.slot && before.slot >= s.slot - s.off;
 }
 
-// Codes of 16 values, by a scale's reciprocal (a power of two: the products are exact but for subnormals of binary32,
+// Codes of 8 values, by a scale's reciprocal (a power of two: the products are exact but for subnormals of binary32,
 // whose codes are zero).
 __device__ __forceinline__ uint2 codes8(const float2* f, float rs) {
     uint32_t w[2];

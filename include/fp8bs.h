@@ -352,7 +352,8 @@ typedef struct {
  *   (a, b) -> (a cos - b sin, a sin + b cos)       for the pairs of channels of
  *                                                  [rot_start, rot_start + rot_dim)
  *
- * in binary32, rounded to bf16 once. Pair i is channels (2i, 2i+1) of that range if `interleaved`,
+ * in binary32 (squares of values of 2^60 and more may leave its range), rounded to bf16 once. Pair i is channels (2i, 2i+1)
+ * of that range if `interleaved`,
  * else (i, i + rot_dim/2); its cosine and sine are cos[p][i], sin[p][i] at p = positions[t].
  *
  *   q [T, q_heads, dk], k [T, cache.heads, dk], v [T, cache.heads, dv]: bf16, rows contiguous and
@@ -452,8 +453,8 @@ FP8BS_API int fp8bs_paged_attention(const fp8bs_paged_attention_args* args, void
  *
  * fp8bs_qk_norm_rope_fp8 -- fp8bs_qk_norm_rope into such a cache (args->cache holds the codes). Keys and values are
  * rounded once, from binary32 (keys) and bf16 (values) to codes. The tokens of the call that go to one page form a run:
- * they stand next to one another in rising slots, and no page gets two runs in one call (its contents are undefined
- * then). For each head, with need = max(amax of the run, 1e-4) / 448 rounded up to a power of two:
+ * they stand next to one another in rising slots (which may leave some out), and no page gets two runs in one call (its
+ * contents are undefined then). For each head, with need = max(amax of the run, 1e-4) / 448 rounded up to a power of two:
  *
  *   run from the page's slot 0     scale = need                      (the page begins anew)
  *   run from a later slot          scale = max(scale, need)          and, where that is larger than it was, every other
@@ -478,7 +479,8 @@ FP8BS_API int fp8bs_qk_norm_rope_fp8(const fp8bs_qk_norm_rope_args* args, float*
  * A query that is not finite gets NaN. The scales of the pages that hold keys have to be positive powers of two. The value
  * scales that a query's keys have lie in 2^-80 .. 2^120 and within 2^80 of one another, else the sum that the
  * probabilities are divided by may be lost (the write's own do where no value is larger than 2^66). Everything else, the
- * workspace too (its size from fp8bs_paged_attention_fp8_workspace_size), is as in fp8bs_paged_attention.
+ * workspace too (its size from fp8bs_paged_attention_fp8_workspace_size, up to 2^26 bytes more), is as in
+ * fp8bs_paged_attention.
  */
 FP8BS_API int fp8bs_paged_attention_fp8_workspace_size(const fp8bs_paged_attention_args* args, size_t* bytes);
 FP8BS_API int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args, const float* k_scale,
@@ -492,6 +494,7 @@ FP8BS_API int fp8bs_paged_attention_fp8(const fp8bs_paged_attention_args* args, 
  *   y = e4m3(n / s), s as in fp8bs_act_quant (per 1 x 128 block, scale_fmt), of n in binary32
  *
  * n is not rounded on its way to y: where norm_out is asked for too, y may differ from fp8bs_act_quant's codes of it.
+ * Squares are summed in binary32: values of 2^57 and more may leave its range.
  *
  *   x, residual: bf16 [T, D], rows contiguous, strides multiples of 8; residual may be NULL.
  *   weight: bf16 [D].
